@@ -30,6 +30,12 @@ MOE_QUANT_NONE = 0
 MOE_QUANT_FP8_E4M3_DYN = 1
 MOE_QUANT_INT8_DYN = 2
 
+MOE_MX_E2M1 = 1  # 4-bit codes, blocks of 32 with an E8M0 scale
+MOE_MX_E4M3 = 2  # 8-bit codes
+
+MOE_MX_PLAIN = 0
+MOE_MX_GATED = 1
+
 MOE_LAYOUT_AUTO = 0
 MOE_LAYOUT_MULTI = 1
 MOE_LAYOUT_SINGLE = 2
@@ -42,6 +48,8 @@ EXPORTED = (
     "moe_unpack", "moe_unpack_padded", "moe_dedup_window_bytes", "moe_rank_rows", "moe_dispatch_dedup",
     "moe_expand_dedup", "moe_status_string", "moe_plan_layout", "moe_plan_dispatch_ws",
     "moe_plan_layout_dispatch", "moe_plan_combine", "moe_plan_layout_ws", "moe_plan_dispatch_planned", "moe_plan_run",
+    "moe_combine_backward", "moe_combine_backward_mx", "moe_dispatch_backward", "moe_combine_checkpoint",
+    "moe_mx_row_bytes", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_product",
 )
 
 # include/moe_probe.h: bandwidth probes for the measurement, not part of the path
@@ -98,6 +106,14 @@ def _load():
                                      [P, I32, I32, I32, P, I64, I32]),
         "moe_plan_combine": (ctypes.c_int, [P, P, I64, I64, P, P, I32, I32, I32, P]),
         "moe_plan_run": (ctypes.c_int, [P, P]),
+        "moe_combine_backward": (ctypes.c_int, [P, P, I64, I64, P, P, I32, I32, I32, P, I64, P, P]),
+        "moe_combine_backward_mx": (ctypes.c_int, [P, P, P, I64, P, P, I32, I32, I32, P, I64, P, P]),
+        "moe_dispatch_backward": (ctypes.c_int, [P, I64, I64, P, I32, I32, I32, P, P]),
+        "moe_combine_checkpoint": (ctypes.c_int, [P, I64, I64, P, P, I32, I32, I32, P, P, P, P]),
+        "moe_mx_row_bytes": (I64, [I32, I32]),
+        "moe_mx_quantize": (ctypes.c_int, [P, I64, P, I64, I32, I32, P, P, P]),
+        "moe_mx_dequantize": (ctypes.c_int, [P, P, P, I64, I32, I32, P, I64, P]),
+        "moe_mx_product": (ctypes.c_int, [P, P, I64, P, I32, P, P, I32, I32, I32, P, I64, P]),
         "moe_probe_fill": (ctypes.c_int, [P, I64, P]),
         "moe_probe_read": (ctypes.c_int, [P, I64, P, P]),
         "moe_probe_copy": (ctypes.c_int, [P, P, I64, P]),
@@ -831,3 +847,245 @@ __all__ = [
     "plan_layout_ws", "plan_dispatch_planned",
     "MOE_PLAN_BYTES",
 ]
+
+
+# ---------------------------------------------------------------- gradients and MX rows
+
+
+class MxRows(NamedTuple):
+    """Rows in microscaled blocks: codes uint8 [..., R, moe_mx_row_bytes(H, format)] and scales uint8
+    [..., R, H / 32]."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def _launch(dev, stream, fn, *args):
+    """fn(*args, stream handle) with dev as the current device: a null stream is the current device's."""
+    index = dev.index
+    if index is None or index == torch.cuda.current_device():
+        _check(fn(*args, _stream(dev, stream)))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, _stream(dev, stream)))
+
+
+def _out(shape, dtype, dev, stream):
+    """A new output for a call on `stream`, from that stream's memory (the current stream's without one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _rows_arg(t, name, H, dev):
+    """Pointer, row stride in bytes and row count of bf16 rows: a [R, H] tensor whose rows are each
+    contiguous, at any stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != H:
+        raise ValueError(f"{name} must be bfloat16 [rows, {H}], got {t.dtype} {tuple(t.shape)}")
+    if t.shape[0] == 0:
+        raise ValueError(f"{name} has no rows")
+    if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < H):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return _ptr(t), (2 * t.stride(0) if t.shape[0] > 1 else 2 * H), t.shape[0]
+
+
+def _table_args(slot_idx, topk_weights=None):
+    _need(slot_idx, "slot_idx", torch.int32, 2)
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, 2, slot_idx.device)
+        if topk_weights.shape != slot_idx.shape:
+            raise ValueError("topk_weights must match slot_idx")
+    return slot_idx.shape[0], slot_idx.shape[1], slot_idx.device
+
+
+def _mx_args(mx, name, rows, H, format, dev):
+    codes, scales = mx
+    _need(codes, f"{name} codes", torch.uint8, device=dev)
+    _need(scales, f"{name} scales", torch.uint8, device=dev)
+    want = (rows, moe_mx_row_bytes(H, format)), (rows, H // 32)
+    if (tuple(codes.shape), tuple(scales.shape)) != want:
+        raise ValueError(f"{name} must be codes {want[0]} and scales {want[1]}, got {tuple(codes.shape)} and "
+                         f"{tuple(scales.shape)}")
+    return _ptr(codes), _ptr(scales)
+
+
+def _gradient_outs(S, K, H, rows, d_expert_out, d_topk_weights, dev, stream):
+    if d_expert_out is None:
+        d_expert_out = _out((rows, H), torch.bfloat16, dev, stream)
+    d_ptr, d_stride, d_count = _rows_arg(d_expert_out, "d_expert_out", H, dev)
+    if d_count != rows:
+        raise ValueError(f"d_expert_out must have {rows} rows")
+    if d_topk_weights is None:
+        d_topk_weights = _out((S, K), torch.float32, dev, stream)
+    _need(d_topk_weights, "d_topk_weights", torch.float32, 2, dev)
+    if tuple(d_topk_weights.shape) != (S, K):
+        raise ValueError(f"d_topk_weights must have shape {(S, K)}")
+    return d_expert_out, d_ptr, d_stride, d_topk_weights
+
+
+def moe_combine_backward(dy, expert_out, slot_idx, topk_weights, d_expert_out=None, d_topk_weights=None,
+                         stream=None):
+    """The combine's gradient: (d_expert_out, d_topk_weights) of dy (bf16 [S, H]) with the forward's
+    expert_out (bf16 [R, H], any row stride), slot_idx and topk_weights. Rows of d_expert_out that no
+    entry names keep their contents (undefined where it is allocated here)."""
+    S, K, dev = _table_args(slot_idx, topk_weights)
+    _need(dy, "dy", torch.bfloat16, 2, dev)
+    H = dy.shape[1]
+    if dy.shape[0] != S:
+        raise ValueError("dy must have one row per token of slot_idx")
+    ptr, stride, rows = _rows_arg(expert_out, "expert_out", H, dev)
+    d_expert_out, d_ptr, d_stride, d_topk_weights = _gradient_outs(S, K, H, rows, d_expert_out, d_topk_weights,
+                                                                   dev, stream)
+    _launch(dev, stream, _lib.moe_combine_backward, _ptr(dy), ptr, stride, rows, _ptr(slot_idx),
+            _ptr(topk_weights), S, H, K, d_ptr, d_stride, _ptr(d_topk_weights))
+    return d_expert_out, d_topk_weights
+
+
+def moe_combine_checkpoint(expert_out, slot_idx, topk_weights, y=None, checkpoint=None, stream=None):
+    """moe_combine that also keeps the rows it reads in 8 bits: (y, MxRows in MOE_MX_E4M3 [R, H]). Rows that
+    no entry names keep their contents (undefined where the checkpoint is allocated here)."""
+    S, K, dev = _table_args(slot_idx, topk_weights)
+    if not isinstance(expert_out, torch.Tensor) or expert_out.dim() != 2:
+        raise ValueError("expert_out must be a bfloat16 [rows, H] tensor")
+    H = expert_out.shape[1]
+    ptr, stride, rows = _rows_arg(expert_out, "expert_out", H, dev)
+    if y is None:
+        y = _out((S, H), torch.bfloat16, dev, stream)
+    _need(y, "y", torch.bfloat16, 2, dev)
+    if tuple(y.shape) != (S, H):
+        raise ValueError(f"y must have shape {(S, H)}")
+    if checkpoint is None:
+        checkpoint = _mx_empty(rows, H, MOE_MX_E4M3, dev, stream)
+    codes, scales = _mx_args(checkpoint, "checkpoint", rows, H, MOE_MX_E4M3, dev)
+    _launch(dev, stream, _lib.moe_combine_checkpoint, ptr, stride, rows, _ptr(slot_idx), _ptr(topk_weights), S, H,
+            K, _ptr(y), codes, scales)
+    return y, MxRows(*checkpoint)
+
+
+def moe_combine_backward_mx(dy, checkpoint, slot_idx, topk_weights, d_expert_out=None, d_topk_weights=None,
+                            stream=None):
+    """moe_combine_backward with the rows of a checkpoint (MxRows in MOE_MX_E4M3) in place of expert_out."""
+    S, K, dev = _table_args(slot_idx, topk_weights)
+    _need(dy, "dy", torch.bfloat16, 2, dev)
+    H = dy.shape[1]
+    if dy.shape[0] != S:
+        raise ValueError("dy must have one row per token of slot_idx")
+    rows = checkpoint[0].shape[0]
+    codes, scales = _mx_args(checkpoint, "checkpoint", rows, H, MOE_MX_E4M3, dev)
+    d_expert_out, d_ptr, d_stride, d_topk_weights = _gradient_outs(S, K, H, rows, d_expert_out, d_topk_weights,
+                                                                   dev, stream)
+    _launch(dev, stream, _lib.moe_combine_backward_mx, _ptr(dy), codes, scales, rows, _ptr(slot_idx),
+            _ptr(topk_weights), S, H, K, d_ptr, d_stride, _ptr(d_topk_weights))
+    return d_expert_out, d_topk_weights
+
+
+def moe_dispatch_backward(d_rows, slot_idx, dx=None, stream=None):
+    """The dispatch's gradient: dx[t] = bf16(sum_k d_rows[slot_idx[t, k]]) of d_rows (bf16 [R, H], any row
+    stride), fp32 accumulation."""
+    S, K, dev = _table_args(slot_idx)
+    if not isinstance(d_rows, torch.Tensor) or d_rows.dim() != 2:
+        raise ValueError("d_rows must be a bfloat16 [rows, H] tensor")
+    H = d_rows.shape[1]
+    ptr, stride, rows = _rows_arg(d_rows, "d_rows", H, dev)
+    if dx is None:
+        dx = _out((S, H), torch.bfloat16, dev, stream)
+    _need(dx, "dx", torch.bfloat16, 2, dev)
+    if tuple(dx.shape) != (S, H):
+        raise ValueError(f"dx must have shape {(S, H)}")
+    _launch(dev, stream, _lib.moe_dispatch_backward, ptr, stride, rows, _ptr(slot_idx), S, H, K, _ptr(dx))
+    return dx
+
+
+def moe_mx_row_bytes(H, format):
+    v = _lib.moe_mx_row_bytes(int(H), int(format))
+    if v < 0:
+        _check(int(v))
+    return int(v)
+
+
+def _mx_empty(rows, H, format, dev, stream):
+    return MxRows(_out((rows, moe_mx_row_bytes(H, format)), torch.uint8, dev, stream),
+                  _out((rows, H // 32), torch.uint8, dev, stream))
+
+
+def _count_arg(num_rows, dev):
+    if num_rows is None:
+        return None
+    _need(num_rows, "num_rows", torch.int32, device=dev)
+    if num_rows.numel() < 1:
+        raise ValueError("num_rows must hold a count")
+    return _ptr(num_rows)
+
+
+def moe_mx_quantize(rows, format, num_rows=None, out=None, stream=None):
+    """MxRows of bf16 rows [R, H] (any row stride). num_rows: None, or the device count of rows to take (e.g.
+    layout.expert_slot_base[E:]); the outputs' other rows keep their contents."""
+    if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
+        raise ValueError("rows must be a bfloat16 [rows, H] tensor")
+    dev, H = rows.device, rows.shape[1]
+    _need(rows[:0], "rows", torch.bfloat16, 2)
+    if out is None:
+        out = _mx_empty(rows.shape[0], H, format, dev, stream)
+    codes, scales = _mx_args(out, "out", rows.shape[0], H, format, dev)
+    count = _count_arg(num_rows, dev)
+    if rows.shape[0]:
+        ptr, stride, n = _rows_arg(rows, "rows", H, dev)
+        _launch(dev, stream, _lib.moe_mx_quantize, ptr, stride, count, n, H, int(format), codes, scales)
+    return MxRows(*out)
+
+
+def moe_mx_dequantize(mx, format, num_rows=None, out=None, stream=None):
+    """The values of MxRows [R, ...] as bf16 rows [R, H] (out: any row stride)."""
+    codes, scales = mx
+    _need(scales, "scales", torch.uint8, 2)
+    dev, n, H = scales.device, scales.shape[0], 32 * scales.shape[1]
+    codes_ptr, scales_ptr = _mx_args(mx, "mx", n, H, format, dev)
+    if out is None:
+        out = _out((n, H), torch.bfloat16, dev, stream)
+    count = _count_arg(num_rows, dev)
+    if n:
+        ptr, stride, rows = _rows_arg(out, "out", H, dev)
+        if rows != n:
+            raise ValueError(f"out must have {n} rows")
+        _launch(dev, stream, _lib.moe_mx_dequantize, codes_ptr, scales_ptr, count, n, H, int(format), ptr, stride)
+    return out
+
+
+def moe_mx_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=None):
+    """The experts' product of MX E2M1 rows a (MxRows [R, ...]) with weights w (MxRows [G, O, ...]): row r of
+    group g (group_base int32 [G + 1] on the device, e.g. layout.expert_slot_base) gives bf16 [O], or
+    [O / 2] of silu(gate) * up with MOE_MX_GATED. Rows outside every group keep their contents (undefined
+    where out is allocated here)."""
+    a_codes, a_scales = a
+    w_codes, w_scales = w
+    _need(a_scales, "a scales", torch.uint8, 2)
+    dev, n, H = a_scales.device, a_scales.shape[0], 32 * a_scales.shape[1]
+    ac, asc = _mx_args(a, "a", n, H, MOE_MX_E2M1, dev)
+    _need(w_codes, "w codes", torch.uint8, 3, dev)
+    _need(w_scales, "w scales", torch.uint8, 3, dev)
+    G, O = w_codes.shape[:2]
+    if tuple(w_codes.shape) != (G, O, H // 2) or tuple(w_scales.shape) != (G, O, H // 32):
+        raise ValueError(f"w must be codes {(G, O, H // 2)} and scales {(G, O, H // 32)}")
+    _need(group_base, "group_base", torch.int32, 1, dev)
+    if group_base.shape[0] != G + 1:
+        raise ValueError(f"group_base must hold {G + 1} values")
+    gated = int(epilogue) == MOE_MX_GATED
+    width = O // 2 if gated else O
+    if out is None:
+        out = _out((n, width), torch.bfloat16, dev, stream)
+    if (not isinstance(out, torch.Tensor) or out.dtype != torch.bfloat16 or out.device != dev
+            or tuple(out.shape) != (n, width)):
+        raise ValueError(f"out must be bfloat16 {(n, width)} on {dev}")
+    if width > 1 and out.stride(1) != 1 or n > 1 and out.stride(0) < width:
+        raise ValueError("out must have contiguous rows that do not overlap")
+    if n:
+        _launch(dev, stream, _lib.moe_mx_product, ac, asc, n, _ptr(group_base), G, _ptr(w_codes), _ptr(w_scales), O,
+                H, int(epilogue), _ptr(out), 2 * out.stride(0) if n > 1 else 2 * width)
+    return out

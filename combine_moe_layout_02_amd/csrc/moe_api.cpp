@@ -12,31 +12,12 @@
 #include <cstring>
 #include <type_traits>
 
+#include "abi_checks.h"
 #include "moe_internal.h"
 
 namespace {
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int check_hidden(int32_t H) {
-    if (H < 16 || H > MOE_MAX_HIDDEN) return MOE_ERR_ARG;
-    if (H % 16 != 0) return MOE_ERR_UNSUPPORTED;
-    return MOE_OK;
-}
-
-int check_tokens(int32_t S, int32_t K) {
-    if (S < 1 || K < 1 || K > MOE_MAX_K) return MOE_ERR_ARG;
-    if (S > MOE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
-    return MOE_OK;
-}
-
-int from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-// True when rows [0, rows) at `stride` bytes apart have byte offsets an int64 can hold (rows * stride
-// <= INT64_MAX), so the kernels' row addresses cannot wrap.
-bool extent_fits(int64_t rows, int64_t stride) {
-    return rows <= 1 || stride <= INT64_MAX / rows;
-}
+using namespace moe::checks;
 
 // Which layout form a call takes: -1 for a path value outside moe_layout_path, 1 for the
 // single-launch form, 0 for the multi-launch form. MOE_LAYOUT_SINGLE on a table the single launch
@@ -60,6 +41,8 @@ int check_experts(int32_t E, int32_t P) {
 }  // namespace
 
 namespace moe {
+
+using namespace checks;
 
 int check_dispatch(const void *x, const int32_t *slot_idx, int32_t S, int32_t H, int32_t K,
                    int32_t quant, const void *window, int64_t window_bytes) {

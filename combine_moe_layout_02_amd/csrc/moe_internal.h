@@ -211,4 +211,40 @@ hipError_t launch_unpack(const void *window, const int32_t *num_slots, int32_t S
                          int32_t H, int32_t quant, void *expand_x, float *expand_scales,
                          int32_t *expand_idx, hipStream_t stream);
 
+// Gradients and MX rows (backward.hip, mx_quant.hip, mx_product.hip); arguments as in moe.h, checked by
+// expert_api.cpp.
+hipError_t launch_combine_backward(const void *dy, const void *expert_out, int64_t row_stride_bytes,
+                                   int64_t expert_rows, const int32_t *slot_idx,
+                                   const float *topk_weights, int32_t S, int32_t H, int32_t K,
+                                   void *d_expert_out, int64_t d_row_stride_bytes,
+                                   float *d_topk_weights, hipStream_t stream);
+
+hipError_t launch_combine_backward_mx(const void *dy, const void *codes, const void *scales,
+                                      int64_t expert_rows, const int32_t *slot_idx,
+                                      const float *topk_weights, int32_t S, int32_t H, int32_t K,
+                                      void *d_expert_out, int64_t d_row_stride_bytes,
+                                      float *d_topk_weights, hipStream_t stream);
+
+hipError_t launch_dispatch_backward(const void *d_rows, int64_t row_stride_bytes,
+                                    int64_t expert_rows, const int32_t *slot_idx, int32_t S,
+                                    int32_t H, int32_t K, void *dx, hipStream_t stream);
+
+hipError_t launch_combine_checkpoint(const void *expert_out, int64_t row_stride_bytes,
+                                     int64_t expert_rows, const int32_t *slot_idx,
+                                     const float *topk_weights, int32_t S, int32_t H, int32_t K,
+                                     void *y, void *codes, void *scales, hipStream_t stream);
+
+hipError_t launch_mx_quantize(const void *rows, int64_t row_stride_bytes, const int32_t *num_rows,
+                              int64_t max_rows, int32_t H, int32_t format, void *codes,
+                              void *scales, hipStream_t stream);
+
+hipError_t launch_mx_dequantize(const void *codes, const void *scales, const int32_t *num_rows,
+                                int64_t max_rows, int32_t H, int32_t format, void *rows,
+                                int64_t row_stride_bytes, hipStream_t stream);
+
+hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t a_rows,
+                             const int32_t *group_base, int32_t G, const void *w_codes,
+                             const void *w_scales, int32_t O, int32_t H, int32_t epilogue, void *out,
+                             int64_t out_stride_bytes, hipStream_t stream);
+
 }  // namespace moe

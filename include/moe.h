@@ -35,7 +35,8 @@ typedef enum {
     MOE_ERR_ALIGN = -2,       /* a pointer or stride is not aligned as documented             */
     MOE_ERR_WINDOW = -3,      /* window_bytes < moe_window_bytes(S, K, H), or a staging buffer
                                  shorter than its S*K rows                                    */
-    MOE_ERR_UNSUPPORTED = -4, /* E % P != 0, H % 16 != 0, or S above MOE_MAX_TOKENS           */
+    MOE_ERR_UNSUPPORTED = -4, /* E % P != 0, H % 16 != 0, S above MOE_MAX_TOKENS, H % 32 != 0 for
+                                 MX rows, or an odd O for a gated product                     */
     MOE_ERR_HIP = -5,         /* the HIP runtime reported an error for a launch               */
     MOE_ERR_SCRATCH = -6      /* moe_dispatch_noalloc: the table needs more than its fixed scratch */
 } moe_status;
@@ -504,6 +505,141 @@ int moe_plan_dispatch_planned(moe_plan *plan, const void *x, const int32_t *slot
                               void *window, int64_t window_bytes, void *workspace,
                               int64_t workspace_bytes);
 int moe_plan_run(const moe_plan *plan, hipStream_t stream);
+
+/* ---- Training: the gradients of the combine and of the dispatch ------------------------------------
+ *
+ * The combine y[t] = sum_k w[t, k] * rows[slot_idx[t, k]] and the dispatch rows[slot_idx[t, k]] = x[t] are
+ * linear, so their gradients move the same rows the other way ("Ascend DeepEP MoE Dispatch Optimization",
+ * section "Dispatch handle 六项分别保存什么": the handle of the forward dispatch drives the backward pass). In
+ * all of these calls slot_idx is the table of the forward pass (int32 [S, K], the valid slots distinct, as
+ * moe_layout writes them), entries outside [0, expert_rows) are skipped like pads, S, K and H have the
+ * ranges of moe_combine, and rows * stride must not exceed INT64_MAX. No output may overlap an input or
+ * another output (MOE_ERR_ARG where the buffers' extents do). Results do not depend on timing: no
+ * atomics, a fixed order of every sum.
+ *
+ * moe_combine_backward: for every valid (t, k) with s = slot_idx[t, k]
+ *      d_expert_out[s]    = bf16( fp32(topk_weights[t, k] * fp32(dy[t])) ), one product rounded to fp32, then
+ *                           to nearest even
+ *      d_topk_weights[t, k] = sum over h of fp32(dy[t, h]) * fp32(expert_out[s, h]), accumulated in fp32 (the
+ *                           sum's order is fixed by H alone); 0 for skipped entries.
+ * In:  dy            bf16 [S, H], 16-byte aligned: the gradient of y.
+ *      expert_out    the forward's rows: 16-byte aligned, row_stride_bytes >= 2H and a multiple of 16.
+ * Out: d_expert_out  bf16 rows, row s at s * d_row_stride_bytes (16-byte aligned, stride >= 2H and a
+ *                    multiple of 16), expert_rows rows. Rows that no entry names keep their contents. Where
+ *                    two entries name one row (a table that moe_layout did not write), it holds the product
+ *                    of one of them.
+ *      d_topk_weights fp32 [S, K], fully overwritten.
+ * Enqueues one kernel. */
+int moe_combine_backward(const void *dy, const void *expert_out, int64_t row_stride_bytes,
+                         int64_t expert_rows, const int32_t *slot_idx, const float *topk_weights,
+                         int32_t S, int32_t H, int32_t K, void *d_expert_out,
+                         int64_t d_row_stride_bytes, float *d_topk_weights, hipStream_t stream);
+
+/* moe_dispatch_backward: dx[t] = bf16( sum over k = 0..K-1 ascending, slot valid, of
+ *                                      fp32(d_rows[slot_idx[t, k]]) ),
+ * fp32 accumulation from +0.0, one rounding to nearest even; a token with no valid entry gives +0.0.
+ * In:  d_rows   bf16 rows, expert_rows of them, 16-byte aligned, row_stride_bytes >= 2H, a multiple of 16.
+ * Out: dx       bf16 [S, H], 16-byte aligned, fully overwritten.
+ * Enqueues one kernel. */
+int moe_dispatch_backward(const void *d_rows, int64_t row_stride_bytes, int64_t expert_rows,
+                          const int32_t *slot_idx, int32_t S, int32_t H, int32_t K, void *dx,
+                          hipStream_t stream);
+
+/* ---- Microscaled (MX) rows ------------------------------------------------------------------------
+ *
+ * The block formats of the OCP Microscaling specification (version 1.0): 32 consecutive values share one
+ * E8M0 scale byte b, worth 2^(b - 127) (255 is NaN), and each value is held as a code, worth its scale times
+ * the code's value. Rows of H values (H % 32 == 0, MOE_ERR_UNSUPPORTED otherwise) are dense: `codes`
+ * uint8 [rows, moe_mx_row_bytes(H, format)], 16-byte aligned, and `scales` uint8 [rows, H / 32].
+ *   MOE_MX_E2M1  4-bit codes (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; the sign in bit 3), two to a byte, the
+ *                even column in the low half. b - 127 = floor(log2(amax)) - 2, the specification's choice; what
+ *                lies above 6 after scaling becomes 6.
+ *   MOE_MX_E4M3  8-bit E4M3FN codes. b - 127 is the smallest exponent with amax <= 448 * 2^(b - 127), so
+ *                that nothing saturates and every value is at most half a step (2^-4 relative, for values
+ *                that are not tiny in their block) off. The specification's floor(log2(amax)) - 8 would cut
+ *                the largest value of a block by up to 1/8, which a gradient that reads the row back
+ *                would see.
+ * In both, b - 127 is held to [-127, 127] (b = 0 for an all-zero block), codes are x / 2^(b - 127) rounded to
+ * the nearest, ties to the even code (a scaled value is exact, so this is the only rounding), the sign of a
+ * zero is kept, and a block that holds a NaN or an infinity gets b = 255 and zero codes: all of it reads
+ * back as NaN. */
+typedef enum {
+    MOE_MX_E2M1 = 1,
+    MOE_MX_E4M3 = 2
+} moe_mx_format;
+
+/* Bytes of one row's codes: H / 2 (E2M1) or H (E4M3); negative moe_status on a bad H or format. */
+int64_t moe_mx_row_bytes(int32_t H, int32_t format);
+
+/* moe_mx_quantize: rows 0..N-1 of a bf16 buffer to MX rows, N = min(*num_rows, max_rows), or max_rows where
+ * num_rows is NULL. Row r is at r * row_stride_bytes (>= 2H, a multiple of 16), so the rows may be
+ * moe_unpack's, or the window's own with stride moe_slot_bytes(H).
+ * moe_mx_dequantize: the values of MX rows as bf16, row r at r * row_stride_bytes. Exact, but for values that
+ * bf16 does not hold: bits below its smallest subnormal are rounded to nearest even, and 2^128, to which a
+ * block's largest values can round when they lie within 1/32 of bf16's largest, becomes an infinity.
+ * num_rows is a DEVICE pointer (e.g. &expert_slot_base[E]), read on the device; negative counts are 0.
+ * max_rows in [0, MOE_MAX_OUT_ROWS]; 0 enqueues nothing. Rows N..max_rows-1 of the outputs keep their
+ * contents, and so do the bytes between rows. Outputs must not overlap inputs. One kernel each. */
+int moe_mx_quantize(const void *rows, int64_t row_stride_bytes, const int32_t *num_rows,
+                    int64_t max_rows, int32_t H, int32_t format, void *codes, void *scales,
+                    hipStream_t stream);
+
+int moe_mx_dequantize(const void *codes, const void *scales, const int32_t *num_rows,
+                      int64_t max_rows, int32_t H, int32_t format, void *rows,
+                      int64_t row_stride_bytes, hipStream_t stream);
+
+/* The combine of a training step that keeps the expert rows for the backward in 8 bits, and the gradient
+ * that reads them: the rows are the layer's largest activation (S * K of them), and the backward needs
+ * them only for d_topk_weights.
+ *
+ * moe_combine_checkpoint: y exactly as moe_combine writes it (same arguments, same bits), and the MX rows
+ *      (MOE_MX_E4M3, as moe_mx_quantize makes them) of every row that an entry of slot_idx names, from the
+ *      one read of the rows that the combine makes. H % 32 == 0. codes uint8 [expert_rows, H] (16-byte
+ *      aligned), scales uint8 [expert_rows, H / 32]; rows that no entry names keep their contents.
+ * moe_combine_backward_mx: moe_combine_backward with the values of such rows in place of expert_out.
+ * Each enqueues one kernel. */
+int moe_combine_checkpoint(const void *expert_out, int64_t row_stride_bytes, int64_t expert_rows,
+                           const int32_t *slot_idx, const float *topk_weights, int32_t S,
+                           int32_t H, int32_t K, void *y, void *codes, void *scales,
+                           hipStream_t stream);
+
+int moe_combine_backward_mx(const void *dy, const void *codes, const void *scales,
+                            int64_t expert_rows, const int32_t *slot_idx,
+                            const float *topk_weights, int32_t S, int32_t H, int32_t K,
+                            void *d_expert_out, int64_t d_row_stride_bytes,
+                            float *d_topk_weights, hipStream_t stream);
+
+/* The experts' product of expert-major rows with the experts' weights, both MX E2M1: the grouped GEMM whose
+ * input moe_unpack lays out ("HCCL Window 模式 (Non-SHMEM) 代码深度剖析", section 3.9 ShareToOutput).
+ *
+ *   c[r, o] = sum over h of A[r, h] * W[g, o, h] for the group g with group_base[g] <= r < group_base[g + 1]
+ *   MOE_MX_PLAIN: out[r, o] = bf16(c[r, o]), o in [0, O)
+ *   MOE_MX_GATED: out[r, o] = bf16(silu(c[r, o]) * c[r, O/2 + o]), o in [0, O/2), silu(v) = v / (1 + exp(-v)):
+ *                 the weights' first O/2 rows are the gate, the rest the up projection
+ * Sums are accumulated in fp32 by the matrix cores, the activation is taken in fp32, and the result is
+ * rounded once. Rows of a group do not influence one another (a NaN block stays in its row).
+ *
+ * In:  a_codes, a_scales  MX E2M1 rows [a_rows, H] (a_rows in [0, MOE_MAX_OUT_ROWS]; 0 enqueues nothing).
+ *      group_base         DEVICE int32 [G + 1], ascending, read on the device: expert_slot_base of the layout, or
+ *                         a part of it (expert_slot_base + first, with the weights of G experts from there).
+ *                         Values are clamped to [0, a_rows]. Empty groups are fine.
+ *      G                  in [1, MOE_MAX_EXPERTS].
+ *      w_codes, w_scales  MX E2M1 rows [G, O, H]; O in [1, MOE_MAX_OUTPUTS], even for MOE_MX_GATED
+ *                         (MOE_ERR_UNSUPPORTED otherwise).
+ * Out: out                bf16, row r at r * out_stride_bytes (2-byte aligned, stride even and at least a row of
+ *                         results). Rows outside every group, and the bytes between rows, keep their contents.
+ * Enqueues one kernel. */
+typedef enum {
+    MOE_MX_PLAIN = 0,
+    MOE_MX_GATED = 1
+} moe_mx_epilogue;
+
+#define MOE_MAX_OUTPUTS 65536
+
+int moe_mx_product(const void *a_codes, const void *a_scales, int64_t a_rows,
+                   const int32_t *group_base, int32_t G, const void *w_codes, const void *w_scales,
+                   int32_t O, int32_t H, int32_t epilogue, void *out, int64_t out_stride_bytes,
+                   hipStream_t stream);
 
 /* Static description of a moe_status value (never NULL). */
 const char *moe_status_string(int status);

@@ -44,6 +44,8 @@ from .dispatch import (
 from .combine import combine, combine_bruteforce, combine_scatter, combine_staged
 from .unpack import aligned_row_base, unpack, unpack_padded
 from .dedup import dispatch_dedup, expand_dedup, rank_rows
+from .backward import combine_backward, dispatch_backward
+from .mx import mx_product, mx_quantize, mx_values
 
 __all__ = [
     "bf16_bits_to_f32",
@@ -69,4 +71,9 @@ __all__ = [
     "rank_rows",
     "dispatch_dedup",
     "expand_dedup",
+    "combine_backward",
+    "dispatch_backward",
+    "mx_quantize",
+    "mx_values",
+    "mx_product",
 ]
