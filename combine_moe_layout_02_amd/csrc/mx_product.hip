@@ -139,21 +139,41 @@ __device__ inline bool find_tile(const int32_t *__restrict__ base, int G, int64_
     return false;
 }
 
-constexpr int kTileThreads = 256;
-constexpr int kStageBlocks = 8;   // MX blocks of a stage: 256 values, 128 bytes of a row
+// Tiles of TM rows x TN weight rows (TN / 2 outputs when GATED), WMC x WNC waves, through LDS.
+//
+// Codes go from memory straight to LDS in stages of 128 values (64 bytes of a row) through a ring of four
+// buffers: at the start of a stage the loads of the third stage after it are issued, so a load has three
+// stages' products to arrive. Scales go through registers, 16 blocks (four stages) at a time. One
+// barrier a stage: it follows each wave's wait for its own loads of the stage and for its LDS reads of the
+// last one, so behind it the stage is whole and the buffer of the last stage is free.
+constexpr int kRing = 4;
+constexpr int kStageBlocks = 4;    // MX blocks of a stage
+constexpr int kScaleBlocks = 16;   // MX blocks of a round of scales: kRing stages
 
-// A tile of TM rows x TN weight rows (TN / 2 outputs when GATED), four waves as 2 x 2, K in stages of 256.
-template <int TM, int TN, bool GATED>
-__global__ __launch_bounds__(kTileThreads) void product_tile_kernel(
+// Waits until at most N of the wave's loads are in flight and its LDS accesses are done, then for all waves.
+template <int N>
+__device__ inline void stage_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int TM, int TN, int WMC, int WNC, bool GATED>
+__global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     const uint8_t *__restrict__ a_codes, const uint8_t *__restrict__ a_scales, int64_t a_rows,
     const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
     const uint8_t *__restrict__ w_scales, int O, int nblk, int ncol, uint8_t *__restrict__ out,
     int64_t out_stride, bool wide) {
-    constexpr int ROWS = TM + TN, WM = TM / 2, WN = TN / 2, MI = WM / 16, NI = WN / 16;
-    constexpr int LOADS = ROWS * 8 / kTileThreads;        // 16-byte pieces of a stage a thread loads
-    constexpr int SLOADS = ROWS * 2 / kTileThreads;       // scale words (four blocks) of a stage
-    __shared__ __align__(1024) uint8_t codes[2][ROWS * 128];
-    __shared__ __align__(16) uint32_t scales[2][ROWS * 2];
+    constexpr int NW = WMC * WNC, THREADS = 64 * NW;
+    constexpr int ROWS = TM + TN, WM = TM / WMC, WN = TN / WNC, MI = WM / 16, NI = WN / 16;
+    constexpr int LOADS = ROWS / 16 / NW;     // 16 rows of a stage a load
+    constexpr int SLOADS = ROWS / THREADS;    // rows of a round of scales a thread
+    static_assert(LOADS * 16 * NW == ROWS && SLOADS * THREADS == ROWS && TM % THREADS == 0 | SLOADS == 1, "shape");
+    // the ring's buffers are objects of their own, so that the compiler sees a buffer's reads and another's
+    // loads apart and puts no wait between them
+    __shared__ __align__(1024) uint8_t ring0[ROWS * 64], ring1[ROWS * 64], ring2[ROWS * 64], ring3[ROWS * 64];
+    uint8_t *const codes[kRing] = {ring0, ring1, ring2, ring3};
+    __shared__ __align__(16) uint8_t scales[2][ROWS * 16];
 
     int g, col;
     int64_t first, last;
@@ -168,63 +188,59 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(
     const int pitch = nblk * 16;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint8_t *wsc = w_scales + (int64_t)g * O * nblk;
-    const uint8_t *asc = a_scales + first * nblk;
     const __amdgpu_buffer_rsrc_t a_src = rsrc(a_codes + first * pitch, (int64_t)rows * pitch);
     const __amdgpu_buffer_rsrc_t w_src = rsrc(w_codes + (int64_t)g * O * pitch, (int64_t)O * pitch);
 
-    // Row of the weights behind tile row j: plain, neighbours; gated, each wave's half of the tile has its gate
+    // Row of the weights behind tile row j: plain, neighbours; gated, each wave's share of the tile has its gate
     // rows first, then the up rows of the same outputs. Rows past the end repeat the last one.
     const auto weight_row = [&](int j) {
         if (!GATED) return min(o0 + j, width - 1);
-        const int half = j / WN, jj = j % WN;
-        const int o = min(o0 + half * (WN / 2) + jj % (WN / 2), width - 1);
+        const int share = j / WN, jj = j % WN;
+        const int o = min(o0 + share * (WN / 2) + jj % (WN / 2), width - 1);
         return jj < WN / 2 ? o : width + o;
     };
 
-    // Piece l of a stage: tile row (l * 256 + tid) / 8, held at place tid % 8 of its 128 bytes; place p of row r
-    // holds block p ^ (r & 7), so that 16 rows' reads of one block spread over the banks.
-    const int place = tid & 7, r8 = tid >> 3, blk = place ^ (r8 & 7);
+    // Load l of a wave takes tile rows 16 (wave + l * NW) .. + 15, a lane 16 bytes: place lane % 4 of row lane / 4.
+    // Place p of row r holds block p ^ (r / 2 % 4): eight neighbouring rows' reads of one block then cover all
+    // the banks (SQ_LDS_BANK_CONFLICT is 0).
+    const int r4 = lane >> 2, blk = (lane & 3) ^ ((r4 >> 1) & 3);
     int voff[LOADS];
 #pragma unroll
     for (int l = 0; l < LOADS; ++l) {
-        const int r = l * (kTileThreads / 8) + r8;
+        const int r = 16 * (wave + l * NW) + r4;
         voff[l] = (r < TM ? min(r, rows - 1) : weight_row(r - TM)) * pitch + blk * 16;
     }
-    int soff[SLOADS];
+    const uint8_t *ssrc[SLOADS];
 #pragma unroll
     for (int l = 0; l < SLOADS; ++l) {
-        const int r = (l * kTileThreads + tid) >> 1;
-        soff[l] = (r < TM ? min(r, rows - 1) : weight_row(r - TM)) * nblk;
+        const int r = l * THREADS + tid;
+        ssrc[l] = r < TM ? a_scales + (first + min(r, rows - 1)) * nblk
+                         : w_scales + ((int64_t)g * O + weight_row(r - TM)) * nblk;
     }
-    const int sword = tid & 1;
 
-    const int stages = (nblk + kStageBlocks - 1) / kStageBlocks;
     const auto load_codes = [&](int st, int buf) {
         const bool past = st * kStageBlocks + blk >= nblk;  // blocks behind the row's end read as zero
 #pragma unroll
-        for (int l = 0; l < LOADS; ++l) {
-            uint8_t *dst = &codes[buf][(l * kTileThreads + wave * 64) * 16];
-            load_to_lds(l * (kTileThreads / 8) < TM ? a_src : w_src, dst, past ? 0x7FFFFFF0 : voff[l], st * 128);
-        }
+        for (int l = 0; l < LOADS; ++l)
+            load_to_lds(16 * (wave + l * NW) < TM ? a_src : w_src, &codes[buf][(wave + l * NW) * 1024],
+                        past ? 0x7FFFFFF0 : voff[l], st * 64);
     };
-    uint32_t sreg[SLOADS];
-    const auto load_scales = [&](int st) {
-        // the word of blocks b .. b + 3; at the row's end, the row's last four bytes (nblk >= 4) moved down, so
-        // that blocks behind the end have scale byte 0
-        const int b = st * kStageBlocks + 4 * sword, from = min(b, nblk - 4);
-        const int down = min(8 * (b - from), 63);
+    u32x4 sreg[SLOADS];
+    // A round of a row's scales: 16 bytes. Rounds that end behind the row take its last 16 bytes (nblk >= 16) and
+    // are moved down when put, so that blocks behind the end have scale byte 0.
+    const auto load_scales = [&](int round) {
+        const int from = min(round * kScaleBlocks, nblk - kScaleBlocks);
+#pragma unroll
+        for (int l = 0; l < SLOADS; ++l) __builtin_memcpy(&sreg[l], ssrc[l] + from, 16);
+    };
+    const auto put_scales = [&](int round, int buf) {
+        const int down = min(max(round * kScaleBlocks - (nblk - kScaleBlocks), 0), 16);
 #pragma unroll
         for (int l = 0; l < SLOADS; ++l) {
-            const uint8_t *src = (((l * kTileThreads + tid) >> 1) < TM ? asc : wsc) + soff[l] + from;
-            uint32_t v;
-            __builtin_memcpy(&v, src, 4);
-            sreg[l] = (uint32_t)((uint64_t)v >> down);
+            const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, sreg[l]);
+            const unsigned __int128 moved = down == 0 ? v : down == 16 ? 0 : v >> (8 * down);
+            *reinterpret_cast<u32x4 *>(&scales[buf][(l * THREADS + tid) * 16]) = __builtin_bit_cast(u32x4, moved);
         }
-    };
-    const auto put_scales = [&](int buf) {
-#pragma unroll
-        for (int l = 0; l < SLOADS; ++l) scales[buf][l * kTileThreads + tid] = sreg[l];
     };
 
     f32x4 acc[MI][NI];
@@ -233,50 +249,47 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(
 #pragma unroll
         for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    const int wm = (wave & 1) * WM, wn = TM + (wave >> 1) * WN;
+    const int wm = (wave % WMC) * WM, wn = TM + (wave / WMC) * WN;
     const int fr = lane & 15, q = lane >> 4;
+    const int at = fr * 64 + (q ^ ((fr >> 1) & 3)) * 16;
 
-    load_codes(0, 0);
+    const int stages = (nblk + kStageBlocks - 1) / kStageBlocks;
     load_scales(0);
-    put_scales(0);
-    __syncthreads();
-    for (int st = 0; st < stages; ++st) {
-        const int buf = st & 1;
-        i32x4 a[2][MI], w[2][NI];
-        u32x2 as[MI], ws[NI];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) as[i] = *reinterpret_cast<const u32x2 *>(&scales[buf][(wm + i * 16 + fr) * 2]);
+    for (int s = 0; s < kRing - 1; ++s) load_codes(s, s);
+    put_scales(0, 0);
+    for (int round = 0; round * kRing < stages; ++round) {
 #pragma unroll
-        for (int j = 0; j < NI; ++j) ws[j] = *reinterpret_cast<const u32x2 *>(&scales[buf][(wn + j * 16 + fr) * 2]);
+        for (int s = 0; s < kRing; ++s) {
+            const int st = round * kRing + s;
+            if (st >= stages) break;
+            stage_barrier<(kRing - 2) * LOADS>();
+            load_codes(st + kRing - 1, (s + kRing - 1) % kRing);
+            if (s == 0) load_scales(round + 1);
+            i32x4 a[MI], w[NI];
+            int as[MI], ws[NI];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const int at = ((4 * ks + q) ^ (fr & 7)) * 16;
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-                a[ks][i] = *reinterpret_cast<const i32x4 *>(&codes[buf][(wm + i * 16 + fr) * 128 + at]);
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-                w[ks][j] = *reinterpret_cast<const i32x4 *>(&codes[buf][(wn + j * 16 + fr) * 128 + at]);
-        }
-        if (st + 1 < stages) {
-            load_codes(st + 1, buf ^ 1);
-            load_scales(st + 1);
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+            for (int j = 0; j < NI; ++j) {
+                w[j] = *reinterpret_cast<const i32x4 *>(&codes[s][(wn + j * 16) * 64 + at]);
+                ws[j] = *reinterpret_cast<const int *>(&scales[round & 1][(wn + j * 16 + fr) * 16 + s * 4]);
+            }
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                const int sa = (int)(as[i][ks] >> (8 * q));
-#pragma unroll
-                for (int j = 0; j < NI; ++j)
-                    acc[i][j] = mfma(w[ks][j], (int)(ws[j][ks] >> (8 * q)), a[ks][i], sa, acc[i][j]);
+                a[i] = *reinterpret_cast<const i32x4 *>(&codes[s][(wm + i * 16) * 64 + at]);
+                as[i] = *reinterpret_cast<const int *>(&scales[round & 1][(wm + i * 16 + fr) * 16 + s * 4]);
             }
+#pragma unroll
+            for (int j = 0; j < NI; ++j) ws[j] = (int)((uint32_t)ws[j] >> (8 * q));
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int sa = (int)((uint32_t)as[i] >> (8 * q));
+#pragma unroll
+                for (int j = 0; j < NI; ++j) acc[i][j] = mfma(w[j], ws[j], a[i], sa, acc[i][j]);
+            }
+            if (s == kRing - 1) put_scales(round + 1, (round + 1) & 1);
         }
-        // the wait for the next stage stays behind this stage's products
-        __builtin_amdgcn_sched_barrier(0);
-        if (st + 1 < stages) put_scales(buf ^ 1);
-        __syncthreads();
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the wave's end
 
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -289,7 +302,7 @@ __global__ __launch_bounds__(kTileThreads) void product_tile_kernel(
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 v[e] = GATED ? silu(acc[i][j][e]) * acc[i][(j + NI / 2) % NI][e] : acc[i][j][e];
-            store4(dst, o0 + (wave >> 1) * (GATED ? WN / 2 : WN) + j * 16 + 4 * q, width, wide, v);
+            store4(dst, o0 + (wave / WMC) * (GATED ? WN / 2 : WN) + j * 16 + 4 * q, width, wide, v);
         }
     }
 }
@@ -338,7 +351,7 @@ __global__ __launch_bounds__(64) void product_kernel(
     }
 }
 
-template <int TM, int TN>
+template <int TM, int TN, int WMC, int WNC>
 hipError_t tiles(const void *a_codes, const void *a_scales, int64_t a_rows, const int32_t *group_base,
                  int32_t G, const void *w_codes, const void *w_scales, int32_t O, int32_t H, bool gated,
                  void *out, int64_t out_stride, bool wide, hipStream_t stream) {
@@ -346,8 +359,8 @@ hipError_t tiles(const void *a_codes, const void *a_scales, int64_t a_rows, cons
     const int ncol = (width + tn - 1) / tn;
     const int64_t row_tiles = a_rows / TM + (a_rows < G ? a_rows : G);  // at most
     const int64_t grid = (row_tiles * ncol + 7) / 8 * 8;
-    auto *kernel = gated ? product_tile_kernel<TM, TN, true> : product_tile_kernel<TM, TN, false>;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(kTileThreads), 0, stream,
+    auto *kernel = gated ? product_tile_kernel<TM, TN, WMC, WNC, true> : product_tile_kernel<TM, TN, WMC, WNC, false>;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WMC * WNC), 0, stream,
                        static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales),
                        a_rows, group_base, G, static_cast<const uint8_t *>(w_codes),
                        static_cast<const uint8_t *>(w_scales), O, H / 32, ncol,
@@ -367,11 +380,11 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
     const int64_t row_tiles = a_rows / 16 + (a_rows < G ? a_rows : G);
     const bool wide = out_stride_bytes % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 8 == 0;
     const int64_t mean = a_rows / G;
-    if (mean >= 192 && H >= 128)
-        return tiles<256, 256>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+    if (mean >= 192 && H >= 512)
+        return tiles<256, 256, 2, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
                                out_stride_bytes, wide, stream);
-    if (mean >= 32 && H >= 128)
-        return tiles<128, 128>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+    if (mean >= 32 && H >= 512)
+        return tiles<128, 128, 2, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
                                out_stride_bytes, wide, stream);
     auto *kernel = gated ? product_kernel<true> : product_kernel<false>;
     hipLaunchKernelGGL(kernel, dim3((uint32_t)row_tiles, (width + 15) / 16), dim3(64), 0, stream,
