@@ -22,6 +22,13 @@ __device__ inline f32x4 mfma(const i32x4 &a, int a_scale, const i32x4 &b, int b_
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, a_scale, 0, b_scale);
 }
 
+// The same with byte S of the scale registers.
+template <int S>
+__device__ inline f32x4 mfma_byte(const i32x4 &a, int a_scale, const i32x4 &b, int b_scale, const f32x4 &c) {
+    const i32x8 a8 = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, b8 = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, S, a_scale, S, b_scale);
+}
+
 // The rows [first, last) that tile number `tile` covers, TM rows at most, and their group; false when there
 // are fewer tiles. Groups' tiles follow one another; every lane of a wave calls this and gets the same.
 template <int TM>
@@ -142,10 +149,11 @@ __device__ inline bool find_tile(const int32_t *__restrict__ base, int G, int64_
 // Tiles of TM rows x TN weight rows (TN / 2 outputs when GATED), WMC x WNC waves, through LDS.
 //
 // Codes go from memory straight to LDS in stages of 128 values (64 bytes of a row) through a ring of four
-// buffers: at the start of a stage the loads of the third stage after it are issued, so a load has three
-// stages' products to arrive. Scales go through registers, 16 blocks (four stages) at a time. One
-// barrier a stage: it follows each wave's wait for its own loads of the stage and for its LDS reads of the
-// last one, so behind it the stage is whole and the buffer of the last stage is free.
+// buffers, and from there to registers one stage ahead of the products: while the matrix cores work on stage
+// s, its successor is read from LDS and stage s + 4 is loaded into the buffer that stage s has left. Scales
+// come through registers, 16 blocks (four stages, one round) at a time, and lie in LDS so that one word holds
+// a lane's four scales of a round. One barrier a stage: it follows each wave's wait for its own loads of the
+// next stage and for its LDS reads of this one, so behind it the next stage is whole and this buffer is free.
 constexpr int kRing = 4;
 constexpr int kStageBlocks = 4;    // MX blocks of a stage
 constexpr int kScaleBlocks = 16;   // MX blocks of a round of scales: kRing stages
@@ -168,7 +176,7 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     constexpr int ROWS = TM + TN, WM = TM / WMC, WN = TN / WNC, MI = WM / 16, NI = WN / 16;
     constexpr int LOADS = ROWS / 16 / NW;     // 16 rows of a stage a load
     constexpr int SLOADS = ROWS / THREADS;    // rows of a round of scales a thread
-    static_assert(LOADS * 16 * NW == ROWS && SLOADS * THREADS == ROWS && TM % THREADS == 0 | SLOADS == 1, "shape");
+    static_assert(LOADS * 16 * NW == ROWS && SLOADS * THREADS == ROWS && kRing == 4, "shape");
     // the ring's buffers are objects of their own, so that the compiler sees a buffer's reads and another's
     // loads apart and puts no wait between them
     __shared__ __align__(1024) uint8_t ring0[ROWS * 64], ring1[ROWS * 64], ring2[ROWS * 64], ring3[ROWS * 64];
@@ -233,13 +241,19 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
 #pragma unroll
         for (int l = 0; l < SLOADS; ++l) __builtin_memcpy(&sreg[l], ssrc[l] + from, 16);
     };
+    // Put as [row][lane's k-block q][stage of the round]: the transpose of the row's 4 x 4 bytes.
     const auto put_scales = [&](int round, int buf) {
         const int down = min(max(round * kScaleBlocks - (nblk - kScaleBlocks), 0), 16);
 #pragma unroll
         for (int l = 0; l < SLOADS; ++l) {
             const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, sreg[l]);
             const unsigned __int128 moved = down == 0 ? v : down == 16 ? 0 : v >> (8 * down);
-            *reinterpret_cast<u32x4 *>(&scales[buf][(l * THREADS + tid) * 16]) = __builtin_bit_cast(u32x4, moved);
+            const u32x4 m = __builtin_bit_cast(u32x4, moved);
+            const uint32_t lo01 = __builtin_amdgcn_perm(m[1], m[0], 0x05010400), hi01 = __builtin_amdgcn_perm(m[1], m[0], 0x07030602);
+            const uint32_t lo23 = __builtin_amdgcn_perm(m[3], m[2], 0x05010400), hi23 = __builtin_amdgcn_perm(m[3], m[2], 0x07030602);
+            *reinterpret_cast<u32x4 *>(&scales[buf][(l * THREADS + tid) * 16]) =
+                u32x4{__builtin_amdgcn_perm(lo23, lo01, 0x05040100), __builtin_amdgcn_perm(lo23, lo01, 0x07060302),
+                      __builtin_amdgcn_perm(hi23, hi01, 0x05040100), __builtin_amdgcn_perm(hi23, hi01, 0x07060302)};
         }
     };
 
@@ -253,6 +267,21 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     const int fr = lane & 15, q = lane >> 4;
     const int at = fr * 64 + (q ^ ((fr >> 1) & 3)) * 16;
 
+    i32x4 a[MI], w[NI];
+    int as[MI], ws[NI];
+    const auto read_codes = [&](const uint8_t *buf) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j) w[j] = *reinterpret_cast<const i32x4 *>(&buf[(wn + j * 16) * 64 + at]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) a[i] = *reinterpret_cast<const i32x4 *>(&buf[(wm + i * 16) * 64 + at]);
+    };
+    const auto read_scales = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j) ws[j] = *reinterpret_cast<const int *>(&scales[buf][(wn + j * 16 + fr) * 16 + q * 4]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) as[i] = *reinterpret_cast<const int *>(&scales[buf][(wm + i * 16 + fr) * 16 + q * 4]);
+    };
+
     const int stages = (nblk + kStageBlocks - 1) / kStageBlocks;
     load_scales(0);
 #pragma unroll
@@ -264,28 +293,24 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
             const int st = round * kRing + s;
             if (st >= stages) break;
             stage_barrier<(kRing - 2) * LOADS>();
-            load_codes(st + kRing - 1, (s + kRing - 1) % kRing);
+            if (s == 0) read_scales(round & 1);
+            read_codes(codes[s]);
             if (s == 0) load_scales(round + 1);
-            i32x4 a[MI], w[NI];
-            int as[MI], ws[NI];
-#pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                w[j] = *reinterpret_cast<const i32x4 *>(&codes[s][(wn + j * 16) * 64 + at]);
-                ws[j] = *reinterpret_cast<const int *>(&scales[round & 1][(wn + j * 16 + fr) * 16 + s * 4]);
-            }
+            load_codes(st + kRing - 1, (s + kRing - 1) % kRing);
+            __builtin_amdgcn_sched_barrier(0);  // the reads and loads are under way before the products
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                a[i] = *reinterpret_cast<const i32x4 *>(&codes[s][(wm + i * 16) * 64 + at]);
-                as[i] = *reinterpret_cast<const int *>(&scales[round & 1][(wm + i * 16 + fr) * 16 + s * 4]);
+#pragma unroll
+                for (int j = 0; j < NI; ++j) {
+                    f32x4 &c = acc[i][j];
+                    const i32x4 &x = a[i], &y = w[j];
+                    if (s == 0) c = mfma_byte<0>(y, ws[j], x, as[i], c);
+                    else if (s == 1) c = mfma_byte<1>(y, ws[j], x, as[i], c);
+                    else if (s == 2) c = mfma_byte<2>(y, ws[j], x, as[i], c);
+                    else c = mfma_byte<3>(y, ws[j], x, as[i], c);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < NI; ++j) ws[j] = (int)((uint32_t)ws[j] >> (8 * q));
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                const int sa = (int)((uint32_t)as[i] >> (8 * q));
-#pragma unroll
-                for (int j = 0; j < NI; ++j) acc[i][j] = mfma(w[j], ws[j], a[i], sa, acc[i][j]);
-            }
+            __builtin_amdgcn_sched_barrier(0);
             if (s == kRing - 1) put_scales(round + 1, (round + 1) & 1);
         }
     }
