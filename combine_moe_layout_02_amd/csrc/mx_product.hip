@@ -16,13 +16,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-__device__ inline f32x4 mfma(const i32x4 &a, int a_scale, const i32x4 &b, int b_scale, const f32x4 &c) {
-    const i32x8 a8 = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, b8 = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
-    // operand formats 4 = E2M1; the scale is the low byte of its register
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, a_scale, 0, b_scale);
-}
-
-// The same with byte S of the scale registers.
+// One such product with byte S of the scale registers (operand formats 4 = E2M1).
 template <int S>
 __device__ inline f32x4 mfma_byte(const i32x4 &a, int a_scale, const i32x4 &b, int b_scale, const f32x4 &c) {
     const i32x8 a8 = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, b8 = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
@@ -82,6 +76,14 @@ __device__ inline __amdgpu_buffer_rsrc_t rsrc(const void *base, int64_t bytes) {
 // whole wave); zero where the buffer ends before.
 __device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t src, uint8_t *dst, int voff, int soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
+}
+
+// The transpose of 4 x 4 bytes: word q of the result has byte q of the four words.
+__device__ inline u32x4 transpose_bytes(const u32x4 &m) {
+    const uint32_t lo01 = __builtin_amdgcn_perm(m[1], m[0], 0x05010400), hi01 = __builtin_amdgcn_perm(m[1], m[0], 0x07030602);
+    const uint32_t lo23 = __builtin_amdgcn_perm(m[3], m[2], 0x05010400), hi23 = __builtin_amdgcn_perm(m[3], m[2], 0x07030602);
+    return u32x4{__builtin_amdgcn_perm(lo23, lo01, 0x05040100), __builtin_amdgcn_perm(lo23, lo01, 0x07060302),
+                 __builtin_amdgcn_perm(hi23, hi01, 0x05040100), __builtin_amdgcn_perm(hi23, hi01, 0x07060302)};
 }
 
 // The groups' rows and tiles, in LDS: rows [lo, hi) of group g, and the number of row tiles up to its end.
@@ -253,11 +255,7 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
         for (int l = 0; l < SLOADS; ++l) {
             const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, sreg[l]);
             const u32x4 m = __builtin_bit_cast(u32x4, down == 0 ? v : v >> (8 * down));
-            const uint32_t lo01 = __builtin_amdgcn_perm(m[1], m[0], 0x05010400), hi01 = __builtin_amdgcn_perm(m[1], m[0], 0x07030602);
-            const uint32_t lo23 = __builtin_amdgcn_perm(m[3], m[2], 0x05010400), hi23 = __builtin_amdgcn_perm(m[3], m[2], 0x07030602);
-            *reinterpret_cast<u32x4 *>(&scales[buf][(l * THREADS + tid) * 16]) =
-                u32x4{__builtin_amdgcn_perm(lo23, lo01, 0x05040100), __builtin_amdgcn_perm(lo23, lo01, 0x07060302),
-                      __builtin_amdgcn_perm(hi23, hi01, 0x05040100), __builtin_amdgcn_perm(hi23, hi01, 0x07060302)};
+            *reinterpret_cast<u32x4 *>(&scales[buf][(l * THREADS + tid) * 16]) = transpose_bytes(m);
         }
     };
 
@@ -377,48 +375,169 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the wave's end
 }
 
-// grid = (row tiles of 16, tiles of 16 outputs), one wave each, straight from memory.
-template <bool GATED>
-__global__ __launch_bounds__(64) void product_kernel(
+// Few rows a group: the weights' bytes bound the product. A workgroup takes 16 * MF rows of a group and 32 weight
+// rows (16 outputs when GATED), its four waves a quarter of H each, and every wave streams its quarter
+// through a ring of its own in LDS, waiting for nobody; the partial sums meet in LDS and are added in the
+// waves' order. LDS turns the loads' order (four lanes to a row, 64 bytes) into the matrix cores' (a lane
+// to a row): loaded straight to registers in their order, each lane's 16 bytes are an access of the L1 of
+// their own, and 8 rows on 32 groups, H = 7168, O = 4096, took 32 us.
+constexpr int kSmallWaves = 4;
+
+// Bytes `from` .. + 15 of a row of n, zero behind its end: loaded now, put in place later, so that nothing waits
+// here. A row's last 16 bytes at the latest are loaded, and moved down when placed; SHORT rows (n < 16) go byte
+// by byte.
+template <bool SHORT>
+__device__ inline u32x4 load_row16(const uint8_t *row, int from, int n) {
+    u32x4 v = {0, 0, 0, 0};
+    if constexpr (!SHORT) {
+        __builtin_memcpy(&v, row + min(from, n - 16), 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (from + i < n) v[i >> 2] |= (uint32_t)row[from + i] << (8 * (i & 3));
+    }
+    return v;
+}
+
+template <bool SHORT>
+__device__ inline u32x4 place_row16(const u32x4 &v, int from, int n) {
+    if constexpr (SHORT) return v;
+    const int down = max(from - (n - 16), 0);
+    const unsigned __int128 wide = __builtin_bit_cast(unsigned __int128, v);
+    return __builtin_bit_cast(u32x4, down == 0 ? wide : down >= 16 ? 0 : wide >> (8 * down));
+}
+
+template <int MF, bool GATED, bool SHORT>
+__global__ __launch_bounds__(64 * kSmallWaves) void product_small_kernel(
     const uint8_t *__restrict__ a_codes, const uint8_t *__restrict__ a_scales, int64_t a_rows,
     const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
-    const uint8_t *__restrict__ w_scales, int O, int H, uint8_t *__restrict__ out,
+    const uint8_t *__restrict__ w_scales, int O, int nblk, int row_tiles, uint8_t *__restrict__ out,
     int64_t out_stride) {
+    constexpr int F = MF + 2, ROWS = 16 * F;  // at most 64; fragments of 16 rows: the rows, then two of the weights
+    __shared__ __align__(1024) uint8_t ring0[kSmallWaves][F * 1024], ring1[kSmallWaves][F * 1024], ring2[kSmallWaves][F * 1024],
+        ring3[kSmallWaves][F * 1024];
+    __shared__ __align__(16) uint8_t scales[kSmallWaves][64 * 16];  // a lane puts a row, the last lanes one again
     int g;
     int64_t first, last;
-    if (!find_rows<16>(base, G, a_rows, blockIdx.x, g, first, last)) return;
-    const int lane = threadIdx.x, r = lane & 15, q = lane >> 4;
-    const int nblk = H / 32, width = GATED ? O / 2 : O;
-    const int o0 = blockIdx.y * 16;
-    const int64_t row = min(first + r, last - 1);          // lanes past the tile repeat its last row
-    const int64_t wrow = (int64_t)g * O + min(o0 + r, width - 1);
-    const int64_t urow = wrow + width;
-    f32x4 acc = {0, 0, 0, 0}, up = {0, 0, 0, 0};
-    for (int b0 = 0; b0 < nblk; b0 += 4) {
-        const int b = b0 + q;
-        const bool in = b < nblk;
-        i32x4 x = {0, 0, 0, 0}, w = {0, 0, 0, 0}, u = {0, 0, 0, 0};
-        int xs = 0, ws = 0, us = 0;
-        if (in) {
-            x = *reinterpret_cast<const i32x4 *>(a_codes + (row * nblk + b) * 16);
-            xs = a_scales[row * nblk + b];
-            w = *reinterpret_cast<const i32x4 *>(w_codes + (wrow * nblk + b) * 16);
-            ws = w_scales[wrow * nblk + b];
-            if (GATED) {
-                u = *reinterpret_cast<const i32x4 *>(w_codes + (urow * nblk + b) * 16);
-                us = w_scales[urow * nblk + b];
-            }
-        }
-        acc = mfma(w, ws, x, xs, acc);
-        if (GATED) up = mfma(u, us, x, xs, up);
-    }
-    if (first + r >= last) return;
-    uint16_t *dst = reinterpret_cast<uint16_t *>(out + (first + r) * out_stride);
+    const int col = blockIdx.x / row_tiles;
+    if (!find_rows<16 * MF>(base, G, a_rows, blockIdx.x - col * row_tiles, g, first, last)) return;
+    g = __builtin_amdgcn_readfirstlane(g);
+    first = __builtin_amdgcn_readfirstlane((int)first);
+    last = __builtin_amdgcn_readfirstlane((int)last);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, q = lane >> 4;
+    const int width = GATED ? O / 2 : O, o0 = col * (GATED ? 16 : 32), pitch = nblk * 16;
+    uint8_t *const codes[kRing] = {ring0[wave], ring1[wave], ring2[wave], ring3[wave]};
+    const int rows = (int)(last - first);
+    const __amdgpu_buffer_rsrc_t a_src = rsrc(a_codes + first * pitch, (int64_t)rows * pitch);
+    const __amdgpu_buffer_rsrc_t w_src = rsrc(w_codes + (int64_t)g * O * pitch, (int64_t)O * pitch);
+    // row r of the tile's ROWS, in its own matrix; rows past the end repeat the last one
+    const auto row_of = [&](int r) {
+        if (r < 16 * MF) return min(r, rows - 1);
+        const int j = r - 16 * MF;
+        return GATED ? min(o0 + (j & 15), width - 1) + (j >> 4) * width : min(o0 + j, width - 1);
+    };
+    const int r4 = lane >> 2, blk = (lane & 3) ^ ((r4 >> 1) & 3);  // as in the tiles above
+    int voff[F];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int o = o0 + 4 * q + i;
-        if (o < width) dst[o] = (uint16_t)bf16_pair(GATED ? silu(acc[i]) * up[i] : acc[i], 0.0f);
+    for (int f = 0; f < F; ++f) voff[f] = row_of(16 * f + r4) * pitch + blk * 16;
+
+    const int steps = (nblk + kStageBlocks - 1) / kStageBlocks;
+    const int share = (steps + kSmallWaves - 1) / kSmallWaves;
+    const int begin = min(wave * share, steps), count = min(share, steps - begin);
+    const auto load_codes = [&](int i, uint8_t *buf) {  // step i of the wave's
+        const bool past = i >= count || (begin + i) * kStageBlocks + blk >= nblk;
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            load_to_lds(f < MF ? a_src : w_src, &buf[f * 1024], past ? 0x7FFFFFF0 : voff[f], (begin + i) * 64);
+    };
+    const int srow_at = min(lane, ROWS - 1);
+    const uint8_t *srow = srow_at < 16 * MF ? a_scales + (first + row_of(srow_at)) * nblk
+                                            : w_scales + ((int64_t)g * O + row_of(srow_at)) * nblk;
+
+    f32x4 acc[MF][2];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+    u32x4 sreg = load_row16<SHORT>(srow, begin * kStageBlocks, nblk);
+#pragma unroll
+    for (int s = 0; s < kRing - 1; ++s) load_codes(s, codes[s]);
+    const int at = fr * 64 + (q ^ ((fr >> 1) & 3)) * 16;
+    const auto put_scales = [&](int i0) {
+        *reinterpret_cast<u32x4 *>(&scales[wave][lane * 16]) =
+            transpose_bytes(place_row16<SHORT>(sreg, (begin + i0) * kStageBlocks, nblk));
+    };
+    put_scales(0);
+    for (int i0 = 0; i0 < count; i0 += kRing) {
+        int sc[F];  // a lane's scales of this round's four steps, one word a fragment
+#pragma unroll
+        for (int f = 0; f < F; ++f) sc[f] = *reinterpret_cast<const int *>(&scales[wave][(f * 16 + fr) * 16 + q * 4]);
+        sreg = load_row16<SHORT>(srow, (begin + i0 + kRing) * kStageBlocks, nblk);
+#pragma unroll
+        for (int s = 0; s < kRing; ++s) {
+            __builtin_amdgcn_sched_barrier(0);  // the scales' load stays above, their use below
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kRing - 2) * F) : "memory");
+            load_codes(i0 + s + kRing - 1, codes[(s + kRing - 1) % kRing]);
+            i32x4 v[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f) v[f] = *reinterpret_cast<const i32x4 *>(&codes[s][f * 1024 + at]);
+            if (i0 + s < count) {  // behind them the codes are zero, but a scale may be a NaN
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        f32x4 &c = acc[i][j];
+                        if (s == 0) c = mfma_byte<0>(v[MF + j], sc[MF + j], v[i], sc[i], c);
+                        else if (s == 1) c = mfma_byte<1>(v[MF + j], sc[MF + j], v[i], sc[i], c);
+                        else if (s == 2) c = mfma_byte<2>(v[MF + j], sc[MF + j], v[i], sc[i], c);
+                        else c = mfma_byte<3>(v[MF + j], sc[MF + j], v[i], sc[i], c);
+                    }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (s == kRing - 1) put_scales(i0 + kRing);
+        }
     }
+    // every load has arrived before the rings hold sums, and before the wave ends
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    f32x4 *const partial = reinterpret_cast<f32x4 *>(&ring0[0][0]);  // [wave][fragment][lane]
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) partial[(wave * 2 * MF + i * 2 + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    // a wave for each fragment of results
+    for (int f = wave; f < (GATED ? MF : 2 * MF); f += kSmallWaves) {
+        const int i = GATED ? f : f >> 1;
+        f32x4 sum = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < kSmallWaves; ++k) {
+            sum += partial[(k * 2 * MF + (GATED ? 2 * f : f)) * 64 + lane];
+            if (GATED) up += partial[(k * 2 * MF + 2 * f + 1) * 64 + lane];
+        }
+        if (16 * i + fr >= rows) continue;
+        uint16_t *dst = reinterpret_cast<uint16_t *>(out + (first + 16 * i + fr) * out_stride);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int o = o0 + (GATED ? 0 : 16 * (f & 1)) + 4 * q + e;
+            if (o < width) dst[o] = (uint16_t)bf16_pair(GATED ? silu(sum[e]) * up[e] : sum[e], 0.0f);
+        }
+    }
+}
+
+template <int MF>
+hipError_t few_rows(const void *a_codes, const void *a_scales, int64_t a_rows, const int32_t *group_base,
+                    int32_t G, const void *w_codes, const void *w_scales, int32_t O, int32_t H, bool gated,
+                    void *out, int64_t out_stride, hipStream_t stream) {
+    const int64_t row_tiles = a_rows / (16 * MF) + (a_rows < G ? a_rows : G);
+    const int ncol = gated ? (O / 2 + 15) / 16 : (O + 31) / 32;
+    auto *kernel = H >= 512 ? (gated ? product_small_kernel<MF, true, false> : product_small_kernel<MF, false, false>)
+                            : (gated ? product_small_kernel<MF, true, true> : product_small_kernel<MF, false, true>);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(row_tiles * ncol)), dim3(64 * kSmallWaves), 0, stream,
+                       static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales), a_rows,
+                       group_base, G, static_cast<const uint8_t *>(w_codes),
+                       static_cast<const uint8_t *>(w_scales), O, H / 32, (int)row_tiles,
+                       static_cast<uint8_t *>(out), out_stride);
+    return hipGetLastError();
 }
 
 template <int TM, int TN, int WMC, int WNC>
@@ -448,7 +567,6 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
     if (a_rows == 0) return hipSuccess;
     const bool gated = epilogue == MOE_MX_GATED;
     const int width = gated ? O / 2 : O;
-    const int64_t row_tiles = a_rows / 16 + (a_rows < G ? a_rows : G);
     // rows of whole 16-byte pieces, and a tile of them within a buffer descriptor's range
     const bool wide = width % 8 == 0 && out_stride_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                       out_stride_bytes <= (1 << 22);
@@ -459,13 +577,11 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
     if (mean >= 32 && H >= 512)
         return tiles<128, 128, 2, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
                                out_stride_bytes, wide, 512, stream);
-    auto *kernel = gated ? product_kernel<true> : product_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)row_tiles, (width + 15) / 16), dim3(64), 0, stream,
-                       static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales),
-                       a_rows, group_base, G, static_cast<const uint8_t *>(w_codes),
-                       static_cast<const uint8_t *>(w_scales), O, H, static_cast<uint8_t *>(out),
-                       out_stride_bytes);
-    return hipGetLastError();
+    if (mean >= 8)
+        return few_rows<2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                           out_stride_bytes, stream);
+    return few_rows<1>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                       out_stride_bytes, stream);
 }
 
 }  // namespace moe

@@ -336,7 +336,7 @@ def product_case(moe, rng, counts, H, O, gated, low=-1, high=1, behind=0, before
 PRODUCTS = [  # rows of each group, H, O
     ([1], 32, 1), ([1], 32, 2), ([3, 0, 1], 64, 16), ([0, 0, 5], 96, 18), ([16, 17, 15], 128, 64), ([0, 33, 0, 1, 0], 160, 100),
     ([130, 7], 288, 130), ([256, 255, 257], 256, 256), ([1] * 40, 512, 72), ([300], 1056, 1000), ([2, 600, 61], 544, 322),
-    ([8] * 3, 7168, 258), ([65, 0, 64, 63], 2048, 510), ([5, 1, 0, 2], 7168, 130), ([40] * 20, 608, 90), ([513, 0, 1023], 992, 514),
+    ([8] * 3, 7168, 258), ([9] * 5, 7168, 96), ([20, 3, 0, 31], 512, 66), ([12, 40], 736, 32), ([1, 2], 480, 48), ([65, 0, 64, 63], 2048, 510), ([5, 1, 0, 2], 7168, 130), ([40] * 20, 608, 90), ([513, 0, 1023], 992, 514),
 ]
 
 
@@ -368,16 +368,18 @@ def test_product_free_scales(moe, counts, H, O):
     assert np.all(err <= H * 2.0**-23 * magnitude + 2.0**-8 * np.abs(exact))
 
 
-@pytest.mark.parametrize("counts", [[2, 3], [40, 30], [300, 20]])
-def test_product_nan_blocks(moe, counts):
+@pytest.mark.parametrize("H", [160, 544, 1056, 2080])
+@pytest.mark.parametrize("counts", [[2, 3], [9, 14], [40, 30], [300, 100]])
+def test_product_nan_blocks(moe, counts, H):
     """A NaN scale of a row makes that row NaN and no other; one of a weight row its column of its group. The last
     block (H is no multiple of the tile's depth) as well as the first."""
     rng = np.random.default_rng(12)
-    H, O, G = 160, 48, len(counts)
+    O, G, end = 48, len(counts), H // 32 - 1
     base = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
     R = int(base[-1])
     a, w = mx_random(rng, (R, H), -1, 1), mx_random(rng, (G, O, H), -1, 1)
-    a[1][1, 4], a[1][R - 1, 0], w[1][1, 7, 4], w[1][0, 0, 0] = 255, 255, 255, 255
+    a[1][1, end], a[1][R - 1, 0], w[1][1, 7, end], w[1][0, 0, 0] = 255, 255, 255, 255
+    a[1][2 % R, end // 2], w[1][1, 9, end // 2 + 1] = 255, 255  # inside, where waves that share H hand over
     out = moe.moe_mx_product(moe.MxRows(*map(to_dev, a)), moe.MxRows(*map(to_dev, w)), to_dev(base))
     want = oracle.mx_product(oracle.mx_values(*a, E2M1), oracle.mx_values(*w, E2M1), base)
     same_bits(bf16_bits(out), bits(want.astype(np.float32)), "nan blocks")
