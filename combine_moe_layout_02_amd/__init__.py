@@ -860,14 +860,19 @@ class MxRows(NamedTuple):
     scales: torch.Tensor
 
 
+# The current device's index without torch.cuda's lazy initialisation check (tensors on a device exist already).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _launch(dev, stream, fn, *args):
     """fn(*args, stream handle) with dev as the current device: a null stream is the current device's."""
-    index = dev.index
-    if index is None or index == torch.cuda.current_device():
-        _check(fn(*args, _stream(dev, stream)))
+    if dev.index == _current_device():
+        rc = fn(*args, _stream(dev, stream))
     else:
-        with torch.cuda.device(index):
-            _check(fn(*args, _stream(dev, stream)))
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev, stream))
+    if rc:
+        _check(rc)
 
 
 def _out(shape, dtype, dev, stream):
@@ -880,40 +885,71 @@ def _out(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _dense(t, name, dtype, shape, dev):
+    """Checks a contiguous device tensor of exactly this shape; the cheap test first, the reason after."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, dtype, len(shape), dev)
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _matrix(t, name, dtype):
+    """Device and shape of a two-dimensional device tensor of this type, whatever its strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype is not dtype or t.dim() != 2:
+        raise ValueError(f"{name} must be {dtype} with 2 dims, got {t.dtype} {tuple(t.shape)}")
+    return t.device, t.size(0), t.size(1)
+
+
 def _rows_arg(t, name, H, dev):
     """Pointer, row stride in bytes and row count of bf16 rows: a [R, H] tensor whose rows are each
     contiguous, at any stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev:
+    if t.get_device() != dev.index:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[1] != H:
+    if t.dtype is not torch.bfloat16 or t.dim() != 2 or t.size(1) != H:
         raise ValueError(f"{name} must be bfloat16 [rows, {H}], got {t.dtype} {tuple(t.shape)}")
-    if t.shape[0] == 0:
+    n = t.size(0)
+    if n > 1:
+        step, col = t.stride()
+        if col != 1 or step < H:
+            raise ValueError(f"{name} must have contiguous rows that do not overlap")
+        return t.data_ptr(), 2 * step, n
+    if n == 0:
         raise ValueError(f"{name} has no rows")
-    if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < H):
-        raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return _ptr(t), (2 * t.stride(0) if t.shape[0] > 1 else 2 * H), t.shape[0]
+    if t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), 2 * H, 1
 
 
 def _table_args(slot_idx, topk_weights=None):
+    """Device, S and K of the table, with the weights checked against it."""
     _need(slot_idx, "slot_idx", torch.int32, 2)
+    dev, shape = slot_idx.device, slot_idx.shape
     if topk_weights is not None:
-        _need(topk_weights, "topk_weights", torch.float32, 2, slot_idx.device)
-        if topk_weights.shape != slot_idx.shape:
-            raise ValueError("topk_weights must match slot_idx")
-    return slot_idx.shape[0], slot_idx.shape[1], slot_idx.device
+        _dense(topk_weights, "topk_weights", torch.float32, shape, dev)
+    return dev, shape[0], shape[1]
+
+
+def _mx_width(H, format):
+    """Code bytes of a row; the library's error for an H or a format that has none."""
+    if 32 <= H <= 16384 and H % 32 == 0:
+        if format == MOE_MX_E2M1:
+            return H // 2
+        if format == MOE_MX_E4M3:
+            return H
+    return moe_mx_row_bytes(H, format)
 
 
 def _mx_args(mx, name, rows, H, format, dev):
     codes, scales = mx
-    _need(codes, f"{name} codes", torch.uint8, device=dev)
-    _need(scales, f"{name} scales", torch.uint8, device=dev)
-    want = (rows, moe_mx_row_bytes(H, format)), (rows, H // 32)
-    if (tuple(codes.shape), tuple(scales.shape)) != want:
-        raise ValueError(f"{name} must be codes {want[0]} and scales {want[1]}, got {tuple(codes.shape)} and "
-                         f"{tuple(scales.shape)}")
-    return _ptr(codes), _ptr(scales)
+    return (_dense(codes, f"{name}.codes", torch.uint8, (rows, _mx_width(H, format)), dev),
+            _dense(scales, f"{name}.scales", torch.uint8, (rows, H // 32), dev))
 
 
 def _gradient_outs(S, K, H, rows, d_expert_out, d_topk_weights, dev, stream):
@@ -924,10 +960,9 @@ def _gradient_outs(S, K, H, rows, d_expert_out, d_topk_weights, dev, stream):
         raise ValueError(f"d_expert_out must have {rows} rows")
     if d_topk_weights is None:
         d_topk_weights = _out((S, K), torch.float32, dev, stream)
-    _need(d_topk_weights, "d_topk_weights", torch.float32, 2, dev)
-    if tuple(d_topk_weights.shape) != (S, K):
-        raise ValueError(f"d_topk_weights must have shape {(S, K)}")
-    return d_expert_out, d_ptr, d_stride, d_topk_weights
+        return d_expert_out, d_ptr, d_stride, d_topk_weights, d_topk_weights.data_ptr()
+    return (d_expert_out, d_ptr, d_stride, d_topk_weights,
+            _dense(d_topk_weights, "d_topk_weights", torch.float32, (S, K), dev))
 
 
 def moe_combine_backward(dy, expert_out, slot_idx, topk_weights, d_expert_out=None, d_topk_weights=None,
@@ -935,71 +970,59 @@ def moe_combine_backward(dy, expert_out, slot_idx, topk_weights, d_expert_out=No
     """The combine's gradient: (d_expert_out, d_topk_weights) of dy (bf16 [S, H]) with the forward's
     expert_out (bf16 [R, H], any row stride), slot_idx and topk_weights. Rows of d_expert_out that no
     entry names keep their contents (undefined where it is allocated here)."""
-    S, K, dev = _table_args(slot_idx, topk_weights)
-    _need(dy, "dy", torch.bfloat16, 2, dev)
-    H = dy.shape[1]
-    if dy.shape[0] != S:
-        raise ValueError("dy must have one row per token of slot_idx")
+    dev, S, K = _table_args(slot_idx, topk_weights)
+    _, _, H = _matrix(dy, "dy", torch.bfloat16)
+    dy_ptr = _dense(dy, "dy", torch.bfloat16, (S, H), dev)
     ptr, stride, rows = _rows_arg(expert_out, "expert_out", H, dev)
-    d_expert_out, d_ptr, d_stride, d_topk_weights = _gradient_outs(S, K, H, rows, d_expert_out, d_topk_weights,
-                                                                   dev, stream)
-    _launch(dev, stream, _lib.moe_combine_backward, _ptr(dy), ptr, stride, rows, _ptr(slot_idx),
-            _ptr(topk_weights), S, H, K, d_ptr, d_stride, _ptr(d_topk_weights))
+    d_expert_out, d_ptr, d_stride, d_topk_weights, dw_ptr = _gradient_outs(S, K, H, rows, d_expert_out,
+                                                                           d_topk_weights, dev, stream)
+    _launch(dev, stream, _lib.moe_combine_backward, dy_ptr, ptr, stride, rows, slot_idx.data_ptr(),
+            topk_weights.data_ptr(), S, H, K, d_ptr, d_stride, dw_ptr)
     return d_expert_out, d_topk_weights
 
 
 def moe_combine_checkpoint(expert_out, slot_idx, topk_weights, y=None, checkpoint=None, stream=None):
     """moe_combine that also keeps the rows it reads in 8 bits: (y, MxRows in MOE_MX_E4M3 [R, H]). Rows that
     no entry names keep their contents (undefined where the checkpoint is allocated here)."""
-    S, K, dev = _table_args(slot_idx, topk_weights)
-    if not isinstance(expert_out, torch.Tensor) or expert_out.dim() != 2:
-        raise ValueError("expert_out must be a bfloat16 [rows, H] tensor")
-    H = expert_out.shape[1]
+    dev, S, K = _table_args(slot_idx, topk_weights)
+    _, _, H = _matrix(expert_out, "expert_out", torch.bfloat16)
     ptr, stride, rows = _rows_arg(expert_out, "expert_out", H, dev)
     if y is None:
         y = _out((S, H), torch.bfloat16, dev, stream)
-    _need(y, "y", torch.bfloat16, 2, dev)
-    if tuple(y.shape) != (S, H):
-        raise ValueError(f"y must have shape {(S, H)}")
+    y_ptr = _dense(y, "y", torch.bfloat16, (S, H), dev)
     if checkpoint is None:
         checkpoint = _mx_empty(rows, H, MOE_MX_E4M3, dev, stream)
     codes, scales = _mx_args(checkpoint, "checkpoint", rows, H, MOE_MX_E4M3, dev)
-    _launch(dev, stream, _lib.moe_combine_checkpoint, ptr, stride, rows, _ptr(slot_idx), _ptr(topk_weights), S, H,
-            K, _ptr(y), codes, scales)
+    _launch(dev, stream, _lib.moe_combine_checkpoint, ptr, stride, rows, slot_idx.data_ptr(),
+            topk_weights.data_ptr(), S, H, K, y_ptr, codes, scales)
     return y, MxRows(*checkpoint)
 
 
 def moe_combine_backward_mx(dy, checkpoint, slot_idx, topk_weights, d_expert_out=None, d_topk_weights=None,
                             stream=None):
     """moe_combine_backward with the rows of a checkpoint (MxRows in MOE_MX_E4M3) in place of expert_out."""
-    S, K, dev = _table_args(slot_idx, topk_weights)
-    _need(dy, "dy", torch.bfloat16, 2, dev)
-    H = dy.shape[1]
-    if dy.shape[0] != S:
-        raise ValueError("dy must have one row per token of slot_idx")
+    dev, S, K = _table_args(slot_idx, topk_weights)
+    _, _, H = _matrix(dy, "dy", torch.bfloat16)
+    dy_ptr = _dense(dy, "dy", torch.bfloat16, (S, H), dev)
     rows = checkpoint[0].shape[0]
     codes, scales = _mx_args(checkpoint, "checkpoint", rows, H, MOE_MX_E4M3, dev)
-    d_expert_out, d_ptr, d_stride, d_topk_weights = _gradient_outs(S, K, H, rows, d_expert_out, d_topk_weights,
-                                                                   dev, stream)
-    _launch(dev, stream, _lib.moe_combine_backward_mx, _ptr(dy), codes, scales, rows, _ptr(slot_idx),
-            _ptr(topk_weights), S, H, K, d_ptr, d_stride, _ptr(d_topk_weights))
+    d_expert_out, d_ptr, d_stride, d_topk_weights, dw_ptr = _gradient_outs(S, K, H, rows, d_expert_out,
+                                                                           d_topk_weights, dev, stream)
+    _launch(dev, stream, _lib.moe_combine_backward_mx, dy_ptr, codes, scales, rows, slot_idx.data_ptr(),
+            topk_weights.data_ptr(), S, H, K, d_ptr, d_stride, dw_ptr)
     return d_expert_out, d_topk_weights
 
 
 def moe_dispatch_backward(d_rows, slot_idx, dx=None, stream=None):
     """The dispatch's gradient: dx[t] = bf16(sum_k d_rows[slot_idx[t, k]]) of d_rows (bf16 [R, H], any row
     stride), fp32 accumulation."""
-    S, K, dev = _table_args(slot_idx)
-    if not isinstance(d_rows, torch.Tensor) or d_rows.dim() != 2:
-        raise ValueError("d_rows must be a bfloat16 [rows, H] tensor")
-    H = d_rows.shape[1]
+    dev, S, K = _table_args(slot_idx)
+    _, _, H = _matrix(d_rows, "d_rows", torch.bfloat16)
     ptr, stride, rows = _rows_arg(d_rows, "d_rows", H, dev)
     if dx is None:
         dx = _out((S, H), torch.bfloat16, dev, stream)
-    _need(dx, "dx", torch.bfloat16, 2, dev)
-    if tuple(dx.shape) != (S, H):
-        raise ValueError(f"dx must have shape {(S, H)}")
-    _launch(dev, stream, _lib.moe_dispatch_backward, ptr, stride, rows, _ptr(slot_idx), S, H, K, _ptr(dx))
+    dx_ptr = _dense(dx, "dx", torch.bfloat16, (S, H), dev)
+    _launch(dev, stream, _lib.moe_dispatch_backward, ptr, stride, rows, slot_idx.data_ptr(), S, H, K, dx_ptr)
     return dx
 
 
@@ -1011,7 +1034,7 @@ def moe_mx_row_bytes(H, format):
 
 
 def _mx_empty(rows, H, format, dev, stream):
-    return MxRows(_out((rows, moe_mx_row_bytes(H, format)), torch.uint8, dev, stream),
+    return MxRows(_out((rows, _mx_width(H, format)), torch.uint8, dev, stream),
                   _out((rows, H // 32), torch.uint8, dev, stream))
 
 
@@ -1021,32 +1044,30 @@ def _count_arg(num_rows, dev):
     _need(num_rows, "num_rows", torch.int32, device=dev)
     if num_rows.numel() < 1:
         raise ValueError("num_rows must hold a count")
-    return _ptr(num_rows)
+    return num_rows.data_ptr()
 
 
 def moe_mx_quantize(rows, format, num_rows=None, out=None, stream=None):
     """MxRows of bf16 rows [R, H] (any row stride). num_rows: None, or the device count of rows to take (e.g.
     layout.expert_slot_base[E:]); the outputs' other rows keep their contents."""
-    if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
-        raise ValueError("rows must be a bfloat16 [rows, H] tensor")
-    dev, H = rows.device, rows.shape[1]
-    _need(rows[:0], "rows", torch.bfloat16, 2)
+    dev, n, H = _matrix(rows, "rows", torch.bfloat16)
     if out is None:
-        out = _mx_empty(rows.shape[0], H, format, dev, stream)
-    codes, scales = _mx_args(out, "out", rows.shape[0], H, format, dev)
+        out = _mx_empty(n, H, format, dev, stream)
+        codes, scales = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        codes, scales = _mx_args(out, "out", n, H, format, dev)
     count = _count_arg(num_rows, dev)
-    if rows.shape[0]:
-        ptr, stride, n = _rows_arg(rows, "rows", H, dev)
-        _launch(dev, stream, _lib.moe_mx_quantize, ptr, stride, count, n, H, int(format), codes, scales)
+    if n:
+        ptr, stride, _ = _rows_arg(rows, "rows", H, dev)
+        _launch(dev, stream, _lib.moe_mx_quantize, ptr, stride, count, n, H, format, codes, scales)
     return MxRows(*out)
 
 
 def moe_mx_dequantize(mx, format, num_rows=None, out=None, stream=None):
     """The values of MxRows [R, ...] as bf16 rows [R, H] (out: any row stride)."""
-    codes, scales = mx
-    _need(scales, "scales", torch.uint8, 2)
-    dev, n, H = scales.device, scales.shape[0], 32 * scales.shape[1]
-    codes_ptr, scales_ptr = _mx_args(mx, "mx", n, H, format, dev)
+    dev, n, blocks = _matrix(mx[1], "mx.scales", torch.uint8)
+    H = 32 * blocks
+    codes, scales = _mx_args(mx, "mx", n, H, format, dev)
     if out is None:
         out = _out((n, H), torch.bfloat16, dev, stream)
     count = _count_arg(num_rows, dev)
@@ -1054,7 +1075,7 @@ def moe_mx_dequantize(mx, format, num_rows=None, out=None, stream=None):
         ptr, stride, rows = _rows_arg(out, "out", H, dev)
         if rows != n:
             raise ValueError(f"out must have {n} rows")
-        _launch(dev, stream, _lib.moe_mx_dequantize, codes_ptr, scales_ptr, count, n, H, int(format), ptr, stride)
+        _launch(dev, stream, _lib.moe_mx_dequantize, codes, scales, count, n, H, format, ptr, stride)
     return out
 
 
@@ -1063,29 +1084,28 @@ def moe_mx_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=Non
     group g (group_base int32 [G + 1] on the device, e.g. layout.expert_slot_base) gives bf16 [O], or
     [O / 2] of silu(gate) * up with MOE_MX_GATED. Rows outside every group keep their contents (undefined
     where out is allocated here)."""
-    a_codes, a_scales = a
+    dev, n, blocks = _matrix(a[1], "a.scales", torch.uint8)
+    H = 32 * blocks
+    a_codes, a_scales = _mx_args(a, "a", n, H, MOE_MX_E2M1, dev)
     w_codes, w_scales = w
-    _need(a_scales, "a scales", torch.uint8, 2)
-    dev, n, H = a_scales.device, a_scales.shape[0], 32 * a_scales.shape[1]
-    ac, asc = _mx_args(a, "a", n, H, MOE_MX_E2M1, dev)
-    _need(w_codes, "w codes", torch.uint8, 3, dev)
-    _need(w_scales, "w scales", torch.uint8, 3, dev)
-    G, O = w_codes.shape[:2]
-    if tuple(w_codes.shape) != (G, O, H // 2) or tuple(w_scales.shape) != (G, O, H // 32):
-        raise ValueError(f"w must be codes {(G, O, H // 2)} and scales {(G, O, H // 32)}")
-    _need(group_base, "group_base", torch.int32, 1, dev)
-    if group_base.shape[0] != G + 1:
-        raise ValueError(f"group_base must hold {G + 1} values")
-    gated = int(epilogue) == MOE_MX_GATED
-    width = O // 2 if gated else O
+    if not isinstance(w_codes, torch.Tensor) or w_codes.dim() != 3:
+        raise ValueError(f"w must be codes [G, O, {H // 2}] and scales [G, O, {blocks}]")
+    G, O = w_codes.size(0), w_codes.size(1)
+    wc_ptr = _dense(w_codes, "w.codes", torch.uint8, (G, O, H // 2), dev)
+    ws_ptr = _dense(w_scales, "w.scales", torch.uint8, (G, O, blocks), dev)
+    base_ptr = _dense(group_base, "group_base", torch.int32, (G + 1,), dev)
+    width = O // 2 if epilogue == MOE_MX_GATED else O
     if out is None:
         out = _out((n, width), torch.bfloat16, dev, stream)
-    if (not isinstance(out, torch.Tensor) or out.dtype != torch.bfloat16 or out.device != dev
-            or tuple(out.shape) != (n, width)):
-        raise ValueError(f"out must be bfloat16 {(n, width)} on {dev}")
-    if width > 1 and out.stride(1) != 1 or n > 1 and out.stride(0) < width:
-        raise ValueError("out must have contiguous rows that do not overlap")
+        out_stride = 2 * width
+    else:
+        if (not isinstance(out, torch.Tensor) or out.dtype is not torch.bfloat16 or out.get_device() != dev.index
+                or out.shape != (n, width)):
+            raise ValueError(f"out must be bfloat16 {(n, width)} on {dev}")
+        if width > 1 and out.stride(1) != 1 or n > 1 and out.stride(0) < width:
+            raise ValueError("out must have contiguous rows that do not overlap")
+        out_stride = 2 * out.stride(0) if n > 1 else 2 * width
     if n:
-        _launch(dev, stream, _lib.moe_mx_product, ac, asc, n, _ptr(group_base), G, _ptr(w_codes), _ptr(w_scales), O,
-                H, int(epilogue), _ptr(out), 2 * out.stride(0) if n > 1 else 2 * width)
+        _launch(dev, stream, _lib.moe_mx_product, a_codes, a_scales, n, base_ptr, G, wc_ptr, ws_ptr, O, H, epilogue,
+                out.data_ptr(), out_stride)
     return out
