@@ -144,16 +144,19 @@ __device__ inline Tile find_tile(const TileTable &table, int G, int ncol, int t)
 // Tiles of TM rows x TN weight rows (TN / 2 outputs when GATED), WMC x WNC waves, through LDS. A workgroup takes
 // tile after tile; the 8 XCDs get contiguous eighths of the tiles (workgroup b runs on XCD b % 8).
 //
-// Codes go from memory straight to LDS in stages of 128 values (64 bytes of a row) through a ring of four
-// buffers: at each stage the loads of the third stage after it are issued, the next tile's first stages
-// behind a tile's last, so that the loads never pause and a tile's results are stored while the next one's
-// rows arrive. Scales come through registers, 16 blocks (four stages, one round) at a time, and lie in LDS
-// so that one word holds a lane's four scales of a round. One barrier a stage: it follows each wave's wait
-// for its own loads of the stage and for its LDS reads of the last one, so behind it the stage is whole and
-// the buffer of the last stage is free.
-constexpr int kRing = 4;
+// Codes go from memory straight to LDS in pairs of stages of 128 values, 128 bytes of a row (whole lines; stages
+// of 64 bytes through a ring of four took 10% longer where the weights' bytes count), through two buffers: while
+// one is multiplied the other fills, the next tile's first pair behind a tile's last, so that the loads never
+// pause and a tile's results are stored while the next one's rows arrive. Scales come through registers, 16
+// blocks (four stages, one round) at a time, and lie in LDS so that one word holds a lane's four scales of a
+// round. One barrier a pair: it follows each wave's wait for its own loads of the pair and for its LDS reads of
+// the last one, so behind it the pair is whole and the last pair's buffer is free.
+//
+// 32768 rows on 32 groups, 7168 -> 4096 gated: the matrix cores alone take 290 to 350 us on random codes (the
+// card's power holds them at 6.5 PFLOP/s), the loads alone 450, together 650.
 constexpr int kStageBlocks = 4;    // MX blocks of a stage
-constexpr int kScaleBlocks = 16;   // MX blocks of a round of scales: kRing stages
+constexpr int kRoundStages = 4;    // stages of a round: two pairs
+constexpr int kScaleBlocks = 16;   // MX blocks of a round
 
 // Waits until at most N of the wave's loads are in flight and its LDS accesses are done, then for all waves.
 template <int N>
@@ -171,17 +174,16 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     int64_t out_stride, bool wide) {
     constexpr int NW = WMC * WNC, THREADS = 64 * NW;
     constexpr int ROWS = TM + TN, WM = TM / WMC, WN = TN / WNC, MI = WM / 16, NI = WN / 16;
-    constexpr int LOADS = ROWS / 16 / NW;     // 16 rows of a stage a load
-    constexpr int SLOADS = ROWS / THREADS;    // rows of a round of scales a thread
-    constexpr int OF = GATED ? NI / 2 : NI;   // column fragments of results
-    constexpr int STORES = MI * OF / 2;       // stores of a wave, 16 bytes a lane
-    static_assert(LOADS * 16 * NW == ROWS && SLOADS * THREADS == ROWS && kRing == 4, "shape");
-    // the ring's buffers are objects of their own, so that the compiler sees a buffer's reads and another's
-    // loads apart and puts no wait between them
-    __shared__ __align__(1024) uint8_t ring0[ROWS * 64], ring1[ROWS * 64], ring2[ROWS * 64], ring3[ROWS * 64];
-    uint8_t *const codes[kRing] = {ring0, ring1, ring2, ring3};
-    __shared__ __align__(16) uint8_t scales[2][ROWS * 16];
-
+    constexpr int LOADS = ROWS / 8 / NW;                    // 8 rows of a pair of stages a load
+    constexpr int SLOADS = (ROWS + THREADS - 1) / THREADS;  // rows of a round of scales a thread
+    constexpr int OF = GATED ? NI / 2 : NI;                 // column fragments of results
+    constexpr int STORES = MI * OF / 2;                     // stores of a wave, 16 bytes a lane
+    static_assert(LOADS * 8 * NW == ROWS && OF % 2 == 0 && MI * 16 * WMC == TM && NI * 16 * WNC == TN, "shape");
+    // the buffers are objects of their own, so that the compiler sees the reads of one and the loads into the
+    // other apart and puts no wait between them
+    __shared__ __align__(1024) uint8_t pair0[ROWS * 128], pair1[ROWS * 128];
+    uint8_t *const codes[2] = {pair0, pair1};
+    __shared__ __align__(16) uint8_t scales[2][SLOADS * THREADS * 16];  // threads past the rows put the last one again
     __shared__ TileTable table;
 
     const int width = GATED ? O / 2 : O;
@@ -195,15 +197,15 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     int t = (int)(blockIdx.x & 7) * share + (int)(blockIdx.x >> 3);
     if (t >= xcd_end) return;
 
-    // Load l of a wave takes tile rows 16 (wave + l * NW) .. + 15, a lane 16 bytes: place lane % 4 of row lane / 4.
-    // Place p of row r holds block p ^ (r / 2 % 4): eight neighbouring rows' reads of one block then cover all
-    // the banks.
-    const int r4 = lane >> 2, blk = (lane & 3) ^ ((r4 >> 1) & 3);
+    // Load l of a wave takes tile rows 8 (wave + l * NW) .. + 7, a lane 16 bytes: place lane % 8 of row lane / 8.
+    // Place p of row r holds block p ^ (r % 8): eight neighbouring rows' reads of one block then cover all the
+    // banks.
+    const int r8 = lane >> 3, blk = (lane & 7) ^ r8;
 
     // What a thread loads of a tile: its rows' places in the codes and its row(s) of scales.
     struct Source {
         __amdgpu_buffer_rsrc_t a, w;
-        int voff[LOADS];
+        int base[LOADS];  // byte offset of the load's first row, the same for the whole wave
         const uint8_t *scales[SLOADS];
     };
     const auto source_of = [&](const Tile &tile) {
@@ -212,33 +214,34 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
         src.w = rsrc(w_codes + (int64_t)tile.group * O * pitch, (int64_t)O * pitch);
         const int o0 = tile.col * (GATED ? TN / 2 : TN);
         // Row of the weights behind tile row j: plain, neighbours; gated, each wave's share of the tile has its
-        // gate rows first, then the up rows of the same outputs. Rows past the end repeat the last one.
+        // gate rows first, then the up rows of the same outputs. Rows past the matrix read as zero, rows past the
+        // gates are up rows: neither's results are stored.
         const auto weight_row = [&](int j) {
-            if (!GATED) return min(o0 + j, width - 1);
-            const int part = j / WN, jj = j % WN;
-            const int o = min(o0 + part * (WN / 2) + jj % (WN / 2), width - 1);
+            if (!GATED) return o0 + j;
+            const int part = j / WN, jj = j % WN, o = o0 + part * (WN / 2) + jj % (WN / 2);
             return jj < WN / 2 ? o : width + o;
         };
 #pragma unroll
         for (int l = 0; l < LOADS; ++l) {
-            const int r = 16 * (wave + l * NW) + r4;
-            src.voff[l] = (r < TM ? min(r, tile.rows - 1) : weight_row(r - TM)) * pitch + blk * 16;
+            const int r = 8 * (wave + l * NW);
+            src.base[l] = (r < TM ? r : weight_row(r - TM)) * pitch;
         }
 #pragma unroll
         for (int l = 0; l < SLOADS; ++l) {
-            const int r = l * THREADS + tid;
+            const int r = min(l * THREADS + tid, ROWS - 1);
             src.scales[l] = r < TM ? a_scales + ((int64_t)tile.first + min(r, tile.rows - 1)) * nblk
-                                   : w_scales + ((int64_t)tile.group * O + weight_row(r - TM)) * nblk;
+                                   : w_scales + ((int64_t)tile.group * O + min(weight_row(r - TM), O - 1)) * nblk;
         }
         return src;
     };
 
+    const int place = r8 * pitch + blk * 16;
     const auto load_codes = [&](const Source &src, int st, uint8_t *buf, bool none) {
         const bool past = none || st * kStageBlocks + blk >= nblk;  // blocks behind the row's end read as zero
 #pragma unroll
         for (int l = 0; l < LOADS; ++l)
-            load_to_lds(16 * (wave + l * NW) < TM ? src.a : src.w, &buf[(wave + l * NW) * 1024],
-                        past ? 0x7FFFFFF0 : src.voff[l], st * 64);
+            load_to_lds(8 * (wave + l * NW) < TM ? src.a : src.w, &buf[(wave + l * NW) * 1024],
+                        past ? 0x7FFFFFF0 : src.base[l] + place, st * 64);
     };
     u32x4 sreg[SLOADS];
     // A round of a row's scales: 16 bytes. Rounds that end behind the row take its last 16 bytes (nblk >= 16) and
@@ -261,14 +264,13 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
 
     const int wm = (wave % WMC) * WM, wn = TM + (wave / WMC) * WN;
     const int fr = lane & 15, q = lane >> 4;
-    const int at = fr * 64 + (q ^ ((fr >> 1) & 3)) * 16;
-    const int stages = (nblk + kStageBlocks - 1) / kStageBlocks, rounds = (stages + kRing - 1) / kRing;
+    const int at0 = fr * 128 + (q ^ (fr & 7)) * 16, at1 = fr * 128 + ((q + 4) ^ (fr & 7)) * 16;
+    const int stages = (nblk + kStageBlocks - 1) / kStageBlocks, rounds = (stages + kRoundStages - 1) / kRoundStages;
 
     Tile tile = find_tile<TM>(table, G, ncol, t);
     Source cur = source_of(tile);
     load_scales(cur, 0);
-#pragma unroll
-    for (int s = 0; s < kRing - 1; ++s) load_codes(cur, s, codes[s], false);
+    load_codes(cur, 0, codes[0], false);
     int sbuf = 0;         // the scales' buffer of this round
     bool stored = false;  // the stores of the tile before are still in flight, STORES of them
     put_scales(0, 0);
@@ -285,10 +287,12 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
             int as[MI], ws[NI];
             const bool last = round + 1 == rounds;
 #pragma unroll
-            for (int s = 0; s < kRing; ++s) {
-                const int st = round * kRing + s;
-                if (s < kRing - 1 && round == 0 && stored) stage_barrier<(kRing - 2) * LOADS + STORES>();
-                else stage_barrier<(kRing - 2) * LOADS>();
+            for (int s = 0; s < kRoundStages; ++s) {
+                const int st = round * kRoundStages + s;
+                if ((s & 1) == 0) {
+                    if (s == 0 && round == 0 && stored) stage_barrier<STORES>();
+                    else stage_barrier<0>();
+                }
                 if (s == 0) {
 #pragma unroll
                     for (int j = 0; j < NI; ++j)
@@ -299,18 +303,21 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
                 }
                 i32x4 a[MI], w[NI];
 #pragma unroll
-                for (int j = 0; j < NI; ++j) w[j] = *reinterpret_cast<const i32x4 *>(&codes[s][(wn + j * 16) * 64 + at]);
+                for (int j = 0; j < NI; ++j)
+                    w[j] = *reinterpret_cast<const i32x4 *>(&codes[s >> 1][(wn + j * 16) * 128 + (s & 1 ? at1 : at0)]);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) a[i] = *reinterpret_cast<const i32x4 *>(&codes[s][(wm + i * 16) * 64 + at]);
-                // behind the tile's last stage come the next tile's first ones
-                load_codes(cur, s > 0 && last ? s - 1 : st + kRing - 1, codes[(s + kRing - 1) % kRing], s > 0 && last && !more);
+                for (int i = 0; i < MI; ++i)
+                    a[i] = *reinterpret_cast<const i32x4 *>(&codes[s >> 1][(wm + i * 16) * 128 + (s & 1 ? at1 : at0)]);
                 if (s == 0) {
+                    load_codes(cur, st + 2, codes[1], false);
                     if (last && more) {
                         next = find_tile<TM>(table, G, ncol, t);
                         cur = source_of(next);
                     }
                     load_scales(cur, last ? 0 : round + 1);
                 }
+                // behind the tile's last pair comes the next tile's first one
+                if (s == 2) load_codes(cur, last ? 0 : st + 2, codes[0], last && !more);
                 __builtin_amdgcn_sched_barrier(0);  // the reads and loads are under way before the products
                 if (st < stages) {
 #pragma unroll
@@ -326,7 +333,7 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                if (s == kRing - 1) {
+                if (s == kRoundStages - 1) {
                     sbuf ^= 1;
                     put_scales(last ? 0 : round + 1, sbuf);
                 }
@@ -375,13 +382,14 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the wave's end
 }
 
-// Few rows a group: the weights' bytes bound the product. A workgroup takes 16 * MF rows of a group and 32 weight
+// Few rows a group: the weights' bytes bound the product. A workgroup takes 16 rows of a group and 32 weight
 // rows (16 outputs when GATED), its four waves a quarter of H each, and every wave streams its quarter
 // through a ring of its own in LDS, waiting for nobody; the partial sums meet in LDS and are added in the
 // waves' order. LDS turns the loads' order (four lanes to a row, 64 bytes) into the matrix cores' (a lane
 // to a row): loaded straight to registers in their order, each lane's 16 bytes are an access of the L1 of
 // their own, and 8 rows on 32 groups, H = 7168, O = 4096, took 32 us.
 constexpr int kSmallWaves = 4;
+constexpr int kRing = 4;  // buffers of a wave's ring, of 128 values each
 
 // Bytes `from` .. + 15 of a row of n, zero behind its end: loaded now, put in place later, so that nothing waits
 // here. A row's last 16 bytes at the latest are loaded, and moved down when placed; SHORT rows (n < 16) go byte
@@ -407,20 +415,20 @@ __device__ inline u32x4 place_row16(const u32x4 &v, int from, int n) {
     return __builtin_bit_cast(u32x4, down == 0 ? wide : down >= 16 ? 0 : wide >> (8 * down));
 }
 
-template <int MF, bool GATED, bool SHORT>
+template <bool GATED, bool SHORT>
 __global__ __launch_bounds__(64 * kSmallWaves) void product_small_kernel(
     const uint8_t *__restrict__ a_codes, const uint8_t *__restrict__ a_scales, int64_t a_rows,
     const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
     const uint8_t *__restrict__ w_scales, int O, int nblk, int row_tiles, uint8_t *__restrict__ out,
     int64_t out_stride) {
-    constexpr int F = MF + 2, ROWS = 16 * F;  // at most 64; fragments of 16 rows: the rows, then two of the weights
+    constexpr int F = 3, ROWS = 16 * F;  // fragments of 16 rows: the rows, then two of the weights
     __shared__ __align__(1024) uint8_t ring0[kSmallWaves][F * 1024], ring1[kSmallWaves][F * 1024], ring2[kSmallWaves][F * 1024],
         ring3[kSmallWaves][F * 1024];
     __shared__ __align__(16) uint8_t scales[kSmallWaves][64 * 16];  // a lane puts a row, the last lanes one again
     int g;
     int64_t first, last;
     const int col = blockIdx.x / row_tiles;
-    if (!find_rows<16 * MF>(base, G, a_rows, blockIdx.x - col * row_tiles, g, first, last)) return;
+    if (!find_rows<16>(base, G, a_rows, blockIdx.x - col * row_tiles, g, first, last)) return;
     g = __builtin_amdgcn_readfirstlane(g);
     first = __builtin_amdgcn_readfirstlane((int)first);
     last = __builtin_amdgcn_readfirstlane((int)last);
@@ -433,8 +441,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void product_small_kernel(
     const __amdgpu_buffer_rsrc_t w_src = rsrc(w_codes + (int64_t)g * O * pitch, (int64_t)O * pitch);
     // row r of the tile's ROWS, in its own matrix; rows past the end repeat the last one
     const auto row_of = [&](int r) {
-        if (r < 16 * MF) return min(r, rows - 1);
-        const int j = r - 16 * MF;
+        if (r < 16) return min(r, rows - 1);
+        const int j = r - 16;
         return GATED ? min(o0 + (j & 15), width - 1) + (j >> 4) * width : min(o0 + j, width - 1);
     };
     const int r4 = lane >> 2, blk = (lane & 3) ^ ((r4 >> 1) & 3);  // as in the tiles above
@@ -449,15 +457,13 @@ __global__ __launch_bounds__(64 * kSmallWaves) void product_small_kernel(
         const bool past = i >= count || (begin + i) * kStageBlocks + blk >= nblk;
 #pragma unroll
         for (int f = 0; f < F; ++f)
-            load_to_lds(f < MF ? a_src : w_src, &buf[f * 1024], past ? 0x7FFFFFF0 : voff[f], (begin + i) * 64);
+            load_to_lds(f == 0 ? a_src : w_src, &buf[f * 1024], past ? 0x7FFFFFF0 : voff[f], (begin + i) * 64);
     };
     const int srow_at = min(lane, ROWS - 1);
-    const uint8_t *srow = srow_at < 16 * MF ? a_scales + (first + row_of(srow_at)) * nblk
-                                            : w_scales + ((int64_t)g * O + row_of(srow_at)) * nblk;
+    const uint8_t *srow = srow_at < 16 ? a_scales + (first + row_of(srow_at)) * nblk
+                                       : w_scales + ((int64_t)g * O + row_of(srow_at)) * nblk;
 
-    f32x4 acc[MF][2];
-#pragma unroll
-    for (int i = 0; i < MF; ++i) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
     u32x4 sreg = load_row16<SHORT>(srow, begin * kStageBlocks, nblk);
 #pragma unroll
     for (int s = 0; s < kRing - 1; ++s) load_codes(s, codes[s]);
@@ -482,15 +488,13 @@ __global__ __launch_bounds__(64 * kSmallWaves) void product_small_kernel(
             for (int f = 0; f < F; ++f) v[f] = *reinterpret_cast<const i32x4 *>(&codes[s][f * 1024 + at]);
             if (i0 + s < count) {  // behind them the codes are zero, but a scale may be a NaN
 #pragma unroll
-                for (int i = 0; i < MF; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        f32x4 &c = acc[i][j];
-                        if (s == 0) c = mfma_byte<0>(v[MF + j], sc[MF + j], v[i], sc[i], c);
-                        else if (s == 1) c = mfma_byte<1>(v[MF + j], sc[MF + j], v[i], sc[i], c);
-                        else if (s == 2) c = mfma_byte<2>(v[MF + j], sc[MF + j], v[i], sc[i], c);
-                        else c = mfma_byte<3>(v[MF + j], sc[MF + j], v[i], sc[i], c);
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    f32x4 &c = acc[j];
+                    if (s == 0) c = mfma_byte<0>(v[1 + j], sc[1 + j], v[0], sc[0], c);
+                    else if (s == 1) c = mfma_byte<1>(v[1 + j], sc[1 + j], v[0], sc[0], c);
+                    else if (s == 2) c = mfma_byte<2>(v[1 + j], sc[1 + j], v[0], sc[0], c);
+                    else c = mfma_byte<3>(v[1 + j], sc[1 + j], v[0], sc[0], c);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
             if (s == kRing - 1) put_scales(i0 + kRing);
@@ -501,37 +505,32 @@ __global__ __launch_bounds__(64 * kSmallWaves) void product_small_kernel(
     __syncthreads();
     f32x4 *const partial = reinterpret_cast<f32x4 *>(&ring0[0][0]);  // [wave][fragment][lane]
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) partial[(wave * 2 * MF + i * 2 + j) * 64 + lane] = acc[i][j];
+    for (int j = 0; j < 2; ++j) partial[(wave * 2 + j) * 64 + lane] = acc[j];
     __syncthreads();
-    // a wave for each fragment of results
-    for (int f = wave; f < (GATED ? MF : 2 * MF); f += kSmallWaves) {
-        const int i = GATED ? f : f >> 1;
-        f32x4 sum = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+    // the first wave adds and stores gate and up, the first two a fragment each of a plain product
+    if (wave >= (GATED ? 1 : 2)) return;
+    f32x4 sum = {0, 0, 0, 0}, up = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < kSmallWaves; ++k) {
-            sum += partial[(k * 2 * MF + (GATED ? 2 * f : f)) * 64 + lane];
-            if (GATED) up += partial[(k * 2 * MF + 2 * f + 1) * 64 + lane];
-        }
-        if (16 * i + fr >= rows) continue;
-        uint16_t *dst = reinterpret_cast<uint16_t *>(out + (first + 16 * i + fr) * out_stride);
+    for (int k = 0; k < kSmallWaves; ++k) {
+        sum += partial[(k * 2 + wave) * 64 + lane];
+        if (GATED) up += partial[(k * 2 + 1) * 64 + lane];
+    }
+    if (fr >= rows) return;
+    uint16_t *dst = reinterpret_cast<uint16_t *>(out + (first + fr) * out_stride);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int o = o0 + (GATED ? 0 : 16 * (f & 1)) + 4 * q + e;
-            if (o < width) dst[o] = (uint16_t)bf16_pair(GATED ? silu(sum[e]) * up[e] : sum[e], 0.0f);
-        }
+    for (int e = 0; e < 4; ++e) {
+        const int o = o0 + 16 * wave + 4 * q + e;
+        if (o < width) dst[o] = (uint16_t)bf16_pair(GATED ? silu(sum[e]) * up[e] : sum[e], 0.0f);
     }
 }
 
-template <int MF>
 hipError_t few_rows(const void *a_codes, const void *a_scales, int64_t a_rows, const int32_t *group_base,
                     int32_t G, const void *w_codes, const void *w_scales, int32_t O, int32_t H, bool gated,
                     void *out, int64_t out_stride, hipStream_t stream) {
-    const int64_t row_tiles = a_rows / (16 * MF) + (a_rows < G ? a_rows : G);
+    const int64_t row_tiles = a_rows / 16 + (a_rows < G ? a_rows : G);  // at most
     const int ncol = gated ? (O / 2 + 15) / 16 : (O + 31) / 32;
-    auto *kernel = H >= 512 ? (gated ? product_small_kernel<MF, true, false> : product_small_kernel<MF, false, false>)
-                            : (gated ? product_small_kernel<MF, true, true> : product_small_kernel<MF, false, true>);
+    auto *kernel = H >= 512 ? (gated ? product_small_kernel<true, false> : product_small_kernel<false, false>)
+                            : (gated ? product_small_kernel<true, true> : product_small_kernel<false, true>);
     hipLaunchKernelGGL(kernel, dim3((uint32_t)(row_tiles * ncol)), dim3(64 * kSmallWaves), 0, stream,
                        static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales), a_rows,
                        group_base, G, static_cast<const uint8_t *>(w_codes),
@@ -570,18 +569,32 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
     // rows of whole 16-byte pieces, and a tile of them within a buffer descriptor's range
     const bool wide = width % 8 == 0 && out_stride_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                       out_stride_bytes <= (1 << 22);
-    const int64_t mean = a_rows / G;
-    if (mean >= 192 && H >= 512)
+    // Which kernel, by the work it would have if the rows were spread evenly over as many groups as they can
+    // reach. Measured with G = 32, weights from memory (us; 7168 -> 4096 gated, 2048 -> 7168 plain):
+    //   rows a group     16           64           128          256          1024
+    //   64 x 128         90.7, 49.3   128, 68.2    189, 95.6    321, 170     947, 564
+    //   128 x 128        96.1, 52.4   109, 60.3    152, 80.6    248, 142     748, 470
+    //   256 x 256                     137, 80.1    161, 87.3    233, 146     629, 396
+    // A tile is also the least that one workgroup can do, at H = 7168 19, 23 and 47 us, so a product of few tiles
+    // takes smaller ones (16 groups, 3001 rows, 1056 -> 1000: 9.9, 11.8, 15.1 us). With only a few hundred tiles
+    // of 64 x 128 the weights are better read by four waves a 16 rows each (few_rows): 8 rows on 32 groups, 7168 ->
+    // 4096, 24.7 against 30.2 us, 16 rows 43.2 against 40.8, where its workgroups exceed what runs at once.
+    const int64_t hit = a_rows < G ? a_rows : G, mean = (a_rows + hit - 1) / hit;
+    const auto tiles_of = [&](int tm, int tn) {
+        const int outs = gated ? tn / 2 : tn;
+        return hit * ((mean + tm - 1) / tm) * ((width + outs - 1) / outs);
+    };
+    if (H < 512 || tiles_of(16, 32) * ((mean < 16 ? mean : 16) + 32) <= 1024 * 33)
+        return few_rows(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                        out_stride_bytes, stream);
+    if (mean >= 160 && tiles_of(256, 256) >= 192)
         return tiles<256, 256, 2, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
-                               out_stride_bytes, wide, 256, stream);
-    if (mean >= 32 && H >= 512)
+                                     out_stride_bytes, wide, 256, stream);
+    if (mean >= 40 && tiles_of(128, 128) >= 192)
         return tiles<128, 128, 2, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
-                               out_stride_bytes, wide, 512, stream);
-    if (mean >= 8)
-        return few_rows<2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
-                           out_stride_bytes, stream);
-    return few_rows<1>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
-                       out_stride_bytes, stream);
+                                     out_stride_bytes, wide, 512, stream);
+    return tiles<64, 128, 2, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                out_stride_bytes, wide, 512, stream);
 }
 
 }  // namespace moe

@@ -336,7 +336,10 @@ def product_case(moe, rng, counts, H, O, gated, low=-1, high=1, behind=0, before
 PRODUCTS = [  # rows of each group, H, O
     ([1], 32, 1), ([1], 32, 2), ([3, 0, 1], 64, 16), ([0, 0, 5], 96, 18), ([16, 17, 15], 128, 64), ([0, 33, 0, 1, 0], 160, 100),
     ([130, 7], 288, 130), ([256, 255, 257], 256, 256), ([1] * 40, 512, 72), ([300], 1056, 1000), ([2, 600, 61], 544, 322),
-    ([8] * 3, 7168, 258), ([9] * 5, 7168, 96), ([20, 3, 0, 31], 512, 66), ([12, 40], 736, 32), ([1, 2], 480, 48), ([65, 0, 64, 63], 2048, 510), ([5, 1, 0, 2], 7168, 130), ([40] * 20, 608, 90), ([513, 0, 1023], 992, 514),
+    ([8] * 3, 7168, 258), ([9] * 5, 7168, 96), ([20, 3, 0, 31], 512, 66), ([12, 40], 736, 32), ([1, 2], 480, 48),
+    ([200, 170, 300, 0] * 4, 512, 4100),
+    ([200, 170, 300, 0] * 4, 1056, 4100), ([50] * 30, 544, 2500), ([300, 90, 0, 260] * 8, 512, 300), ([7] * 64, 544, 1500),
+    ([7] * 64, 1024, 700), ([1000], 768, 6200), ([65, 0, 64, 63], 2048, 510), ([5, 1, 0, 2], 7168, 130), ([40] * 20, 608, 90), ([513, 0, 1023], 992, 514),
 ]
 
 
