@@ -905,13 +905,22 @@ def _matrix(t, name, dtype):
     return t.device, t.size(0), t.size(1)
 
 
+def _width(t, name):
+    """The row length of a two-dimensional tensor; type and device are checked with the rest of it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
+    return t.size(1)
+
+
 def _rows_arg(t, name, H, dev):
     """Pointer, row stride in bytes and row count of bf16 rows: a [R, H] tensor whose rows are each
     contiguous, at any stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != dev.index:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        raise ValueError(f"{name} must be a device tensor on {dev}, got {t.device}")
     if t.dtype is not torch.bfloat16 or t.dim() != 2 or t.size(1) != H:
         raise ValueError(f"{name} must be bfloat16 [rows, {H}], got {t.dtype} {tuple(t.shape)}")
     n = t.size(0)
@@ -952,14 +961,17 @@ def _mx_args(mx, name, rows, H, format, dev):
             _dense(scales, f"{name}.scales", torch.uint8, (rows, H // 32), dev))
 
 
-def _gradient_outs(S, K, H, rows, d_expert_out, d_topk_weights, dev, stream):
+def _gradient_outs(S, K, H, rows, topk_weights, d_expert_out, d_topk_weights, dev, stream):
     if d_expert_out is None:
         d_expert_out = _out((rows, H), torch.bfloat16, dev, stream)
     d_ptr, d_stride, d_count = _rows_arg(d_expert_out, "d_expert_out", H, dev)
     if d_count != rows:
         raise ValueError(f"d_expert_out must have {rows} rows")
     if d_topk_weights is None:
-        d_topk_weights = _out((S, K), torch.float32, dev, stream)
+        if stream is None:
+            d_topk_weights = torch.empty_like(topk_weights)
+        else:
+            d_topk_weights = _out((S, K), torch.float32, dev, stream)
         return d_expert_out, d_ptr, d_stride, d_topk_weights, d_topk_weights.data_ptr()
     return (d_expert_out, d_ptr, d_stride, d_topk_weights,
             _dense(d_topk_weights, "d_topk_weights", torch.float32, (S, K), dev))
@@ -971,11 +983,11 @@ def moe_combine_backward(dy, expert_out, slot_idx, topk_weights, d_expert_out=No
     expert_out (bf16 [R, H], any row stride), slot_idx and topk_weights. Rows of d_expert_out that no
     entry names keep their contents (undefined where it is allocated here)."""
     dev, S, K = _table_args(slot_idx, topk_weights)
-    _, _, H = _matrix(dy, "dy", torch.bfloat16)
+    H = _width(dy, "dy")
     dy_ptr = _dense(dy, "dy", torch.bfloat16, (S, H), dev)
     ptr, stride, rows = _rows_arg(expert_out, "expert_out", H, dev)
-    d_expert_out, d_ptr, d_stride, d_topk_weights, dw_ptr = _gradient_outs(S, K, H, rows, d_expert_out,
-                                                                           d_topk_weights, dev, stream)
+    d_expert_out, d_ptr, d_stride, d_topk_weights, dw_ptr = _gradient_outs(S, K, H, rows, topk_weights,
+                                                                           d_expert_out, d_topk_weights, dev, stream)
     _launch(dev, stream, _lib.moe_combine_backward, dy_ptr, ptr, stride, rows, slot_idx.data_ptr(),
             topk_weights.data_ptr(), S, H, K, d_ptr, d_stride, dw_ptr)
     return d_expert_out, d_topk_weights
@@ -985,7 +997,7 @@ def moe_combine_checkpoint(expert_out, slot_idx, topk_weights, y=None, checkpoin
     """moe_combine that also keeps the rows it reads in 8 bits: (y, MxRows in MOE_MX_E4M3 [R, H]). Rows that
     no entry names keep their contents (undefined where the checkpoint is allocated here)."""
     dev, S, K = _table_args(slot_idx, topk_weights)
-    _, _, H = _matrix(expert_out, "expert_out", torch.bfloat16)
+    H = _width(expert_out, "expert_out")
     ptr, stride, rows = _rows_arg(expert_out, "expert_out", H, dev)
     if y is None:
         y = _out((S, H), torch.bfloat16, dev, stream)
@@ -1002,12 +1014,12 @@ def moe_combine_backward_mx(dy, checkpoint, slot_idx, topk_weights, d_expert_out
                             stream=None):
     """moe_combine_backward with the rows of a checkpoint (MxRows in MOE_MX_E4M3) in place of expert_out."""
     dev, S, K = _table_args(slot_idx, topk_weights)
-    _, _, H = _matrix(dy, "dy", torch.bfloat16)
+    H = _width(dy, "dy")
     dy_ptr = _dense(dy, "dy", torch.bfloat16, (S, H), dev)
     rows = checkpoint[0].shape[0]
     codes, scales = _mx_args(checkpoint, "checkpoint", rows, H, MOE_MX_E4M3, dev)
-    d_expert_out, d_ptr, d_stride, d_topk_weights, dw_ptr = _gradient_outs(S, K, H, rows, d_expert_out,
-                                                                           d_topk_weights, dev, stream)
+    d_expert_out, d_ptr, d_stride, d_topk_weights, dw_ptr = _gradient_outs(S, K, H, rows, topk_weights,
+                                                                           d_expert_out, d_topk_weights, dev, stream)
     _launch(dev, stream, _lib.moe_combine_backward_mx, dy_ptr, codes, scales, rows, slot_idx.data_ptr(),
             topk_weights.data_ptr(), S, H, K, d_ptr, d_stride, dw_ptr)
     return d_expert_out, d_topk_weights
@@ -1017,7 +1029,7 @@ def moe_dispatch_backward(d_rows, slot_idx, dx=None, stream=None):
     """The dispatch's gradient: dx[t] = bf16(sum_k d_rows[slot_idx[t, k]]) of d_rows (bf16 [R, H], any row
     stride), fp32 accumulation."""
     dev, S, K = _table_args(slot_idx)
-    _, _, H = _matrix(d_rows, "d_rows", torch.bfloat16)
+    H = _width(d_rows, "d_rows")
     ptr, stride, rows = _rows_arg(d_rows, "d_rows", H, dev)
     if dx is None:
         dx = _out((S, H), torch.bfloat16, dev, stream)
