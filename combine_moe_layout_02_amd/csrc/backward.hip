@@ -4,7 +4,13 @@
 //   d row(s) = w[t,k] * g      and      d w[t,k] = <g, row(s)>,
 // so one pass over a token's K rows reads them once (bf16, or E4M3 blocks kept by the forward) and writes
 // K gradient rows. The dispatch copies x[t] to K rows, so its gradient is their sum.
-// All of it is HBM traffic with a few operations a value.
+//
+// All of it is HBM traffic with a few operations a value. What bounds it is that the rows of a token lie all
+// over the buffers: with rows in token order instead the combine's gradient took 180 us for 998 MB (S = 4096,
+// H = 7168, K = 8) instead of 213, the checkpointed combine 145 instead of 164. Two ways to visit the rows in
+// slot order, through an inverse of slot_idx that a first kernel writes, came to 196 us (a workgroup a row) and
+// 205 us (a workgroup a quarter row, sums joined by a third kernel): the gain is spent on the second read of
+// dy for every row, the chain from slot to token to dy, and the launches; a call would need a workspace too.
 
 #include "mx_blocks.h"
 
@@ -16,7 +22,10 @@ using namespace mx;
 constexpr int kLoadPolicy = 2;              // nt: rows are read once
 constexpr int kStorePolicy = 1 | 16;        // sc0 sc1
 constexpr int kStreamPolicy = 1 | 16 | 2;   // sc0 sc1 nt: rows stream to HBM
-constexpr int kPartThreads = 32;            // 16-byte vectors of a part (checkpoint, dispatch gradient)
+// 16-byte vectors of a part, a lane each. S = 4096, H = 7168, K = 8: the dispatch's gradient takes 87.9 us with
+// 32, 89.1 with 64 and 90.2 with 128; the checkpointed combine 164, 153 and 153 (a row's codes are half as wide).
+template <bool KEEP>
+constexpr int part_threads() { return KEEP ? 64 : 32; }
 
 __device__ inline __amdgpu_buffer_rsrc_t rsrc(const void *base, int32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
@@ -45,7 +54,10 @@ __device__ inline float wave_sums(float (&v)[N]) {
 }
 
 // grid = S; workgroup t takes token t, its lanes vectors threadIdx.x, + blockDim.x, ... of the rows (at most
-// two rounds: nvec <= 2048 and 1024 lanes). MX: the rows are E4M3 codes and scales (stride = H).
+// two rounds: nvec <= 2048 and 1024 lanes; a lane a vector where they suffice, so that all of a token's loads are
+// under way at once: 214 us at S = 4096, H = 7168, K = 8, as with 128, 256 or 512 lanes and more rounds, 211 to 214).
+// MX: the rows are E4M3 codes and scales (stride = H). d_weights: a lane's sum over its values in order, the wave's
+// lanes by a fixed tree, the waves in order, all in fp32.
 template <int KMAX, bool MX>
 __global__ __launch_bounds__(1024) void combine_backward_kernel(
     const uint8_t *__restrict__ dy, const uint8_t *__restrict__ rows, const uint8_t *__restrict__ scales,
@@ -130,7 +142,7 @@ __global__ __launch_bounds__(1024) void combine_backward_kernel(
 //   KEEP = true:  y[t] = the weighted sum, each product and each sum rounded to fp32 on its own as in the
 //                 combine (this file is compiled with -ffp-contract=off), and the rows' E4M3 blocks.
 template <int KMAX, bool KEEP>
-__global__ __launch_bounds__(kPartThreads) void gather_kernel(
+__global__ __launch_bounds__(part_threads<KEEP>()) void gather_kernel(
     const uint8_t *__restrict__ rows, int64_t stride, int64_t nrows,
     const int32_t *__restrict__ slot_idx, const float *__restrict__ weights, int S, int K, int nvec,
     int nparts, uint8_t *__restrict__ out, uint8_t *__restrict__ codes,
@@ -140,7 +152,7 @@ __global__ __launch_bounds__(kPartThreads) void gather_kernel(
     const int q = m - i * nparts;
     const int64_t t = 8 * i + (blockIdx.x & 7);
     if (t >= S) return;
-    const int v = q * kPartThreads + threadIdx.x;
+    const int v = q * part_threads<KEEP>() + threadIdx.x;
     const int row_bytes = nvec << 4;
     int64_t slot[KMAX];
     float w[KMAX];
@@ -216,9 +228,10 @@ hipError_t gather(const void *rows, int64_t stride, int64_t nrows, const int32_t
                   const float *weights, int S, int H, int K, void *out, void *codes, void *scales,
                   hipStream_t stream) {
     const int nvec = H / 8;
-    const int nparts = (nvec + kPartThreads - 1) / kPartThreads;
+    constexpr int lanes = part_threads<KEEP>();
+    const int nparts = (nvec + lanes - 1) / lanes;
     const uint32_t grid = 8u * (uint32_t)((S + 7) / 8) * (uint32_t)nparts;
-    hipLaunchKernelGGL((gather_kernel<KMAX, KEEP>), dim3(grid), dim3(kPartThreads), 0, stream,
+    hipLaunchKernelGGL((gather_kernel<KMAX, KEEP>), dim3(grid), dim3(lanes), 0, stream,
                        static_cast<const uint8_t *>(rows), stride, nrows, slot_idx, weights, S, K, nvec,
                        nparts, static_cast<uint8_t *>(out), static_cast<uint8_t *>(codes),
                        static_cast<uint8_t *>(scales));
