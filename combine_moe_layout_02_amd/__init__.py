@@ -880,7 +880,7 @@ def _out(shape, dtype, dev, stream):
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
@@ -1016,7 +1016,7 @@ def moe_combine_backward_mx(dy, checkpoint, slot_idx, topk_weights, d_expert_out
     dev, S, K = _table_args(slot_idx, topk_weights)
     H = _width(dy, "dy")
     dy_ptr = _dense(dy, "dy", torch.bfloat16, (S, H), dev)
-    rows = checkpoint[0].shape[0]
+    _, rows, _ = _matrix(checkpoint[1], "checkpoint.scales", torch.uint8)
     codes, scales = _mx_args(checkpoint, "checkpoint", rows, H, MOE_MX_E4M3, dev)
     d_expert_out, d_ptr, d_stride, d_topk_weights, dw_ptr = _gradient_outs(S, K, H, rows, topk_weights,
                                                                            d_expert_out, d_topk_weights, dev, stream)

@@ -86,32 +86,66 @@ __device__ inline u32x4 transpose_bytes(const u32x4 &m) {
                  __builtin_amdgcn_perm(hi23, hi01, 0x05040100), __builtin_amdgcn_perm(hi23, hi01, 0x07060302)};
 }
 
+// Bytes `from` .. + 15 of a row of n, zero behind its end: loaded now, put in place later, so that nothing waits
+// here. A row's last 16 bytes at the latest are loaded, and moved down when placed; SHORT rows (n < 16) go byte
+// by byte.
+template <bool SHORT>
+__device__ inline u32x4 load_row16(const uint8_t *row, int from, int n) {
+    u32x4 v = {0, 0, 0, 0};
+    if constexpr (!SHORT) {
+        __builtin_memcpy(&v, row + min(from, n - 16), 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (from + i < n) v[i >> 2] |= (uint32_t)row[from + i] << (8 * (i & 3));
+    }
+    return v;
+}
+
+template <bool SHORT>
+__device__ inline u32x4 place_row16(const u32x4 &v, int from, int n) {
+    if constexpr (SHORT) return v;
+    const int down = max(from - (n - 16), 0);
+    const unsigned __int128 wide = __builtin_bit_cast(unsigned __int128, v);
+    return __builtin_bit_cast(u32x4, down == 0 ? wide : down >= 16 ? 0 : wide >> (8 * down));
+}
+
 // The groups' rows and tiles, in LDS: rows [lo, hi) of group g, and the number of row tiles up to its end.
 struct TileTable {
     int32_t lo[MOE_MAX_EXPERTS], hi[MOE_MAX_EXPERTS], end[MOE_MAX_EXPERTS];
 };
 
-// One wave fills the table for row tiles of TM.
+// One wave fills the table for row tiles of TM. A base below an earlier one counts as that one, so that the
+// groups' rows are disjoint and their tiles as many as the grid's arithmetic assumes, whatever the bases are.
 template <int TM>
 __device__ inline void fill_table(TileTable &table, const int32_t *__restrict__ base, int G, int64_t a_rows) {
     const int lane = threadIdx.x & 63;
-    int before = 0;
+    int before = 0, reached = 0;
     for (int g0 = 0; g0 < G; g0 += 64) {
         const int g = g0 + lane;
-        int64_t lo = 0, hi = 0;
+        int lo = 0, hi = 0;
         if (g < G) {
-            lo = min(max((int64_t)base[g], (int64_t)0), a_rows);
-            hi = min(max((int64_t)base[g + 1], lo), a_rows);
+            lo = min(max(base[g], 0), (int)a_rows);
+            hi = min(max(base[g + 1], lo), (int)a_rows);
         }
-        int incl = (int)((hi - lo + TM - 1) / TM);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int u = __shfl_up(hi, d, 64);
+            if (lane >= d) hi = max(hi, u);
+        }
+        hi = max(hi, reached);
+        const int prev = __shfl_up(hi, 1, 64);
+        lo = max(lo, lane > 0 ? prev : reached);
+        reached = __shfl(hi, 63, 64);
+        int incl = (hi - lo + TM - 1) / TM;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int u = __shfl_up(incl, d, 64);
             if (lane >= d) incl += u;
         }
         if (g < G) {
-            table.lo[g] = (int)lo;
-            table.hi[g] = (int)hi;
+            table.lo[g] = lo;
+            table.hi[g] = hi;
             table.end[g] = before + incl;
         }
         before += __shfl(incl, 63, 64);
@@ -166,7 +200,7 @@ __device__ inline void stage_barrier() {
     asm volatile("" ::: "memory");
 }
 
-template <int TM, int TN, int WMC, int WNC, bool GATED>
+template <int TM, int TN, int WMC, int WNC, bool GATED, bool SHORT>
 __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     const uint8_t *__restrict__ a_codes, const uint8_t *__restrict__ a_scales, int64_t a_rows,
     const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
@@ -243,23 +277,17 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
             load_to_lds(8 * (wave + l * NW) < TM ? src.a : src.w, &buf[(wave + l * NW) * 1024],
                         past ? 0x7FFFFFF0 : src.base[l] + place, st * 64);
     };
-    u32x4 sreg[SLOADS];
-    // A round of a row's scales: 16 bytes. Rounds that end behind the row take its last 16 bytes (nblk >= 16) and
-    // are moved down when put, so that blocks behind the end have scale byte 0.
+    u32x4 sreg[SLOADS];  // a round of the rows' scales, 16 bytes each
     const auto load_scales = [&](const Source &src, int round) {
-        const int from = min(round * kScaleBlocks, nblk - kScaleBlocks);
 #pragma unroll
-        for (int l = 0; l < SLOADS; ++l) __builtin_memcpy(&sreg[l], src.scales[l] + from, 16);
+        for (int l = 0; l < SLOADS; ++l) sreg[l] = load_row16<SHORT>(src.scales[l], round * kScaleBlocks, nblk);
     };
     // Put as [row][lane's k-block q][stage of the round]: the transpose of the row's 4 x 4 bytes.
     const auto put_scales = [&](int round, int buf) {
-        const int down = max(round * kScaleBlocks - (nblk - kScaleBlocks), 0);  // < 16
 #pragma unroll
-        for (int l = 0; l < SLOADS; ++l) {
-            const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, sreg[l]);
-            const u32x4 m = __builtin_bit_cast(u32x4, down == 0 ? v : v >> (8 * down));
-            *reinterpret_cast<u32x4 *>(&scales[buf][(l * THREADS + tid) * 16]) = transpose_bytes(m);
-        }
+        for (int l = 0; l < SLOADS; ++l)
+            *reinterpret_cast<u32x4 *>(&scales[buf][(l * THREADS + tid) * 16]) =
+                transpose_bytes(place_row16<SHORT>(sreg[l], round * kScaleBlocks, nblk));
     };
 
     const int wm = (wave % WMC) * WM, wn = TM + (wave / WMC) * WN;
@@ -391,44 +419,19 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
 constexpr int kSmallWaves = 4;
 constexpr int kRing = 4;  // buffers of a wave's ring, of 128 values each
 
-// Bytes `from` .. + 15 of a row of n, zero behind its end: loaded now, put in place later, so that nothing waits
-// here. A row's last 16 bytes at the latest are loaded, and moved down when placed; SHORT rows (n < 16) go byte
-// by byte.
-template <bool SHORT>
-__device__ inline u32x4 load_row16(const uint8_t *row, int from, int n) {
-    u32x4 v = {0, 0, 0, 0};
-    if constexpr (!SHORT) {
-        __builtin_memcpy(&v, row + min(from, n - 16), 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (from + i < n) v[i >> 2] |= (uint32_t)row[from + i] << (8 * (i & 3));
-    }
-    return v;
-}
-
-template <bool SHORT>
-__device__ inline u32x4 place_row16(const u32x4 &v, int from, int n) {
-    if constexpr (SHORT) return v;
-    const int down = max(from - (n - 16), 0);
-    const unsigned __int128 wide = __builtin_bit_cast(unsigned __int128, v);
-    return __builtin_bit_cast(u32x4, down == 0 ? wide : down >= 16 ? 0 : wide >> (8 * down));
-}
-
 template <bool GATED, bool SHORT>
 __global__ __launch_bounds__(64 * kSmallWaves) void product_small_kernel(
     const uint8_t *__restrict__ a_codes, const uint8_t *__restrict__ a_scales, int64_t a_rows,
     const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
-    const uint8_t *__restrict__ w_scales, int O, int nblk, int row_tiles, uint8_t *__restrict__ out,
-    int64_t out_stride) {
+    const uint8_t *__restrict__ w_scales, int O, int nblk, uint8_t *__restrict__ out, int64_t out_stride) {
     constexpr int F = 3, ROWS = 16 * F;  // fragments of 16 rows: the rows, then two of the weights
     __shared__ __align__(1024) uint8_t ring0[kSmallWaves][F * 1024], ring1[kSmallWaves][F * 1024], ring2[kSmallWaves][F * 1024],
         ring3[kSmallWaves][F * 1024];
     __shared__ __align__(16) uint8_t scales[kSmallWaves][64 * 16];  // a lane puts a row, the last lanes one again
     int g;
     int64_t first, last;
-    const int col = blockIdx.x / row_tiles;
-    if (!find_rows<16>(base, G, a_rows, blockIdx.x - col * row_tiles, g, first, last)) return;
+    const int col = blockIdx.y;
+    if (!find_rows<16>(base, G, a_rows, blockIdx.x, g, first, last)) return;
     g = __builtin_amdgcn_readfirstlane(g);
     first = __builtin_amdgcn_readfirstlane((int)first);
     last = __builtin_amdgcn_readfirstlane((int)last);
@@ -531,11 +534,10 @@ hipError_t few_rows(const void *a_codes, const void *a_scales, int64_t a_rows, c
     const int ncol = gated ? (O / 2 + 15) / 16 : (O + 31) / 32;
     auto *kernel = H >= 512 ? (gated ? product_small_kernel<true, false> : product_small_kernel<false, false>)
                             : (gated ? product_small_kernel<true, true> : product_small_kernel<false, true>);
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)(row_tiles * ncol)), dim3(64 * kSmallWaves), 0, stream,
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)row_tiles, ncol), dim3(64 * kSmallWaves), 0, stream,
                        static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales), a_rows,
                        group_base, G, static_cast<const uint8_t *>(w_codes),
-                       static_cast<const uint8_t *>(w_scales), O, H / 32, (int)row_tiles,
-                       static_cast<uint8_t *>(out), out_stride);
+                       static_cast<const uint8_t *>(w_scales), O, H / 32, static_cast<uint8_t *>(out), out_stride);
     return hipGetLastError();
 }
 
@@ -548,7 +550,10 @@ hipError_t tiles(const void *a_codes, const void *a_scales, int64_t a_rows, cons
     const int64_t row_tiles = a_rows / TM + (a_rows < G ? a_rows : G);  // at most
     const int64_t need = (row_tiles * ncol + 7) / 8 * 8;
     const int64_t grid = need < resident ? need : resident;
-    auto *kernel = gated ? product_tile_kernel<TM, TN, WMC, WNC, true> : product_tile_kernel<TM, TN, WMC, WNC, false>;
+    auto *kernel = H >= 512 ? (gated ? product_tile_kernel<TM, TN, WMC, WNC, true, false>
+                                     : product_tile_kernel<TM, TN, WMC, WNC, false, false>)
+                            : (gated ? product_tile_kernel<TM, TN, WMC, WNC, true, true>
+                                     : product_tile_kernel<TM, TN, WMC, WNC, false, true>);
     hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WMC * WNC), 0, stream,
                        static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales),
                        a_rows, group_base, G, static_cast<const uint8_t *>(w_codes),
@@ -584,7 +589,7 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
         const int outs = gated ? tn / 2 : tn;
         return hit * ((mean + tm - 1) / tm) * ((width + outs - 1) / outs);
     };
-    if (H < 512 || tiles_of(16, 32) * ((mean < 16 ? mean : 16) + 32) <= 1024 * 33)
+    if (tiles_of(16, 32) * ((mean < 16 ? mean : 16) + 32) <= 1024 * 33)
         return few_rows(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
                         out_stride_bytes, stream);
     if (mean >= 160 && tiles_of(256, 256) >= 192)

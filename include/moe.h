@@ -515,7 +515,7 @@ int moe_plan_run(const moe_plan *plan, hipStream_t stream);
  * moe_layout writes them), entries outside [0, expert_rows) are skipped like pads, S, K and H have the
  * ranges of moe_combine, and rows * stride must not exceed INT64_MAX. No output may overlap an input or
  * another output (MOE_ERR_ARG where the buffers' extents do). Results do not depend on timing: no
- * atomics, a fixed order of every sum.
+ * atomics, a fixed order of every sum. A null stream is the current device's, here and below.
  *
  * moe_combine_backward: for every valid (t, k) with s = slot_idx[t, k]
  *      d_expert_out[s]    = bf16( fp32(topk_weights[t, k] * fp32(dy[t])) ), one product rounded to fp32, then
@@ -526,8 +526,8 @@ int moe_plan_run(const moe_plan *plan, hipStream_t stream);
  *      expert_out    the forward's rows: 16-byte aligned, row_stride_bytes >= 2H and a multiple of 16.
  * Out: d_expert_out  bf16 rows, row s at s * d_row_stride_bytes (16-byte aligned, stride >= 2H and a
  *                    multiple of 16), expert_rows rows. Rows that no entry names keep their contents. Where
- *                    two entries name one row (a table that moe_layout did not write), it holds the product
- *                    of one of them.
+ *                    two entries name one row (a table that moe_layout did not write), each 16 bytes of it
+ *                    are those of one of the two products.
  *      d_topk_weights fp32 [S, K], fully overwritten.
  * Enqueues one kernel. */
 int moe_combine_backward(const void *dy, const void *expert_out, int64_t row_stride_bytes,
@@ -622,7 +622,8 @@ int moe_combine_backward_mx(const void *dy, const void *codes, const void *scale
  * In:  a_codes, a_scales  MX E2M1 rows [a_rows, H] (a_rows in [0, MOE_MAX_OUT_ROWS]; 0 enqueues nothing).
  *      group_base         DEVICE int32 [G + 1], ascending, read on the device: expert_slot_base of the layout, or
  *                         a part of it (expert_slot_base + first, with the weights of G experts from there).
- *                         Values are clamped to [0, a_rows]. Empty groups are fine.
+ *                         Values are clamped to [0, a_rows]. Empty groups are fine. Bases that descend leave
+ *                         it open which of the rows in [0, a_rows) are computed.
  *      G                  in [1, MOE_MAX_EXPERTS].
  *      w_codes, w_scales  MX E2M1 rows [G, O, H]; O in [1, MOE_MAX_OUTPUTS], even for MOE_MX_GATED
  *                         (MOE_ERR_UNSUPPORTED otherwise).

@@ -340,6 +340,7 @@ PRODUCTS = [  # rows of each group, H, O
     ([200, 170, 300, 0] * 4, 512, 4100),
     ([200, 170, 300, 0] * 4, 1056, 4100), ([50] * 30, 544, 2500), ([300, 90, 0, 260] * 8, 512, 300), ([7] * 64, 544, 1500),
     ([7] * 64, 1024, 700), ([1000], 768, 6200), ([65, 0, 64, 63], 2048, 510), ([5, 1, 0, 2], 7168, 130), ([40] * 20, 608, 90), ([513, 0, 1023], 992, 514),
+    ([700, 690], 480, 9000), ([90] * 20, 96, 1300), ([30000, 20000], 32, 66), ([2, 1], 32, 65536), ([50, 3] * 8, 224, 700),
 ]
 
 
@@ -417,6 +418,23 @@ def test_product_bases_out_of_range(moe, base):
     has = ~np.isnan(want[:, 0])
     same_bits(got[has], bits(want[has].astype(np.float32)))
     assert np.all(got[~has] == 0xABAB)
+
+
+@pytest.mark.parametrize("O", [24, 300])
+def test_product_descending_bases(moe, O):
+    """Bases that go up and down: nothing outside the rows is touched, and rows of ascending parts are computed."""
+    rng = np.random.default_rng(16)
+    R, H, G = 500, 544, 512
+    base = np.zeros(G + 1, dtype=np.int32)
+    base[1::2] = 1 << 30
+    a, w = mx_random(rng, (R, H), -1, 1), mx_random(rng, (1, O, H), -1, 1)
+    w = [np.broadcast_to(m, (G, *m.shape[1:])) for m in w]
+    out = poison((R + 64, O), torch.bfloat16)
+    moe.moe_mx_product(moe.MxRows(*map(to_dev, a)), moe.MxRows(*map(to_dev, w)), to_dev(base), out=out[:R])
+    want = oracle.mx_product(oracle.mx_values(*a, E2M1), oracle.mx_values(w[0][:1], w[1][:1], E2M1), np.array([0, R]))
+    got = bf16_bits(out)
+    assert np.all(got[R:] == 0xABAB)
+    same_bits(got[:R], bits(want.astype(np.float32)))  # every group has the same weights
 
 
 def test_product_of_many_groups(moe):
