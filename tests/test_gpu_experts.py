@@ -170,7 +170,7 @@ def test_mx_of_no_rows(moe):
 TABLES = [  # S, K, E, H, masked share
     (1, 1, 1, 16, 0.0), (1, 8, 16, 7168, 0.0), (3, 2, 4, 1024, 0.5), (33, 3, 7, 2064, 0.2), (128, 2, 16, 1024, 0.0),
     (40, 16, 64, 96, 0.1), (7, 5, 9, 8192, 0.1), (5, 4, 6, 16384, 0.1), (9, 9, 20, 8208, 0.0), (21, 6, 48, 2080, 1.0),
-    (700, 8, 64, 512, 0.05),
+    (700, 8, 64, 512, 0.05), (6, 16, 40, 16384, 0.1),
 ]
 MX_TABLES = [(s, k, e, (h + 31) // 32 * 32, p) for s, k, e, h, p in TABLES]
 
@@ -254,6 +254,121 @@ def test_dispatch_backward(moe, S, K, E, H, p, gap):
     dx = poison((S, H), torch.bfloat16)
     moe.moe_dispatch_backward(strided(rows, gap), to_dev(slot), dx=dx)
     same_bits(bf16_bits(dx), oracle.dispatch_backward(rows, slot))
+
+
+def test_gradients_are_differences(moe):
+    """The calls' own forwards, moved by small integers: every value and sum is exact, so are the differences."""
+    rng = np.random.default_rng(30)
+    S, K, E, H = 33, 3, 7, 64
+    idx = to_dev(random_tiny_routing(rng, S, K, E, p_mask=0.2))
+    lay = moe.moe_layout(idx, E, 1, 1)
+    slot, R = lay.slot_idx, S * K
+    small = lambda shape, n: torch.from_numpy(rng.integers(-n, n + 1, shape).astype(np.float32)).to(DEV)  # noqa: E731
+    rows, dy, w, x = small((R, H), 3), small((S, H), 3), small((S, K), 4), small((S, H), 3)
+    as_bf16 = lambda t: t.to(torch.bfloat16).contiguous()  # noqa: E731
+
+    def loss(rows, w):
+        return float((dy.double() * moe.moe_combine(as_bf16(rows), slot, w.contiguous()).double()).sum())
+
+    start = torch.zeros((R, H), dtype=torch.bfloat16, device=DEV)
+    d_rows, d_w = moe.moe_combine_backward(as_bf16(dy), as_bf16(rows), slot, w, d_expert_out=start)
+    for _ in range(3):
+        step, w_step = small((R, H), 2), small((S, K), 2)
+        assert loss(rows + step, w) - loss(rows, w) == float((step.double() * d_rows.double()).sum())
+        assert loss(rows, w + w_step) - loss(rows, w) == float((w_step.double() * d_w.double()).sum())
+
+    g = small((R, H), 3)
+    dx = moe.moe_dispatch_backward(as_bf16(g), slot)
+    N = int(lay.expert_slot_base[-1])
+
+    def sent(x):
+        win = torch.zeros(moe.moe_window_bytes(S, K, H), dtype=torch.uint8, device=DEV)
+        moe.moe_dispatch(as_bf16(x), slot, win, moe.MOE_QUANT_NONE)
+        rows = win.view(R, -1)[:N, : 2 * H].contiguous().view(torch.bfloat16)
+        return float((g[:N].double() * rows.double()).sum())
+
+    for _ in range(3):
+        step = small((S, H), 2)
+        assert sent(x + step) - sent(x) == float((step.double() * dx.double()).sum())
+
+
+def test_one_row_in_two_entries(moe):
+    """A table that names rows twice: sums and weight gradients count each entry, 16 bytes of a gradient row are
+    those of one of its products, the checkpoint holds the row."""
+    rng = np.random.default_rng(31)
+    S, K, H, R = 24, 4, 512, 9
+    slot = rng.integers(-1, R, (S, K)).astype(np.int32)
+    slot[:, 3] = slot[:, 0]
+    rows, dy, w = spread_rows(rng, R, H), spread_rows(rng, S, H), rng.random((S, K), dtype=np.float32)
+    y, kept = moe.moe_combine_checkpoint(bf16_dev(rows), to_dev(slot), to_dev(w))
+    same_bits(bf16_bits(y), oracle.combine(rows, slot, w), "y")
+    codes, scales = oracle.mx_quantize(rows, E4M3)
+    assert np.array_equal(kept.codes.cpu().numpy(), codes) and np.array_equal(kept.scales.cpu().numpy(), scales)
+    same_bits(bf16_bits(moe.moe_dispatch_backward(bf16_dev(rows), to_dev(slot))), oracle.dispatch_backward(rows, slot), "dx")
+    kept_values = oracle.mx_values(codes, scales, E4M3)
+    for got, values in ((moe.moe_combine_backward(bf16_dev(dy), bf16_dev(rows), to_dev(slot), to_dev(w)), oracle.bf16_bits_to_f32(rows)),
+                        (moe.moe_combine_backward_mx(bf16_dev(dy), kept, to_dev(slot), to_dev(w)), kept_values)):
+        _, want_w, magnitude = oracle.combine_backward(dy, values.astype(np.float64), slot, w, np.zeros((R, H)))
+        assert np.all(np.abs(got[1].cpu().numpy() - want_w) <= weight_error_bound(magnitude))
+        d_rows = bf16_bits(got[0])
+        for s in range(R):
+            t, k = np.nonzero(slot == s)
+            products = bits(w[t, k, None] * oracle.bf16_bits_to_f32(dy[t])).reshape(-1, H // 8, 8)
+            assert np.all((products == d_rows[s].reshape(-1, 8)).all(axis=2).any(axis=0)), s
+
+
+def test_the_most_entries(moe):
+    """65536 tokens of 16 entries, the smallest rows."""
+    rng = np.random.default_rng(32)
+    S, K, H = 65536, 16, 32
+    R = S * K
+    slot = rng.permutation(R).astype(np.int32).reshape(S, K)
+    slot[rng.random((S, K)) < 0.1] = -1
+    rows, dy, w = bits(rng.standard_normal((R, H))), bits(rng.standard_normal((S, H))), rng.random((S, K), dtype=np.float32)
+    src, idx, weights = bf16_dev(rows), to_dev(slot), to_dev(w)
+    check_combine_backward(moe, lambda d, dw: moe.moe_combine_backward(bf16_dev(dy), src, idx, weights, d, dw),
+                           oracle.bf16_bits_to_f32(rows).astype(np.float64), dy, slot, w, R, H)
+    same_bits(bf16_bits(moe.moe_dispatch_backward(src, idx)), oracle.dispatch_backward(rows, slot))
+    y, kept = moe.moe_combine_checkpoint(src, idx, weights)
+    same_bits(bf16_bits(y), oracle.combine(rows, slot, w), "y")
+    codes, scales = oracle.mx_quantize(rows, E4M3)
+    live = np.sort(slot[slot >= 0])
+    assert np.array_equal(kept.codes.cpu().numpy()[live], codes[live]) and np.array_equal(kept.scales.cpu().numpy()[live], scales[live])
+    all_rows = moe.moe_mx_quantize(src, E2M1)  # the most rows
+    codes, scales = oracle.mx_quantize(rows, E2M1)
+    assert np.array_equal(all_rows.codes.cpu().numpy(), codes) and np.array_equal(all_rows.scales.cpu().numpy(), scales)
+
+
+def test_rows_past_4_gib(moe):
+    """Rows, checkpoints and gradients whose offsets pass 32 bits."""
+    rng = np.random.default_rng(33)
+    S, K, H, R = 3, 2, 16384, 300_000
+    slot = np.array([[299_999, 5], [-1, 262_143], [140_000, 262_144]], dtype=np.int32)
+    named = slot[slot >= 0]
+    values, dy, w = spread_rows(rng, len(named), H), spread_rows(rng, S, H), rng.random((S, K), dtype=np.float32)
+    place = np.full((S, K), -1, dtype=np.int32)  # the same table over the named rows alone
+    place[slot >= 0] = np.arange(len(named))
+    rows, where = torch.empty((R, H), dtype=torch.bfloat16, device=DEV), to_dev(named.astype(np.int64))
+    rows[where] = bf16_dev(values)
+    y, kept = moe.moe_combine_checkpoint(rows, to_dev(slot), to_dev(w))
+    same_bits(bf16_bits(y), oracle.combine(values, place, w), "y")
+    codes, scales = oracle.mx_quantize(values, E4M3)
+    assert np.array_equal(kept.codes[where].cpu().numpy(), codes) and np.array_equal(kept.scales[where].cpu().numpy(), scales)
+    same_bits(bf16_bits(moe.moe_dispatch_backward(rows, to_dev(slot))), oracle.dispatch_backward(values, place), "dx")
+    d_rows = torch.empty_like(rows)
+    for call, v in ((lambda: moe.moe_combine_backward(bf16_dev(dy), rows, to_dev(slot), to_dev(w), d_rows), oracle.bf16_bits_to_f32(values)),
+                    (lambda: moe.moe_combine_backward_mx(bf16_dev(dy), kept, to_dev(slot), to_dev(w), d_rows), oracle.mx_values(codes, scales, E4M3))):
+        d_w = call()[1]
+        want, want_w, magnitude = oracle.combine_backward(dy, v.astype(np.float64), place, w, values)
+        same_bits(bf16_bits(d_rows[where]), want, "d_rows")
+        assert np.all(np.abs(d_w.cpu().numpy() - want_w) <= weight_error_bound(magnitude))
+    back = moe.moe_mx_dequantize(moe.moe_mx_quantize(rows[299_990:], E2M1), E2M1)
+    assert np.array_equal(bf16_bits(back[9:]), bits(oracle.mx_values(*oracle.mx_quantize(values[:1], E2M1), E2M1)))
+    whole = moe.moe_mx_quantize(rows, E2M1, out=moe.MxRows(kept.codes.view(-1)[: R * H // 2].view(R, H // 2), kept.scales))
+    codes, scales = oracle.mx_quantize(values, E2M1)
+    assert np.array_equal(whole.codes[where].cpu().numpy(), codes) and np.array_equal(whole.scales[where].cpu().numpy(), scales)
+    back = moe.moe_mx_dequantize(whole, E2M1, out=d_rows)
+    assert np.array_equal(bf16_bits(back[where]), bits(oracle.mx_values(codes, scales, E2M1)))
 
 
 # ---------------------------------------------------------------- 8-bit checkpoints
@@ -350,6 +465,28 @@ def test_product_exact(moe, counts, H, O):
     note("product", counts, H, O)
     got, exact, _ = product_case(moe, rng, counts, H, O, False, before=2, behind=3, gap=O % 3)
     same_bits(got, bits(exact.astype(np.float32)), "product")
+
+
+@pytest.mark.parametrize("counts", [[0] * 8 + [3], [0] * 7 + [300, 200]])
+def test_product_of_weights_past_4_gib(moe, counts):
+    """The largest matrices and rows: 9 x 65536 x 16384 codes, of which the last groups' first and last rows are
+    compared. Scales of 1: products are multiples of 1/4 and sums below 36 * 16384 < 2^24 / 4, exact in fp32."""
+    rng = np.random.default_rng(34)
+    G, O, H = len(counts), 65536, 16384
+    base = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    R = int(base[-1])
+    codes = torch.zeros((G, O, H // 2), dtype=torch.uint8, device=DEV)
+    picked = np.array([0, 1, 130, 40_000, 65_407, 65_534, 65_535])
+    some = mx_random(rng, (G, len(picked), H), 0, 0)
+    for g in range(G):
+        codes[g, to_dev(picked)] = to_dev(some[0][g])
+    scales = torch.full((G, O, H // 32), 127, dtype=torch.uint8, device=DEV)
+    a = mx_random(rng, (R, H), 0, 0)
+    got = moe.moe_mx_product(moe.MxRows(*map(to_dev, a)), moe.MxRows(codes, scales), to_dev(base))
+    want = oracle.mx_product(oracle.mx_values(*a, E2M1), oracle.mx_values(*some, E2M1), base)
+    same_bits(bf16_bits(got[:, to_dev(picked)]), bits(want.astype(np.float32)))
+    got[:, to_dev(picked)] = 0
+    assert not got.any()
 
 
 @pytest.mark.parametrize("counts,H,O", [c for c in PRODUCTS if c[2] % 2 == 0])
