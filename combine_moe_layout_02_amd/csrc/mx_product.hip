@@ -187,7 +187,9 @@ __device__ inline Tile find_tile(const TileTable &table, int G, int ncol, int t)
 // the last one, so behind it the pair is whole and the last pair's buffer is free.
 //
 // 32768 rows on 32 groups, 7168 -> 4096 gated: the matrix cores alone take 290 to 350 us on random codes (the
-// card's power holds them at 6.5 PFLOP/s), the loads alone 450, together 650.
+// card's power holds them at 6.5 PFLOP/s), the loads alone 450, the products with their reads of LDS 500, together
+// 636. Four waves of 128 x 128 results read a third less of LDS, but took 700, and 718 with the next stage's operands
+// read ahead: one wave a SIMD leaves its loads and reads uncovered.
 constexpr int kStageBlocks = 4;    // MX blocks of a stage
 constexpr int kRoundStages = 4;    // stages of a round: two pairs
 constexpr int kScaleBlocks = 16;   // MX blocks of a round
@@ -580,6 +582,7 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
     //   64 x 128         90.7, 49.3   128, 68.2    189, 95.6    321, 170     947, 564
     //   128 x 128        96.1, 52.4   109, 60.3    152, 80.6    248, 142     748, 470
     //   256 x 256                     137, 80.1    161, 87.3    233, 146     629, 396
+    // Rows shorter than 512 take the same rule (32 groups of 16 rows, 480 -> 2048, 9.0 us; by few_rows 18.1).
     // A tile is also the least that one workgroup can do, at H = 7168 19, 23 and 47 us, so a product of few tiles
     // takes smaller ones (16 groups, 3001 rows, 1056 -> 1000: 9.9, 11.8, 15.1 us). With only a few hundred tiles
     // of 64 x 128 the weights are better read by four waves a 16 rows each (few_rows): 8 rows on 32 groups, 7168 ->
