@@ -175,21 +175,27 @@ __device__ inline Tile find_tile(const TileTable &table, int G, int ncol, int t)
     return Tile{g, first, min(TM, hi - first), col};
 }
 
-// Tiles of TM rows x TN weight rows (TN / 2 outputs when GATED), WMC x WNC waves, through LDS. A workgroup takes
-// tile after tile; the 8 XCDs get contiguous eighths of the tiles (workgroup b runs on XCD b % 8).
+// Tiles of TM rows x TN weight rows (TN / 2 outputs when GATED), WMC x WNC waves, through LDS. The 8 XCDs get
+// contiguous eighths of the tiles (workgroup b runs on XCD b % 8).
 //
 // Codes go from memory straight to LDS in pairs of stages of 128 values, 128 bytes of a row (whole lines; stages
-// of 64 bytes through a ring of four took 10% longer where the weights' bytes count), through two buffers: while
-// one is multiplied the other fills, the next tile's first pair behind a tile's last, so that the loads never
-// pause and a tile's results are stored while the next one's rows arrive. Scales come through registers, 16
-// blocks (four stages, one round) at a time, and lie in LDS so that one word holds a lane's four scales of a
-// round. One barrier a pair: it follows each wave's wait for its own loads of the pair and for its LDS reads of
-// the last one, so behind it the pair is whole and the last pair's buffer is free.
+// of 64 bytes through a ring of four took 10% longer where the weights' bytes count), through PAIRS buffers: while
+// one is multiplied the others fill. Scales come through registers, 16 blocks (four stages, one round) at a time, and
+// lie in LDS so that one word holds a lane's four scales of a round. One barrier a pair: it follows each wave's wait
+// for its own loads of the pair and for its LDS reads of the last one, so behind it the pair is whole and the last
+// pair's buffer is free.
+//
+// PAIRS == 2, many tiles: a workgroup takes tile after tile, the next tile's first pair behind a tile's last, so that
+// the loads never pause and a tile's results are stored while the next one's rows arrive.
 //
 // 32768 rows on 32 groups, 7168 -> 4096 gated: the matrix cores alone take 290 to 350 us on random codes (the
 // card's power holds them at 6.5 PFLOP/s), the loads alone 450, the products with their reads of LDS 500, together
 // 636. Four waves of 128 x 128 results read a third less of LDS, but took 700, and 718 with the next stage's operands
 // read ahead: one wave a SIMD leaves its loads and reads uncovered.
+//
+// PAIRS > 2, tiles for every compute unit once at most: a workgroup takes one tile, whose time is its pairs' way
+// from memory and through the matrix cores: 0.55 us a pair with one under way and 0.45 with three at 64 x 128, 0.31
+// at 64 x 64, 0.27 at 32 x 64 (with seven under way no less: there the reads and products of one wave count).
 constexpr int kStageBlocks = 4;    // MX blocks of a stage
 constexpr int kRoundStages = 4;    // stages of a round: two pairs
 constexpr int kScaleBlocks = 16;   // MX blocks of a round
@@ -202,7 +208,7 @@ __device__ inline void stage_barrier() {
     asm volatile("" ::: "memory");
 }
 
-template <int TM, int TN, int WMC, int WNC, bool GATED, bool SHORT>
+template <int TM, int TN, int WMC, int WNC, int PAIRS, bool GATED, bool SHORT>
 __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     const uint8_t *__restrict__ a_codes, const uint8_t *__restrict__ a_scales, int64_t a_rows,
     const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
@@ -214,11 +220,12 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     constexpr int SLOADS = (ROWS + THREADS - 1) / THREADS;  // rows of a round of scales a thread
     constexpr int OF = GATED ? NI / 2 : NI;                 // column fragments of results
     constexpr int STORES = MI * OF / 2;                     // stores of a wave, 16 bytes a lane
-    static_assert(LOADS * 8 * NW == ROWS && OF % 2 == 0 && MI * 16 * WMC == TM && NI * 16 * WNC == TN, "shape");
+    static_assert((PAIRS == 2 || PAIRS == 4) && LOADS * 8 * NW == ROWS && OF % 2 == 0 && MI * 16 * WMC == TM && NI * 16 * WNC == TN, "shape");
     // the buffers are objects of their own, so that the compiler sees the reads of one and the loads into the
     // other apart and puts no wait between them
     __shared__ __align__(1024) uint8_t pair0[ROWS * 128], pair1[ROWS * 128];
-    uint8_t *const codes[2] = {pair0, pair1};
+    __shared__ __align__(1024) uint8_t pair2[PAIRS > 2 ? ROWS * 128 : 16], pair3[PAIRS > 2 ? ROWS * 128 : 16];
+    uint8_t *const codes[4] = {pair0, pair1, pair2, pair3};
     __shared__ __align__(16) uint8_t scales[2][SLOADS * THREADS * 16];  // threads past the rows put the last one again
     __shared__ TileTable table;
 
@@ -279,17 +286,17 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
             load_to_lds(8 * (wave + l * NW) < TM ? src.a : src.w, &buf[(wave + l * NW) * 1024],
                         past ? 0x7FFFFFF0 : src.base[l] + place, st * 64);
     };
-    u32x4 sreg[SLOADS];  // a round of the rows' scales, 16 bytes each
-    const auto load_scales = [&](const Source &src, int round) {
+    u32x4 sreg[PAIRS / 2][SLOADS];  // rounds of the rows' scales, 16 bytes each
+    const auto load_scales = [&](const Source &src, int round, u32x4 (&to)[SLOADS]) {
 #pragma unroll
-        for (int l = 0; l < SLOADS; ++l) sreg[l] = load_row16<SHORT>(src.scales[l], round * kScaleBlocks, nblk);
+        for (int l = 0; l < SLOADS; ++l) to[l] = load_row16<SHORT>(src.scales[l], round * kScaleBlocks, nblk);
     };
     // Put as [row][lane's k-block q][stage of the round]: the transpose of the row's 4 x 4 bytes.
-    const auto put_scales = [&](int round, int buf) {
+    const auto put_scales = [&](int round, int buf, const u32x4 (&from)[SLOADS]) {
 #pragma unroll
         for (int l = 0; l < SLOADS; ++l)
             *reinterpret_cast<u32x4 *>(&scales[buf][(l * THREADS + tid) * 16]) =
-                transpose_bytes(place_row16<SHORT>(sreg[l], round * kScaleBlocks, nblk));
+                transpose_bytes(place_row16<SHORT>(from[l], round * kScaleBlocks, nblk));
     };
 
     const int wm = (wave % WMC) * WM, wn = TM + (wave / WMC) * WN;
@@ -297,75 +304,104 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
     const int at0 = fr * 128 + (q ^ (fr & 7)) * 16, at1 = fr * 128 + ((q + 4) ^ (fr & 7)) * 16;
     const int stages = (nblk + kStageBlocks - 1) / kStageBlocks, rounds = (stages + kRoundStages - 1) / kRoundStages;
 
+    f32x4 acc[MI][NI];
+    int as[MI], ws[NI];
+    i32x4 a[MI], w[NI];
+    const auto read_scales = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+            ws[j] = *reinterpret_cast<const int *>(&scales[buf][(wn + j * 16 + fr) * 16 + q * 4]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            as[i] = *reinterpret_cast<const int *>(&scales[buf][(wm + i * 16 + fr) * 16 + q * 4]);
+    };
+    const auto read_codes = [&](const uint8_t *buf, int at) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j) w[j] = *reinterpret_cast<const i32x4 *>(&buf[(wn + j * 16) * 128 + at]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) a[i] = *reinterpret_cast<const i32x4 *>(&buf[(wm + i * 16) * 128 + at]);
+    };
+    const auto multiply = [&](int s) {  // s: the stage's number in its round, a constant where this is unrolled
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                f32x4 &c = acc[i][j];
+                if (s == 0) c = mfma_byte<0>(w[j], ws[j], a[i], as[i], c);
+                else if (s == 1) c = mfma_byte<1>(w[j], ws[j], a[i], as[i], c);
+                else if (s == 2) c = mfma_byte<2>(w[j], ws[j], a[i], as[i], c);
+                else c = mfma_byte<3>(w[j], ws[j], a[i], as[i], c);
+            }
+        }
+    };
+
     Tile tile = find_tile<TM>(table, G, ncol, t);
     Source cur = source_of(tile);
-    load_scales(cur, 0);
-    load_codes(cur, 0, codes[0], false);
+#pragma unroll
+    for (int r = 0; r < PAIRS / 2; ++r) load_scales(cur, r, sreg[r]);
+#pragma unroll
+    for (int i = 0; i < PAIRS - 1; ++i) load_codes(cur, 2 * i, codes[i], false);
     int sbuf = 0;         // the scales' buffer of this round
     bool stored = false;  // the stores of the tile before are still in flight, STORES of them
-    put_scales(0, 0);
+    put_scales(0, 0, sreg[0]);
     for (;;) {
         t += step;
-        const bool more = t < xcd_end;
+        const bool more = PAIRS == 2 && t < xcd_end;
         Tile next = tile;
-        f32x4 acc[MI][NI];
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        for (int round = 0; round < rounds; ++round) {
-            int as[MI], ws[NI];
-            const bool last = round + 1 == rounds;
+        if constexpr (PAIRS > 2) {
+            // All but one of the pairs are under way while that one is multiplied; a round's scales are loaded as many
+            // rounds ahead as the pairs are, so that the wait for them is none for codes that are not needed yet.
+            for (int round = 0; round < rounds; round += PAIRS / 2) {
 #pragma unroll
-            for (int s = 0; s < kRoundStages; ++s) {
-                const int st = round * kRoundStages + s;
-                if ((s & 1) == 0) {
-                    if (s == 0 && round == 0 && stored) stage_barrier<STORES>();
-                    else stage_barrier<0>();
-                }
-                if (s == 0) {
-#pragma unroll
-                    for (int j = 0; j < NI; ++j)
-                        ws[j] = *reinterpret_cast<const int *>(&scales[sbuf][(wn + j * 16 + fr) * 16 + q * 4]);
-#pragma unroll
-                    for (int i = 0; i < MI; ++i)
-                        as[i] = *reinterpret_cast<const int *>(&scales[sbuf][(wm + i * 16 + fr) * 16 + q * 4]);
-                }
-                i32x4 a[MI], w[NI];
-#pragma unroll
-                for (int j = 0; j < NI; ++j)
-                    w[j] = *reinterpret_cast<const i32x4 *>(&codes[s >> 1][(wn + j * 16) * 128 + (s & 1 ? at1 : at0)]);
-#pragma unroll
-                for (int i = 0; i < MI; ++i)
-                    a[i] = *reinterpret_cast<const i32x4 *>(&codes[s >> 1][(wm + i * 16) * 128 + (s & 1 ? at1 : at0)]);
-                if (s == 0) {
-                    load_codes(cur, st + 2, codes[1], false);
-                    if (last && more) {
-                        next = find_tile<TM>(table, G, ncol, t);
-                        cur = source_of(next);
+                for (int s = 0; s < 2 * PAIRS; ++s) {
+                    const int st = round * kRoundStages + s, r = s / kRoundStages;
+                    if (s % 2 == 0) stage_barrier<(PAIRS - 2) * LOADS>();
+                    if (s % kRoundStages == 0) {
+                        read_scales(r & 1);
+                        load_scales(cur, round + r + PAIRS / 2, sreg[r]);
                     }
-                    load_scales(cur, last ? 0 : round + 1);
+                    read_codes(codes[s >> 1], s & 1 ? at1 : at0);
+                    if (s % 2 == 0) load_codes(cur, st + 2 * (PAIRS - 1), codes[((s >> 1) + PAIRS - 1) % PAIRS], false);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (st < stages) multiply(s % kRoundStages);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (s % kRoundStages == kRoundStages - 1)
+                        put_scales(round + r + 1, (r + 1) & 1, sreg[(r + 1) % (PAIRS / 2)]);
                 }
-                // behind the tile's last pair comes the next tile's first one
-                if (s == 2) load_codes(cur, last ? 0 : st + 2, codes[0], last && !more);
-                __builtin_amdgcn_sched_barrier(0);  // the reads and loads are under way before the products
-                if (st < stages) {
+            }
+        } else {
+            for (int round = 0; round < rounds; ++round) {
+                const bool last = round + 1 == rounds;
 #pragma unroll
-                    for (int i = 0; i < MI; ++i) {
-#pragma unroll
-                        for (int j = 0; j < NI; ++j) {
-                            f32x4 &c = acc[i][j];
-                            if (s == 0) c = mfma_byte<0>(w[j], ws[j], a[i], as[i], c);
-                            else if (s == 1) c = mfma_byte<1>(w[j], ws[j], a[i], as[i], c);
-                            else if (s == 2) c = mfma_byte<2>(w[j], ws[j], a[i], as[i], c);
-                            else c = mfma_byte<3>(w[j], ws[j], a[i], as[i], c);
+                for (int s = 0; s < kRoundStages; ++s) {
+                    const int st = round * kRoundStages + s;
+                    if ((s & 1) == 0) {
+                        if (s == 0 && round == 0 && stored) stage_barrier<STORES>();
+                        else stage_barrier<0>();
+                    }
+                    if (s == 0) read_scales(sbuf);
+                    read_codes(codes[s >> 1], s & 1 ? at1 : at0);
+                    if (s == 0) {
+                        load_codes(cur, st + 2, codes[1], false);
+                        if (last && more) {
+                            next = find_tile<TM>(table, G, ncol, t);
+                            cur = source_of(next);
                         }
+                        load_scales(cur, last ? 0 : round + 1, sreg[0]);
                     }
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                if (s == kRoundStages - 1) {
-                    sbuf ^= 1;
-                    put_scales(last ? 0 : round + 1, sbuf);
+                    // behind the tile's last pair comes the next tile's first one
+                    if (s == 2) load_codes(cur, last ? 0 : st + 2, codes[0], last && !more);
+                    __builtin_amdgcn_sched_barrier(0);  // the reads and loads are under way before the products
+                    if (st < stages) multiply(s);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (s == kRoundStages - 1) {
+                        sbuf ^= 1;
+                        put_scales(last ? 0 : round + 1, sbuf, sreg[0]);
+                    }
                 }
             }
         }
@@ -450,7 +486,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void product_small_kernel(
         const int j = r - 16;
         return GATED ? min(o0 + (j & 15), width - 1) + (j >> 4) * width : min(o0 + j, width - 1);
     };
-    const int r4 = lane >> 2, blk = (lane & 3) ^ ((r4 >> 1) & 3);  // as in the tiles above
+    const int r4 = lane >> 2, blk = (lane & 3) ^ ((r4 >> 1) & 3);  // places against bank conflicts, as in the tiles
     int voff[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) voff[f] = row_of(16 * f + r4) * pitch + blk * 16;
@@ -543,19 +579,22 @@ hipError_t few_rows(const void *a_codes, const void *a_scales, int64_t a_rows, c
     return hipGetLastError();
 }
 
-template <int TM, int TN, int WMC, int WNC>
+constexpr int kUnits = 256;  // compute units of an MI355X
+
+template <int TM, int TN, int WMC, int WNC, int PAIRS>
 hipError_t tiles(const void *a_codes, const void *a_scales, int64_t a_rows, const int32_t *group_base,
                  int32_t G, const void *w_codes, const void *w_scales, int32_t O, int32_t H, bool gated,
-                 void *out, int64_t out_stride, bool wide, int resident, hipStream_t stream) {
+                 void *out, int64_t out_stride, bool wide, hipStream_t stream) {
+    constexpr int resident = TM + TN > 256 ? kUnits : 2 * kUnits;  // workgroups that run at once, by their LDS
     const int width = gated ? O / 2 : O, tn = gated ? TN / 2 : TN;
     const int ncol = (width + tn - 1) / tn;
     const int64_t row_tiles = a_rows / TM + (a_rows < G ? a_rows : G);  // at most
     const int64_t need = (row_tiles * ncol + 7) / 8 * 8;
-    const int64_t grid = need < resident ? need : resident;
-    auto *kernel = H >= 512 ? (gated ? product_tile_kernel<TM, TN, WMC, WNC, true, false>
-                                     : product_tile_kernel<TM, TN, WMC, WNC, false, false>)
-                            : (gated ? product_tile_kernel<TM, TN, WMC, WNC, true, true>
-                                     : product_tile_kernel<TM, TN, WMC, WNC, false, true>);
+    const int64_t grid = PAIRS > 2 || need < resident ? need : resident;
+    auto *kernel = H >= 512 ? (gated ? product_tile_kernel<TM, TN, WMC, WNC, PAIRS, true, false>
+                                     : product_tile_kernel<TM, TN, WMC, WNC, PAIRS, false, false>)
+                            : (gated ? product_tile_kernel<TM, TN, WMC, WNC, PAIRS, true, true>
+                                     : product_tile_kernel<TM, TN, WMC, WNC, PAIRS, false, true>);
     hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WMC * WNC), 0, stream,
                        static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales),
                        a_rows, group_base, G, static_cast<const uint8_t *>(w_codes),
@@ -576,33 +615,56 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
     // rows of whole 16-byte pieces, and a tile of them within a buffer descriptor's range
     const bool wide = width % 8 == 0 && out_stride_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                       out_stride_bytes <= (1 << 22);
-    // Which kernel, by the work it would have if the rows were spread evenly over as many groups as they can
-    // reach. Measured with G = 32, weights from memory (us; 7168 -> 4096 gated, 2048 -> 7168 plain):
-    //   rows a group     16           64           128          256          1024
-    //   64 x 128         90.7, 49.3   128, 68.2    189, 95.6    321, 170     947, 564
-    //   128 x 128        96.1, 52.4   109, 60.3    152, 80.6    248, 142     748, 470
-    //   256 x 256                     137, 80.1    161, 87.3    233, 146     629, 396
-    // Rows shorter than 512 take the same rule (32 groups of 16 rows, 480 -> 2048, 9.0 us; by few_rows 18.1).
-    // A tile is also the least that one workgroup can do, at H = 7168 19, 23 and 47 us, so a product of few tiles
-    // takes smaller ones (16 groups, 3001 rows, 1056 -> 1000: 9.9, 11.8, 15.1 us). With only a few hundred tiles
-    // of 64 x 128 the weights are better read by four waves a 16 rows each (few_rows): 8 rows on 32 groups, 7168 ->
-    // 4096, 24.7 against 30.2 us, 16 rows 43.2 against 40.8, where its workgroups exceed what runs at once.
+    // Which kernel, by the tiles it would have if the rows were spread over as many groups as they can reach, a
+    // quarter of them more in the fuller ones. Measured with weights from memory (us; groups x rows a group):
+    //   7168 -> 4096 gated   1x8    1x64   1x256  1x512  4x16   4x32   8x32   8x64   4x128  8x128  32x16  32x64  32x256
+    //   few_rows             6.9    17.6                 32.2   36.5   68.7                        221
+    //   32 x 64, four pairs  11.6   11.9   15.8   28.6   16.8   23.9   45.1   58.4   48.7   82.7   100    198    536
+    //   64 x 64, four        13.1   13.1   14.5   21.4   17.1   18.2   31.2   41.3   35.7   57.7   102    157    404
+    //   64 x 128, four       16.9   17.3   17.8   20.2   22.2   23.7   28.1   45.1   41.4   63.3   98.0   141    383
+    //   128 x 128, four             23.0   23.9   26.2          26.2   30.3   31.8   29.1   55.5          139    325
+    //   64 x 128, two        19.4   19.9   20.3   22.4   30.1   30.3   33.5   43.1   38.5   63.5   91.4   130    323
+    //   128 x 128, two              23.2   23.9   25.4          32.5   35.6   36.1   33.8   50.7          108    255
+    //   256 x 256, two              47.8   48.8   50.0                        58.2   58.0   61.4          146    234
+    // and 2048 -> 7168, 1x64, in the same order: 11.3, 6.4, 6.7, 8.1, 10.2, 8.6, 9.8, 17.7.
+    // Where the tiles are no more than the compute units, all of a tile's time is its way through one, and small
+    // tiles with more pairs under way shorten it; few_rows, whose waves share H, is ahead while its workgroups read
+    // no more than 15360 rows (5x101, 6528 -> 220: 8.3 against 11.8). Four pairs of a large tile leave room for one
+    // workgroup a compute unit, which short rows do not repay (1024 -> 1024 gated, 32x32: 64 x 128 8.2 against 7.5;
+    // 32x64: 128 x 128 9.9 against 8.7). With more tiles the two pairs' kernels, which start a tile while they end
+    // another, are ahead, the larger the more rows there are to share the weights: 128 x 128 from 300 tiles (16
+    // groups, 3001 rows, 1056 -> 1000, 256 tiles: 12.4 against 10.2), 256 x 256 where they fill the compute units
+    // (2048 -> 7168, 8x256, 448 tiles: 44.1 against 40.3; 32x256: 135 against 139).
     const int64_t hit = a_rows < G ? a_rows : G, mean = (a_rows + hit - 1) / hit;
+    const int64_t most = hit > 1 ? mean + mean / 4 : mean;
     const auto tiles_of = [&](int tm, int tn) {
         const int outs = gated ? tn / 2 : tn;
-        return hit * ((mean + tm - 1) / tm) * ((width + outs - 1) / outs);
+        return hit * ((most + tm - 1) / tm) * ((width + outs - 1) / outs);
     };
-    if (tiles_of(16, 32) * ((mean < 16 ? mean : 16) + 32) <= 1024 * 33)
+    if (tiles_of(16, 32) * ((most < 16 ? most : 16) + 32) <= 320 * 48)  // rows that its workgroups read
         return few_rows(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
                         out_stride_bytes, stream);
-    if (mean >= 160 && tiles_of(256, 256) >= 192)
-        return tiles<256, 256, 2, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
-                                     out_stride_bytes, wide, 256, stream);
-    if (mean >= 40 && tiles_of(128, 128) >= 192)
-        return tiles<128, 128, 2, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
-                                     out_stride_bytes, wide, 512, stream);
-    return tiles<64, 128, 2, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
-                                out_stride_bytes, wide, 512, stream);
+    if (tiles_of(32, 64) <= (most <= 32 ? 448 : kUnits))  // two at once on a compute unit, and room for a fuller group
+        return tiles<32, 64, 2, 1, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                      out_stride_bytes, wide, stream);
+    if (tiles_of(64, 64) <= kUnits)
+        return tiles<64, 64, 4, 1, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                      out_stride_bytes, wide, stream);
+    if (H >= 2048 && tiles_of(64, 128) <= kUnits)
+        return tiles<64, 128, 2, 2, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                       out_stride_bytes, wide, stream);
+    if (H >= 4096 && tiles_of(128, 128) <= kUnits)
+        return tiles<128, 128, 2, 2, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                        out_stride_bytes, wide, stream);
+    const int64_t large = tiles_of(256, 256);
+    if (mean >= 160 && (large >= 4 * kUnits || (H >= 4096 && large >= 192 && large <= kUnits)))
+        return tiles<256, 256, 2, 4, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                        out_stride_bytes, wide, stream);
+    if (mean >= 40 && tiles_of(128, 128) >= 300)
+        return tiles<128, 128, 2, 2, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                        out_stride_bytes, wide, stream);
+    return tiles<64, 128, 2, 2, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                   out_stride_bytes, wide, stream);
 }
 
 }  // namespace moe

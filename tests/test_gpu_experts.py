@@ -456,6 +456,9 @@ PRODUCTS = [  # rows of each group, H, O
     ([200, 170, 300, 0] * 4, 1056, 4100), ([50] * 30, 544, 2500), ([300, 90, 0, 260] * 8, 512, 300), ([7] * 64, 544, 1500),
     ([7] * 64, 1024, 700), ([1000], 768, 6200), ([65, 0, 64, 63], 2048, 510), ([5, 1, 0, 2], 7168, 130), ([40] * 20, 608, 90), ([513, 0, 1023], 992, 514),
     ([700, 690], 480, 9000), ([90] * 20, 96, 1300), ([30000, 20000], 32, 66), ([2, 1], 32, 65536), ([50, 3] * 8, 224, 700),
+    ([30, 31], 1024, 3840), ([30, 31], 544, 3842), ([40, 44, 30, 46], 1056, 2400), ([40, 44, 0, 46], 1120, 2402), ([40, 44, 30, 46], 2080, 7200),
+    ([60, 1, 64, 33], 2144, 7202), ([90, 60, 100, 30], 4128, 7200), ([127, 1, 128, 5], 4192, 7202), ([400, 380], 4096, 12960), ([500, 290], 4128, 12801),
+    ([7400, 7500, 7690, 7410], 96, 1680),
 ]
 
 
@@ -509,13 +512,16 @@ def test_product_free_scales(moe, counts, H, O):
     assert np.all(err <= H * 2.0**-23 * magnitude + 2.0**-8 * np.abs(exact))
 
 
-@pytest.mark.parametrize("H", [160, 544, 1056, 2080])
-@pytest.mark.parametrize("counts", [[2, 3], [9, 14], [40, 30], [300, 100]])
-def test_product_nan_blocks(moe, counts, H):
+NAN_CASES = [(H, counts, O) for H in (160, 544, 1056, 2080) for counts in ([2, 3], [9, 14], [40, 30], [300, 100]) for O in (48, 3900)]
+NAN_CASES += [(1056, [40, 44, 30, 46], 2400), (2080, [40, 44, 30, 46], 7200), (4128, [90, 60, 100, 30], 7200), (4128, [400, 380], 12801)]
+
+
+@pytest.mark.parametrize("H,counts,O", NAN_CASES)
+def test_product_nan_blocks(moe, H, counts, O):
     """A NaN scale of a row makes that row NaN and no other; one of a weight row its column of its group. The last
     block (H is no multiple of the tile's depth) as well as the first."""
     rng = np.random.default_rng(12)
-    O, G, end = 48, len(counts), H // 32 - 1
+    G, end = len(counts), H // 32 - 1
     base = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
     R = int(base[-1])
     a, w = mx_random(rng, (R, H), -1, 1), mx_random(rng, (G, O, H), -1, 1)
