@@ -863,86 +863,94 @@ class MxRows(NamedTuple):
 # The current device's index without torch.cuda's lazy initialisation check (tensors on a device exist already).
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
+# These calls take about as long on the host as a small kernel on the GPU, so each argument is first tested by the
+# cheapest accesses that accept it; the reason for a refusal is looked for only after that. Devices are indices here.
+_Tensor, _empty = torch.Tensor, torch.empty
+_bf16, _fp32, _int32, _uint8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
 
 def _launch(dev, stream, fn, *args):
     """fn(*args, stream handle) with dev as the current device: a null stream is the current device's."""
-    if dev.index == _current_device():
-        rc = fn(*args, _stream(dev, stream))
+    if dev == _current_device():
+        rc = fn(*args, _raw_stream(dev) if stream is None and _raw_stream is not None
+                else _stream(torch.device("cuda", dev), stream))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream(dev, stream))
+            rc = fn(*args, _stream(torch.device("cuda", dev), stream))
     if rc:
         _check(rc)
 
 
-def _out(shape, dtype, dev, stream):
+def _out(rows, columns, dtype, dev, stream):
     """A new output for a call on `stream`, from that stream's memory (the current stream's without one)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _empty(rows, columns, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _empty(rows, columns, dtype=dtype, device=dev)
 
 
 def _dense(t, name, dtype, shape, dev):
-    """Checks a contiguous device tensor of exactly this shape; the cheap test first, the reason after."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index and t.shape == shape
+    """Pointer of a contiguous device tensor of exactly this shape."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
             and t.is_contiguous()):
         return t.data_ptr()
-    _need(t, name, dtype, len(shape), dev)
+    _need(t, name, dtype, len(shape), torch.device("cuda", dev))
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _matrix(t, name, dtype):
     """Device and shape of a two-dimensional device tensor of this type, whatever its strides."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    dev, shape = t.get_device(), t.shape
+    if dev < 0:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dtype is not dtype or t.dim() != 2:
-        raise ValueError(f"{name} must be {dtype} with 2 dims, got {t.dtype} {tuple(t.shape)}")
-    return t.device, t.size(0), t.size(1)
+    if t.dtype is not dtype or len(shape) != 2:
+        raise ValueError(f"{name} must be {dtype} with 2 dims, got {t.dtype} {tuple(shape)}")
+    return dev, shape[0], shape[1]
 
 
 def _width(t, name):
     """The row length of a two-dimensional tensor; type and device are checked with the rest of it."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
-    return t.size(1)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have 2 dims, got {len(shape)}")
+    return shape[1]
 
 
 def _rows_arg(t, name, H, dev):
     """Pointer, row stride in bytes and row count of bf16 rows: a [R, H] tensor whose rows are each
     contiguous, at any stride."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != dev.index:
-        raise ValueError(f"{name} must be a device tensor on {dev}, got {t.device}")
-    if t.dtype is not torch.bfloat16 or t.dim() != 2 or t.size(1) != H:
-        raise ValueError(f"{name} must be bfloat16 [rows, {H}], got {t.dtype} {tuple(t.shape)}")
-    n = t.size(0)
-    if n > 1:
-        step, col = t.stride()
-        if col != 1 or step < H:
-            raise ValueError(f"{name} must have contiguous rows that do not overlap")
-        return t.data_ptr(), 2 * step, n
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor on cuda:{dev}, got {t.device}")
+    shape = t.shape
+    if t.dtype is not _bf16 or len(shape) != 2 or shape[1] != H:
+        raise ValueError(f"{name} must be bfloat16 [rows, {H}], got {t.dtype} {tuple(shape)}")
+    n = shape[0]
     if n == 0:
         raise ValueError(f"{name} has no rows")
-    if t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), 2 * H, 1
+    if t.is_contiguous():
+        return t.data_ptr(), 2 * H, n
+    step, col = t.stride()
+    if col != 1 or n > 1 and step < H:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), 2 * step if n > 1 else 2 * H, n
 
 
-def _table_args(slot_idx, topk_weights=None):
-    """Device, S and K of the table, with the weights checked against it."""
+def _table_arg(slot_idx):
+    """Device, S, K and pointer of the table."""
+    if isinstance(slot_idx, _Tensor) and slot_idx.dtype is _int32 and slot_idx.is_contiguous():
+        dev, shape = slot_idx.get_device(), slot_idx.shape
+        if dev >= 0 and len(shape) == 2:
+            return dev, shape[0], shape[1], slot_idx.data_ptr()
     _need(slot_idx, "slot_idx", torch.int32, 2)
-    dev, shape = slot_idx.device, slot_idx.shape
-    if topk_weights is not None:
-        _dense(topk_weights, "topk_weights", torch.float32, shape, dev)
-    return dev, shape[0], shape[1]
+    raise ValueError("slot_idx must be a device tensor")
 
 
 def _mx_width(H, format):
@@ -957,24 +965,21 @@ def _mx_width(H, format):
 
 def _mx_args(mx, name, rows, H, format, dev):
     codes, scales = mx
-    return (_dense(codes, f"{name}.codes", torch.uint8, (rows, _mx_width(H, format)), dev),
-            _dense(scales, f"{name}.scales", torch.uint8, (rows, H // 32), dev))
+    return (_dense(codes, f"{name}.codes", _uint8, (rows, _mx_width(H, format)), dev),
+            _dense(scales, f"{name}.scales", _uint8, (rows, H // 32), dev))
 
 
 def _gradient_outs(S, K, H, rows, topk_weights, d_expert_out, d_topk_weights, dev, stream):
     if d_expert_out is None:
-        d_expert_out = _out((rows, H), torch.bfloat16, dev, stream)
+        d_expert_out = _out(rows, H, _bf16, dev, stream)
     d_ptr, d_stride, d_count = _rows_arg(d_expert_out, "d_expert_out", H, dev)
     if d_count != rows:
         raise ValueError(f"d_expert_out must have {rows} rows")
     if d_topk_weights is None:
-        if stream is None:
-            d_topk_weights = torch.empty_like(topk_weights)
-        else:
-            d_topk_weights = _out((S, K), torch.float32, dev, stream)
+        d_topk_weights = torch.empty_like(topk_weights) if stream is None else _out(S, K, _fp32, dev, stream)
         return d_expert_out, d_ptr, d_stride, d_topk_weights, d_topk_weights.data_ptr()
     return (d_expert_out, d_ptr, d_stride, d_topk_weights,
-            _dense(d_topk_weights, "d_topk_weights", torch.float32, (S, K), dev))
+            _dense(d_topk_weights, "d_topk_weights", _fp32, (S, K), dev))
 
 
 def moe_combine_backward(dy, expert_out, slot_idx, topk_weights, d_expert_out=None, d_topk_weights=None,
@@ -982,59 +987,62 @@ def moe_combine_backward(dy, expert_out, slot_idx, topk_weights, d_expert_out=No
     """The combine's gradient: (d_expert_out, d_topk_weights) of dy (bf16 [S, H]) with the forward's
     expert_out (bf16 [R, H], any row stride), slot_idx and topk_weights. Rows of d_expert_out that no
     entry names keep their contents (undefined where it is allocated here)."""
-    dev, S, K = _table_args(slot_idx, topk_weights)
+    dev, S, K, table = _table_arg(slot_idx)
+    weights = _dense(topk_weights, "topk_weights", _fp32, (S, K), dev)
     H = _width(dy, "dy")
-    dy_ptr = _dense(dy, "dy", torch.bfloat16, (S, H), dev)
+    dy_ptr = _dense(dy, "dy", _bf16, (S, H), dev)
     ptr, stride, rows = _rows_arg(expert_out, "expert_out", H, dev)
     d_expert_out, d_ptr, d_stride, d_topk_weights, dw_ptr = _gradient_outs(S, K, H, rows, topk_weights,
                                                                            d_expert_out, d_topk_weights, dev, stream)
-    _launch(dev, stream, _lib.moe_combine_backward, dy_ptr, ptr, stride, rows, slot_idx.data_ptr(),
-            topk_weights.data_ptr(), S, H, K, d_ptr, d_stride, dw_ptr)
+    _launch(dev, stream, _lib.moe_combine_backward, dy_ptr, ptr, stride, rows, table, weights, S, H, K, d_ptr,
+            d_stride, dw_ptr)
     return d_expert_out, d_topk_weights
 
 
 def moe_combine_checkpoint(expert_out, slot_idx, topk_weights, y=None, checkpoint=None, stream=None):
     """moe_combine that also keeps the rows it reads in 8 bits: (y, MxRows in MOE_MX_E4M3 [R, H]). Rows that
     no entry names keep their contents (undefined where the checkpoint is allocated here)."""
-    dev, S, K = _table_args(slot_idx, topk_weights)
+    dev, S, K, table = _table_arg(slot_idx)
+    weights = _dense(topk_weights, "topk_weights", _fp32, (S, K), dev)
     H = _width(expert_out, "expert_out")
     ptr, stride, rows = _rows_arg(expert_out, "expert_out", H, dev)
     if y is None:
-        y = _out((S, H), torch.bfloat16, dev, stream)
-    y_ptr = _dense(y, "y", torch.bfloat16, (S, H), dev)
+        y = _out(S, H, _bf16, dev, stream)
+    y_ptr = _dense(y, "y", _bf16, (S, H), dev)
     if checkpoint is None:
         checkpoint = _mx_empty(rows, H, MOE_MX_E4M3, dev, stream)
     codes, scales = _mx_args(checkpoint, "checkpoint", rows, H, MOE_MX_E4M3, dev)
-    _launch(dev, stream, _lib.moe_combine_checkpoint, ptr, stride, rows, slot_idx.data_ptr(),
-            topk_weights.data_ptr(), S, H, K, y_ptr, codes, scales)
+    _launch(dev, stream, _lib.moe_combine_checkpoint, ptr, stride, rows, table, weights, S, H, K, y_ptr, codes,
+            scales)
     return y, MxRows(*checkpoint)
 
 
 def moe_combine_backward_mx(dy, checkpoint, slot_idx, topk_weights, d_expert_out=None, d_topk_weights=None,
                             stream=None):
     """moe_combine_backward with the rows of a checkpoint (MxRows in MOE_MX_E4M3) in place of expert_out."""
-    dev, S, K = _table_args(slot_idx, topk_weights)
+    dev, S, K, table = _table_arg(slot_idx)
+    weights = _dense(topk_weights, "topk_weights", _fp32, (S, K), dev)
     H = _width(dy, "dy")
-    dy_ptr = _dense(dy, "dy", torch.bfloat16, (S, H), dev)
+    dy_ptr = _dense(dy, "dy", _bf16, (S, H), dev)
     _, rows, _ = _matrix(checkpoint[1], "checkpoint.scales", torch.uint8)
     codes, scales = _mx_args(checkpoint, "checkpoint", rows, H, MOE_MX_E4M3, dev)
     d_expert_out, d_ptr, d_stride, d_topk_weights, dw_ptr = _gradient_outs(S, K, H, rows, topk_weights,
                                                                            d_expert_out, d_topk_weights, dev, stream)
-    _launch(dev, stream, _lib.moe_combine_backward_mx, dy_ptr, codes, scales, rows, slot_idx.data_ptr(),
-            topk_weights.data_ptr(), S, H, K, d_ptr, d_stride, dw_ptr)
+    _launch(dev, stream, _lib.moe_combine_backward_mx, dy_ptr, codes, scales, rows, table, weights, S, H, K, d_ptr,
+            d_stride, dw_ptr)
     return d_expert_out, d_topk_weights
 
 
 def moe_dispatch_backward(d_rows, slot_idx, dx=None, stream=None):
     """The dispatch's gradient: dx[t] = bf16(sum_k d_rows[slot_idx[t, k]]) of d_rows (bf16 [R, H], any row
     stride), fp32 accumulation."""
-    dev, S, K = _table_args(slot_idx)
+    dev, S, K, table = _table_arg(slot_idx)
     H = _width(d_rows, "d_rows")
     ptr, stride, rows = _rows_arg(d_rows, "d_rows", H, dev)
     if dx is None:
-        dx = _out((S, H), torch.bfloat16, dev, stream)
-    dx_ptr = _dense(dx, "dx", torch.bfloat16, (S, H), dev)
-    _launch(dev, stream, _lib.moe_dispatch_backward, ptr, stride, rows, slot_idx.data_ptr(), S, H, K, dx_ptr)
+        dx = _out(S, H, _bf16, dev, stream)
+    dx_ptr = _dense(dx, "dx", _bf16, (S, H), dev)
+    _launch(dev, stream, _lib.moe_dispatch_backward, ptr, stride, rows, table, S, H, K, dx_ptr)
     return dx
 
 
@@ -1046,14 +1054,13 @@ def moe_mx_row_bytes(H, format):
 
 
 def _mx_empty(rows, H, format, dev, stream):
-    return MxRows(_out((rows, _mx_width(H, format)), torch.uint8, dev, stream),
-                  _out((rows, H // 32), torch.uint8, dev, stream))
+    return MxRows(_out(rows, _mx_width(H, format), _uint8, dev, stream), _out(rows, H // 32, _uint8, dev, stream))
 
 
 def _count_arg(num_rows, dev):
     if num_rows is None:
         return None
-    _need(num_rows, "num_rows", torch.int32, device=dev)
+    _need(num_rows, "num_rows", torch.int32, device=torch.device("cuda", dev))
     if num_rows.numel() < 1:
         raise ValueError("num_rows must hold a count")
     return num_rows.data_ptr()
@@ -1081,7 +1088,7 @@ def moe_mx_dequantize(mx, format, num_rows=None, out=None, stream=None):
     H = 32 * blocks
     codes, scales = _mx_args(mx, "mx", n, H, format, dev)
     if out is None:
-        out = _out((n, H), torch.bfloat16, dev, stream)
+        out = _out(n, H, _bf16, dev, stream)
     count = _count_arg(num_rows, dev)
     if n:
         ptr, stride, rows = _rows_arg(out, "out", H, dev)
@@ -1100,20 +1107,21 @@ def moe_mx_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=Non
     H = 32 * blocks
     a_codes, a_scales = _mx_args(a, "a", n, H, MOE_MX_E2M1, dev)
     w_codes, w_scales = w
-    if not isinstance(w_codes, torch.Tensor) or w_codes.dim() != 3:
+    shape = w_codes.shape if isinstance(w_codes, _Tensor) else ()
+    if len(shape) != 3:
         raise ValueError(f"w must be codes [G, O, {H // 2}] and scales [G, O, {blocks}]")
-    G, O = w_codes.size(0), w_codes.size(1)
+    G, O, _ = shape
     wc_ptr = _dense(w_codes, "w.codes", torch.uint8, (G, O, H // 2), dev)
     ws_ptr = _dense(w_scales, "w.scales", torch.uint8, (G, O, blocks), dev)
     base_ptr = _dense(group_base, "group_base", torch.int32, (G + 1,), dev)
     width = O // 2 if epilogue == MOE_MX_GATED else O
     if out is None:
-        out = _out((n, width), torch.bfloat16, dev, stream)
+        out = _out(n, width, _bf16, dev, stream)
         out_stride = 2 * width
     else:
-        if (not isinstance(out, torch.Tensor) or out.dtype is not torch.bfloat16 or out.get_device() != dev.index
+        if (not isinstance(out, torch.Tensor) or out.dtype is not torch.bfloat16 or out.get_device() != dev
                 or out.shape != (n, width)):
-            raise ValueError(f"out must be bfloat16 {(n, width)} on {dev}")
+            raise ValueError(f"out must be bfloat16 {(n, width)} on cuda:{dev}")
         if width > 1 and out.stride(1) != 1 or n > 1 and out.stride(0) < width:
             raise ValueError("out must have contiguous rows that do not overlap")
         out_stride = 2 * out.stride(0) if n > 1 else 2 * width
