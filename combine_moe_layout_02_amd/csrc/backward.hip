@@ -21,7 +21,10 @@ using namespace mx;
 
 constexpr int kLoadPolicy = 2;              // nt: rows are read once
 constexpr int kStorePolicy = 1 | 16;        // sc0 sc1
-constexpr int kStreamPolicy = 1 | 16 | 2;   // sc0 sc1 nt: rows stream to HBM
+constexpr int kStreamPolicy = 1 | 16 | 2;   // sc0 sc1 nt: a checkpoint's codes stream to HBM
+// nt: gradient rows (S = 4096, K = 8; bf16, then from a checkpoint: H = 7168 211 and 166 us, with kStreamPolicy 217
+// and 169, write-back 214 and 175; H = 2048 61 and 47.8, 62.7 and 48.9; 1024 tokens of 7168 53 and 56).
+constexpr int kRowPolicy = 2;
 // 16-byte vectors of a part, a lane each. S = 4096, H = 7168, K = 8: the dispatch's gradient takes 87.9 us with
 // 32, 89.1 with 64 and 90.2 with 128; the checkpointed combine 164, 153 and 153 (a row's codes are half as wide).
 template <bool KEEP>
@@ -53,10 +56,11 @@ __device__ inline float wave_sums(float (&v)[N]) {
     return s;
 }
 
-// grid = S; workgroup t takes token t, its lanes vectors threadIdx.x, + blockDim.x, ... of the rows (at most
-// two rounds: nvec <= 2048 and 1024 lanes; a lane a vector where they suffice, so that all of a token's loads are
-// under way at once. S = 4096, K = 8: 214 us at H = 7168 and 114 at H = 4096; with 64 lanes and more rounds 205 and
-// 153, with 256 lanes 210 and 124; 64 tokens 9 us, 20 and 10).
+// grid = S; workgroup t takes token t, its lanes vectors threadIdx.x, + blockDim.x, ... of the rows (at most two
+// rounds: nvec <= 2048 and 1024 lanes; a lane a vector where they suffice, so that all of a token's loads are
+// under way at once. S = 4096, K = 8: 211 to 217 us at H = 7168 and 112 at H = 4096; with 64 lanes and more rounds 205
+// and 153, with 256 lanes 210 and 124; 64 tokens 9 us, 20 and 10). An eighth of the tokens in order for each XCD
+// takes 202 us at H = 7168, but 115 at H = 4096, and 228 for 218 with 8192 tokens there.
 // MX: the rows are E4M3 codes and scales (stride = H). d_weights: a lane's sum over its values in order, the wave's
 // lanes by a fixed tree, the waves in order, all in fp32.
 template <int KMAX, bool MX>
@@ -121,7 +125,7 @@ __global__ __launch_bounds__(1024) void combine_backward_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i) out[i] = bf16_pair(w[k] * gf[2 * i], w[k] * gf[2 * i + 1]);
             __builtin_amdgcn_raw_buffer_store_b128(out, rsrc(d_rows + slot[k] * d_stride, row_bytes),
-                                                   v << 4, 0, kStreamPolicy);
+                                                   v << 4, 0, kRowPolicy);
         }
     }
     const float s = wave_sums<KMAX>(sum);
