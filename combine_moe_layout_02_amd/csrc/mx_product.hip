@@ -23,21 +23,40 @@ __device__ inline f32x4 mfma_byte(const i32x4 &a, int a_scale, const i32x4 &b, i
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, S, a_scale, S, b_scale);
 }
 
+// The rows [lo, hi) of groups g0 .. g0 + 63, one a lane (none past the last group). A base below an earlier one
+// counts as that one, so that the groups' rows are disjoint and their tiles as many as the grid's arithmetic assumes,
+// whatever the bases are. `reached` is where the groups before g0 end, and then where these do. Every lane of a
+// wave calls this; bases that ascend, the same for the whole wave, need no running maximum.
+__device__ inline void group_rows(const int32_t *__restrict__ base, int G, int a_rows, int g0, int &reached, int &lo,
+                                  int &hi) {
+    const int lane = threadIdx.x & 63;
+    lo = min(max(base[min(g0 + lane, G)], 0), a_rows);
+    hi = min(max(base[min(g0 + lane + 1, G)], 0), a_rows);
+    if (__any(hi < lo || lo < reached)) {
+        hi = max(hi, lo);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int u = __shfl_up(hi, d, 64);
+            if (lane >= d) hi = max(hi, u);
+        }
+        hi = max(hi, reached);
+        const int prev = __shfl_up(hi, 1, 64);
+        lo = max(lo, lane > 0 ? prev : reached);
+    }
+    reached = __shfl(hi, 63, 64);
+}
+
 // The rows [first, last) that tile number `tile` covers, TM rows at most, and their group; false when there
 // are fewer tiles. Groups' tiles follow one another; every lane of a wave calls this and gets the same.
 template <int TM>
 __device__ inline bool find_rows(const int32_t *__restrict__ base, int G, int64_t a_rows, int tile,
                                  int &group, int64_t &first, int64_t &last) {
     const int lane = threadIdx.x & 63;
-    int before = 0;
+    int before = 0, reached = 0;
     for (int g0 = 0; g0 < G; g0 += 64) {
-        const int g = g0 + lane;
-        int64_t lo = 0, hi = 0;
-        if (g < G) {
-            lo = min(max((int64_t)base[g], (int64_t)0), a_rows);
-            hi = min(max((int64_t)base[g + 1], lo), a_rows);
-        }
-        const int tiles = (int)((hi - lo + TM - 1) / TM);
+        int lo, hi;
+        group_rows(base, G, (int)a_rows, g0, reached, lo, hi);
+        const int tiles = (hi - lo + TM - 1) / TM;
         int incl = tiles;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -48,7 +67,7 @@ __device__ inline bool find_rows(const int32_t *__restrict__ base, int G, int64_
         if (here) {
             const int src = __ffsll((unsigned long long)here) - 1;
             const int skipped = before + __shfl(incl - tiles, src, 64);
-            const int64_t glo = __shfl((int)lo, src, 64), ghi = __shfl((int)hi, src, 64);
+            const int64_t glo = __shfl(lo, src, 64), ghi = __shfl(hi, src, 64);
             group = g0 + src;
             first = glo + (int64_t)(tile - skipped) * TM;
             last = min(first + TM, ghi);
@@ -115,28 +134,15 @@ struct TileTable {
     int32_t lo[MOE_MAX_EXPERTS], hi[MOE_MAX_EXPERTS], end[MOE_MAX_EXPERTS];
 };
 
-// One wave fills the table for row tiles of TM. A base below an earlier one counts as that one, so that the
-// groups' rows are disjoint and their tiles as many as the grid's arithmetic assumes, whatever the bases are.
+// One wave fills the table for row tiles of TM.
 template <int TM>
 __device__ inline void fill_table(TileTable &table, const int32_t *__restrict__ base, int G, int64_t a_rows) {
     const int lane = threadIdx.x & 63;
     int before = 0, reached = 0;
     for (int g0 = 0; g0 < G; g0 += 64) {
         const int g = g0 + lane;
-        int lo = 0, hi = 0;
-        if (g < G) {
-            lo = min(max(base[g], 0), (int)a_rows);
-            hi = min(max(base[g + 1], lo), (int)a_rows);
-        }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int u = __shfl_up(hi, d, 64);
-            if (lane >= d) hi = max(hi, u);
-        }
-        hi = max(hi, reached);
-        const int prev = __shfl_up(hi, 1, 64);
-        lo = max(lo, lane > 0 ? prev : reached);
-        reached = __shfl(hi, 63, 64);
+        int lo, hi;
+        group_rows(base, G, (int)a_rows, g0, reached, lo, hi);
         int incl = (hi - lo + TM - 1) / TM;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {

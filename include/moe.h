@@ -622,8 +622,8 @@ int moe_combine_backward_mx(const void *dy, const void *codes, const void *scale
  * In:  a_codes, a_scales  MX E2M1 rows [a_rows, H] (a_rows in [0, MOE_MAX_OUT_ROWS]; 0 enqueues nothing).
  *      group_base         DEVICE int32 [G + 1], ascending, read on the device: expert_slot_base of the layout, or
  *                         a part of it (expert_slot_base + first, with the weights of G experts from there).
- *                         Values are clamped to [0, a_rows]. Empty groups are fine. Bases that descend leave
- *                         it open which of the rows in [0, a_rows) are computed.
+ *                         Values are clamped to [0, a_rows]. Empty groups are fine. A base below an earlier one
+ *                         counts as that one, so every row belongs to one group at most.
  *      G                  in [1, MOE_MAX_EXPERTS].
  *      w_codes, w_scales  MX E2M1 rows [G, O, H]; O in [1, MOE_MAX_OUTPUTS], even for MOE_MX_GATED
  *                         (MOE_ERR_UNSUPPORTED otherwise).

@@ -1,0 +1,56 @@
+"""GPU tests of the calls around the experts at their edges: values at the ends of the formats' ranges, gates far
+below zero, bases that descend, weights of more rows than a layout has, and calls given a stream.
+
+Tolerances, derived before the first run, are written at each test; the oracle is numpy in 64 bits.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from test_gpu_experts import (DEV, E2M1, E4M3, bf16_bits, bf16_dev, bits, moe, mx_random, note, poison, same_bits,
+                              spread_rows, table, to_dev, weight_error_bound)  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- bases that descend
+
+
+def disjoint(base, R):
+    """The rows [lo, hi) of each group where a base below an earlier one counts as that one."""
+    b, reached, out = np.clip(base, 0, R), 0, []
+    for g in range(len(base) - 1):
+        lo, reached = max(b[g], reached), max(b[g], b[g + 1], reached)
+        out.append((lo, reached))
+    return out
+
+
+DESCENDING = [  # R, G, O, H: the waves that share H; four pairs of 32 x 64 and of 64 x 64; two pairs of 64 x 128
+    (40, 6, 24, 160), (500, 8, 100, 544), (640, 32, 700, 544), (1600, 32, 300, 544), (3000, 40, 900, 544), (900, 130, 8, 64),
+]
+
+
+@pytest.mark.parametrize("R,G,O,H", DESCENDING)
+def test_descending_bases_give_disjoint_groups(moe, R, G, O, H):  # noqa: F811
+    """Each row of the groups' disjoint reading has the product with its own group's weights, whichever kernel
+    runs, and no other row is touched. Exact sums: bit for bit."""
+    rng = np.random.default_rng(R + O)
+    note("descending bases", R, G, O, H)
+    a, w = mx_random(rng, (R, H), -1, 1), mx_random(rng, (G, O, H), -1, 1)
+    av, wv = oracle.mx_values(*a, E2M1), oracle.mx_values(*w, E2M1)
+    ascending = np.linspace(0, R - 3, G + 1).astype(np.int32)
+    swapped, back, random = ascending.copy(), ascending.copy(), rng.integers(-5, R + 5, G + 1).astype(np.int32)
+    swapped[1], swapped[2] = swapped[2], swapped[1]
+    back[G // 2] = 0
+    for base in (ascending, swapped, back, random, random[::-1].copy(), ascending[::-1].copy()):
+        want, inside = np.zeros((R, O)), np.zeros(R, dtype=bool)
+        for g, (lo, hi) in enumerate(disjoint(base, R)):
+            want[lo:hi] = av[lo:hi] @ wv[g].T
+            inside[lo:hi] = True
+        out = poison((R, O), torch.bfloat16)
+        moe.moe_mx_product(moe.MxRows(*map(to_dev, a)), moe.MxRows(*map(to_dev, w)), to_dev(base), out=out)
+        got = bf16_bits(out)
+        same_bits(got[inside], bits(want[inside].astype(np.float32)), "rows of the groups")
+        assert np.all(got[~inside] == 0xABAB)
