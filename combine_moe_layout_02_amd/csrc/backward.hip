@@ -25,6 +25,9 @@ constexpr int kStreamPolicy = 1 | 16 | 2;   // sc0 sc1 nt: a checkpoint's codes 
 // nt: gradient rows (S = 4096, K = 8; bf16, then from a checkpoint: H = 7168 211 and 166 us, with kStreamPolicy 217
 // and 169, write-back 214 and 175; H = 2048 61 and 47.8, 62.7 and 48.9; 1024 tokens of 7168 53 and 56).
 constexpr int kRowPolicy = 2;
+// A checkpoint's values are taken at half their size, and the sums doubled: a block's largest can be 2^128, past
+// fp32, whose product with a small or zero gradient is finite.
+constexpr float kHalf = 0.5f;
 // 16-byte vectors of a part, a lane each. S = 4096, H = 7168, K = 8: the dispatch's gradient takes 87.9 us with
 // 32, 89.1 with 64 and 90.2 with 128; the checkpointed combine 164, 153 and 153 (a row's codes are half as wide).
 template <bool KEEP>
@@ -111,7 +114,7 @@ __global__ __launch_bounds__(1024) void combine_backward_kernel(
             if (slot[k] < 0) continue;
             float xf[8];
             if constexpr (MX) {
-                decode_e4m3(u32x2{x[k][0], x[k][1]}, scale_value(byte[k]), xf);
+                decode_e4m3(u32x2{x[k][0], x[k][1]}, kHalf * scale_value(byte[k]), xf);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -137,7 +140,7 @@ __global__ __launch_bounds__(1024) void combine_backward_kernel(
         const int nwaves = (blockDim.x + 63) >> 6;
         for (int i = 0; i < nwaves; ++i) total += partial[i][threadIdx.x];
         const int64_t sk = slot_idx[t * K + threadIdx.x];
-        d_weights[t * K + threadIdx.x] = sk >= 0 && sk < nrows ? total : 0.0f;
+        d_weights[t * K + threadIdx.x] = sk >= 0 && sk < nrows ? total * (MX ? 1.0f / kHalf : 1.0f) : 0.0f;
     }
 }
 

@@ -596,7 +596,8 @@ int moe_mx_dequantize(const void *codes, const void *scales, const int32_t *num_
  *      (MOE_MX_E4M3, as moe_mx_quantize makes them) of every row that an entry of slot_idx names, from the
  *      one read of the rows that the combine makes. H % 32 == 0. codes uint8 [expert_rows, H] (16-byte
  *      aligned), scales uint8 [expert_rows, H / 32]; rows that no entry names keep their contents.
- * moe_combine_backward_mx: moe_combine_backward with the values of such rows in place of expert_out.
+ * moe_combine_backward_mx: moe_combine_backward with the values of such rows in place of expert_out (2^128, past
+ *      fp32, counts as itself: its products with dy are summed).
  * Each enqueues one kernel. */
 int moe_combine_checkpoint(const void *expert_out, int64_t row_stride_bytes, int64_t expert_rows,
                            const int32_t *slot_idx, const float *topk_weights, int32_t S,

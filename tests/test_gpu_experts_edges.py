@@ -54,3 +54,28 @@ def test_descending_bases_give_disjoint_groups(moe, R, G, O, H):  # noqa: F811
         got = bf16_bits(out)
         same_bits(got[inside], bits(want[inside].astype(np.float32)), "rows of the groups")
         assert np.all(got[~inside] == 0xABAB)
+
+
+# ---------------------------------------------------------------- the ends of the formats' ranges
+
+
+@pytest.mark.parametrize("S,K,H", [(5, 2, 64), (40, 5, 2080), (9, 16, 8224)])
+def test_checkpoint_gradient_of_the_largest_values(moe, S, K, H):  # noqa: F811
+    """Rows that hold bf16's lowest and highest finite values: E4M3 holds them as 2^128, which fp32 does not, but
+    their products with dy, zeros among it, are finite, and so is the gradient. The bound of the gradient's tests."""
+    rng = np.random.default_rng(H)
+    slot = table(rng, S, K, 2 * K, 0.1)
+    R = S * K
+    rows, w = spread_rows(rng, R, H), rng.random((S, K), dtype=np.float32)
+    dy = bits(rng.standard_normal((S, H)) * 2.0**-40)
+    rows[:, 7], rows[:, 40], rows[::2, 50] = 0xFF7F, 0x7F7F, 0x7F70
+    dy[:, 7] = 0
+    codes, scales = oracle.mx_quantize(rows, E4M3)
+    values = oracle.mx_values(codes, scales, E4M3)
+    assert np.abs(values).max() == 2.0**128
+    y, kept = moe.moe_combine_checkpoint(bf16_dev(rows), to_dev(slot), to_dev(w))
+    got = moe.moe_combine_backward_mx(bf16_dev(dy), kept, to_dev(slot), to_dev(w), d_expert_out=poison((R, H), torch.bfloat16))
+    want, want_w, magnitude = oracle.combine_backward(dy, values, slot, w, np.full((R, H), 0xABAB))
+    same_bits(bf16_bits(got[0]), want, "d_rows")
+    assert np.isfinite(want_w).all()
+    assert np.all(np.abs(got[1].cpu().numpy() - want_w) <= weight_error_bound(magnitude))
