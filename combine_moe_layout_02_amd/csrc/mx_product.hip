@@ -78,12 +78,15 @@ __device__ inline bool find_rows(const int32_t *__restrict__ base, int G, int64_
     return false;
 }
 
-// v / (1 + exp(-v)) by the hardware's exp2 and reciprocal (within 2^-16 relative for |v| <= 88, far below bf16's
-// half step of 2^-8). Far below zero the denominator's reciprocal would be subnormal and come out as zero:
-// both sides are scaled there.
-__device__ inline float silu(float v) {
-    const float s = v < -40.0f ? 0x1p-32f : 1.0f;
-    return (v * s) * __builtin_amdgcn_rcpf((1.0f + __expf(-v)) * s);
+// silu(v) * up with silu(v) = v / (1 + exp(-v)), by the hardware's exp2 and reciprocal (within 2^-14 relative, far below
+// bf16's half step of 2^-8). Far below zero, where exp(-v) leaves fp32's range and 1 + exp(v) is 1, silu(v) = v * exp(v)
+// is taken as two factors, h = exp(v / 2) and v * h, and up goes between them: the result is right wherever h is a
+// normal number (v >= -174), also where silu(v) alone would be none.
+__device__ inline float silu_times(float v, float up) {
+    const bool far = v < -40.0f;
+    const float e = __builtin_amdgcn_exp2f(v * (far ? 0.72134752f : -1.44269504f));  // log2(e) / 2, -log2(e)
+    const float f = far ? e : __builtin_amdgcn_rcpf(1.0f + e);
+    return (v * f) * (far ? e * up : up);
 }
 
 __device__ inline __amdgpu_buffer_rsrc_t rsrc(const void *base, int64_t bytes) {
@@ -428,7 +431,7 @@ __global__ __launch_bounds__(64 * WMC * WNC) void product_tile_kernel(
                     float f[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        f[e] = GATED ? silu(acc[i][j + k][e]) * acc[i][(j + k + OF) % NI][e] : acc[i][j + k][e];
+                        f[e] = GATED ? silu_times(acc[i][j + k][e], acc[i][(j + k + OF) % NI][e]) : acc[i][j + k][e];
                     v[k][0] = bf16_pair(f[0], f[1]);
                     v[k][1] = bf16_pair(f[2], f[3]);
                 }
@@ -567,7 +570,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void product_small_kernel(
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int o = o0 + 16 * wave + 4 * q + e;
-        if (o < width) dst[o] = (uint16_t)bf16_pair(GATED ? silu(sum[e]) * up[e] : sum[e], 0.0f);
+        if (o < width) dst[o] = (uint16_t)bf16_pair(GATED ? silu_times(sum[e], up[e]) : sum[e], 0.0f);
     }
 }
 

@@ -617,8 +617,9 @@ int moe_combine_backward_mx(const void *dy, const void *codes, const void *scale
  *   MOE_MX_PLAIN: out[r, o] = bf16(c[r, o]), o in [0, O)
  *   MOE_MX_GATED: out[r, o] = bf16(silu(c[r, o]) * c[r, O/2 + o]), o in [0, O/2), silu(v) = v / (1 + exp(-v)):
  *                 the weights' first O/2 rows are the gate, the rest the up projection
- * Sums are accumulated in fp32 by the matrix cores, the activation is taken in fp32, and the result is
- * rounded once. Rows of a group do not influence one another (a NaN block stays in its row).
+ * Sums are accumulated in fp32 by the matrix cores, the activation is taken in fp32 (for a gate below -174 it may
+ * count as 0), and the result is rounded once. Rows of a group do not influence one another (a NaN block stays in
+ * its row).
  *
  * In:  a_codes, a_scales  MX E2M1 rows [a_rows, H] (a_rows in [0, MOE_MAX_OUT_ROWS]; 0 enqueues nothing).
  *      group_base         DEVICE int32 [G + 1], ascending, read on the device: expert_slot_base of the layout, or

@@ -79,3 +79,69 @@ def test_checkpoint_gradient_of_the_largest_values(moe, S, K, H):  # noqa: F811
     same_bits(bf16_bits(got[0]), want, "d_rows")
     assert np.isfinite(want_w).all()
     assert np.all(np.abs(got[1].cpu().numpy() - want_w) <= weight_error_bound(magnitude))
+
+
+# ---------------------------------------------------------------- gates far below zero, and not finite ones
+
+
+def gated(c):
+    """silu(gate) * up of exact sums [R, O], as the definition has it, in 64 bits."""
+    gate, up = c[:, : c.shape[1] // 2], c[:, c.shape[1] // 2 :]
+    with np.errstate(over="ignore", invalid="ignore"):
+        return gate / (1 + np.exp(-gate)) * up
+
+
+GATED = [(20, 2, 48, 128), (300, 3, 300, 160), (640, 32, 700, 128), (900, 8, 5000, 128), (4000, 4, 5200, 128)]
+
+
+@pytest.mark.parametrize("R,G,O,H", GATED)
+@pytest.mark.parametrize("up_scale", [-60, 0, 60])
+def test_gates_far_below_zero(moe, R, G, O, H, up_scale):  # noqa: F811
+    """Gates down to -400 with large, ordinary and tiny up projections. Sums are exact (one scale for the gates and
+    one for the up rows, multiples of 1/4 below 36 * 160 times the scale). exp(v / 2), |v| <= 174, has an argument
+    off by two roundings of at most 87 * 1.45, so 2 * 126 * ln 2 * 2^-24 < 2^-16 relative, twice that in its square
+    with a few ulps: 2^-14; then half a bf16 step 2^-8 or half of bf16's smallest subnormal, 2^-134. Below
+    -174 silu's magnitude is under 175 * exp(-174) and 0 may stand for it."""
+    rng = np.random.default_rng(R + O)
+    note("gates far below zero", R, G, O, H, up_scale)
+    a, w = mx_random(rng, (R, H), 0, 0), mx_random(rng, (G, O, H), 0, 0)
+    w[1][:, O // 2 :] = 127 + up_scale
+    base = np.linspace(0, R, G + 1).astype(np.int32)
+    out = moe.moe_mx_product(moe.MxRows(*map(to_dev, a)), moe.MxRows(*map(to_dev, w)), to_dev(base), moe.MOE_MX_GATED)
+    c = oracle.mx_product(oracle.mx_values(*a, E2M1), oracle.mx_values(*w, E2M1), base)
+    gate, up = c[:, : O // 2], c[:, O // 2 :]
+    assert gate.min() < -180 and ((gate < -90) & (gate > -174)).any()
+    want, got = gated(c), oracle.bf16_bits_to_f32(bf16_bits(out)).astype(np.float64)
+    low = np.where(gate < -174, 175 * np.exp(-174.0) * np.abs(up), 0)
+    assert np.all(np.abs(got - want) <= np.abs(want) * (2.0**-8 + 2.0**-14) + 2.0**-134 + low)
+
+
+@pytest.mark.parametrize("R,G,O", [(40, 2, 64), (300, 2, 600), (640, 32, 700), (900, 8, 5000), (4000, 4, 5200)])
+def test_gated_product_of_what_is_not_finite(moe, R, G, O):  # noqa: F811
+    """One value a row, so that a sum is one product: gates and up projections of zero, ordinary, huge, infinite
+    (past fp32's range) and NaN values in every pairing, against the definition applied to the sums as fp32 has
+    them. Zeros keep their sign; tolerance as for finite gates."""
+    rng = np.random.default_rng(R)
+    H = 64
+    a, w = mx_random(rng, (R, H), 0, 0), mx_random(rng, (G, O, H), 0, 0)
+    a[0][:] = 0
+    column = rng.integers(0, H, R)
+    a[0][np.arange(R), column // 2] = np.where(column % 2 == 0, 0x02, 0x20)  # 1.0
+    ends = np.array([127, 254, 255], dtype=np.uint8)
+    a[1][:] = ends[np.minimum(rng.integers(0, 8, (R, 1)) // 3, 2)]
+    w[1][:] = ends[np.minimum(rng.integers(0, 40, (G, O, 1)) // 19, 2)]
+    base = np.linspace(0, R, G + 1).astype(np.int32)
+    note("not finite", R, G, O)
+    out = moe.moe_mx_product(moe.MxRows(*map(to_dev, a)), moe.MxRows(*map(to_dev, w)), to_dev(base), moe.MOE_MX_GATED)
+    with np.errstate(over="ignore", invalid="ignore"):
+        sums = oracle.mx_product(oracle.mx_values(*a, E2M1), oracle.mx_values(*w, E2M1), base).astype(np.float32).astype(np.float64)
+        want = gated(sums).astype(np.float32).astype(np.float64)
+        got = oracle.bf16_bits_to_f32(bf16_bits(out)).astype(np.float64)
+        assert np.isnan(want).any() and np.isinf(want).any() and np.isfinite(want).any()
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        rest = ~np.isnan(want)
+        same = got[rest] == want[rest]
+        close = np.abs(got[rest] - want[rest]) <= np.abs(want[rest]) * (2.0**-8 + 2.0**-14) + 2.0**-134
+        assert np.all(same | (close & np.isfinite(want[rest])))
+        zero = rest & (want == 0) & (got == 0)
+        assert np.array_equal(np.signbit(got[zero]), np.signbit(want[zero]))
