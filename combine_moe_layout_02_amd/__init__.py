@@ -885,10 +885,14 @@ def _out(rows, columns, dtype, dev, stream):
     """A new output for a call on `stream`, from that stream's memory (the current stream's without one)."""
     if stream is None:
         return _empty(rows, columns, dtype=dtype, device=dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream, dev)):
         return _empty(rows, columns, dtype=dtype, device=dev)
+
+
+def _torch_stream(stream, dev):
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
 
 
 def _dense(t, name, dtype, shape, dev):
@@ -1066,9 +1070,33 @@ def _count_arg(num_rows, dev):
     return num_rows.data_ptr()
 
 
+_CALL_ROWS = 1 << 20  # MOE_MAX_OUT_ROWS: the rows that one call of the library converts at most
+
+
+def _mx_parts(name, ptr, stride, codes, scales, count, num_rows, n, H, format, dev, stream):
+    """Rows to MX or back, more of them than one call converts: call after call, all on the one stream."""
+    quantize, fn, width, blocks = name == "moe_mx_quantize", getattr(_lib, name), _mx_width(H, format), H // 32
+    # a call checks its own part alone for outputs over inputs or over one another
+    spans = ((ptr, (n - 1) * stride + 2 * H), (codes, n * width), (scales, n * blocks), (count or 0, 4 if count else 0))
+    for i, j in (((0, 1), (0, 2), (1, 2), (1, 3), (2, 3)) if quantize else ((0, 1), (0, 2), (0, 3))):
+        (x, x_bytes), (y, y_bytes) = spans[i], spans[j]
+        if y_bytes and x < y + y_bytes and y < x + x_bytes:
+            raise ValueError(f"{name}: outputs must not overlap inputs or one another")
+    with torch.cuda.stream(torch.cuda.current_stream(dev) if stream is None else _torch_stream(stream, dev)):
+        for at in range(0, n, _CALL_ROWS):
+            rows, left = min(_CALL_ROWS, n - at), None
+            if count is not None:
+                left = num_rows.reshape(-1)[:1].long().sub(at).clamp(0, rows).int()
+            r, c, s, left_ptr = ptr + at * stride, codes + at * width, scales + at * blocks, left if left is None else left.data_ptr()
+            if quantize:
+                _launch(dev, stream, fn, r, stride, left_ptr, rows, H, format, c, s)
+            else:
+                _launch(dev, stream, fn, c, s, left_ptr, rows, H, format, r, stride)
+
+
 def moe_mx_quantize(rows, format, num_rows=None, out=None, stream=None):
-    """MxRows of bf16 rows [R, H] (any row stride). num_rows: None, or the device count of rows to take (e.g.
-    layout.expert_slot_base[E:]); the outputs' other rows keep their contents."""
+    """MxRows of bf16 rows [R, H] (any row stride), R without a limit. num_rows: None, or the device count of rows
+    to take (e.g. layout.expert_slot_base[E:]); the outputs' other rows keep their contents."""
     dev, n, H = _matrix(rows, "rows", torch.bfloat16)
     if out is None:
         out = _mx_empty(n, H, format, dev, stream)
@@ -1078,12 +1106,15 @@ def moe_mx_quantize(rows, format, num_rows=None, out=None, stream=None):
     count = _count_arg(num_rows, dev)
     if n:
         ptr, stride, _ = _rows_arg(rows, "rows", H, dev)
-        _launch(dev, stream, _lib.moe_mx_quantize, ptr, stride, count, n, H, format, codes, scales)
+        if n > _CALL_ROWS:
+            _mx_parts("moe_mx_quantize", ptr, stride, codes, scales, count, num_rows, n, H, format, dev, stream)
+        else:
+            _launch(dev, stream, _lib.moe_mx_quantize, ptr, stride, count, n, H, format, codes, scales)
     return MxRows(*out)
 
 
 def moe_mx_dequantize(mx, format, num_rows=None, out=None, stream=None):
-    """The values of MxRows [R, ...] as bf16 rows [R, H] (out: any row stride)."""
+    """The values of MxRows [R, ...] as bf16 rows [R, H] (out: any row stride), R without a limit."""
     dev, n, blocks = _matrix(mx[1], "mx.scales", torch.uint8)
     H = 32 * blocks
     codes, scales = _mx_args(mx, "mx", n, H, format, dev)
@@ -1094,7 +1125,10 @@ def moe_mx_dequantize(mx, format, num_rows=None, out=None, stream=None):
         ptr, stride, rows = _rows_arg(out, "out", H, dev)
         if rows != n:
             raise ValueError(f"out must have {n} rows")
-        _launch(dev, stream, _lib.moe_mx_dequantize, codes, scales, count, n, H, format, ptr, stride)
+        if n > _CALL_ROWS:
+            _mx_parts("moe_mx_dequantize", ptr, stride, codes, scales, count, num_rows, n, H, format, dev, stream)
+        else:
+            _launch(dev, stream, _lib.moe_mx_dequantize, codes, scales, count, n, H, format, ptr, stride)
     return out
 
 

@@ -578,7 +578,8 @@ int64_t moe_mx_row_bytes(int32_t H, int32_t format);
  * bf16 does not hold: bits below its smallest subnormal are rounded to nearest even, and 2^128, to which a
  * block's largest values can round when they lie within 1/32 of bf16's largest, becomes an infinity.
  * num_rows is a DEVICE pointer (e.g. &expert_slot_base[E]), read on the device; negative counts are 0.
- * max_rows in [0, MOE_MAX_OUT_ROWS]; 0 enqueues nothing. Rows N..max_rows-1 of the outputs keep their
+ * max_rows in [0, MOE_MAX_OUT_ROWS]; 0 enqueues nothing. Rows stand alone, so more of them, as all experts'
+ * weights can have, are converted in parts, a call each. Rows N..max_rows-1 of the outputs keep their
  * contents, and so do the bytes between rows. Outputs must not overlap inputs. One kernel each. */
 int moe_mx_quantize(const void *rows, int64_t row_stride_bytes, const int32_t *num_rows,
                     int64_t max_rows, int32_t H, int32_t format, void *codes, void *scales,

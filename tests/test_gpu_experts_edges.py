@@ -145,3 +145,75 @@ def test_gated_product_of_what_is_not_finite(moe, R, G, O):  # noqa: F811
         assert np.all(same | (close & np.isfinite(want[rest])))
         zero = rest & (want == 0) & (got == 0)
         assert np.array_equal(np.signbit(got[zero]), np.signbit(want[zero]))
+
+
+# ---------------------------------------------------------------- matrices of more rows than a layout has
+
+
+@pytest.mark.parametrize("form", [E2M1, E4M3])
+def test_more_rows_than_a_layout(moe, form):  # noqa: F811
+    """17 matrices of 65536 rows, more than 2^20: there and back, with a device count and without, and the E2M1 ones
+    as the weights of a product."""
+    rng = np.random.default_rng(40)
+    G, O, H = 17, 65536, 32
+    w = bits(rng.standard_normal((G * O, H)))
+    codes, scales = oracle.mx_quantize(w, form)
+    dev = bf16_dev(w)
+    q = moe.moe_mx_quantize(dev, form)
+    assert np.array_equal(q.codes.cpu().numpy(), codes) and np.array_equal(q.scales.cpu().numpy(), scales)
+    values = bits(oracle.mx_values(codes, scales, form).astype(np.float32))
+    assert np.array_equal(bf16_bits(moe.moe_mx_dequantize(q, form)), values)
+    for count in (-(2**31), 0, 1000, 2**20, 2**20 + 9, G * O, 2**31 - 1):
+        n, num = min(max(count, 0), G * O), torch.tensor([count], dtype=torch.int32, device=DEV)
+        out = moe.MxRows(poison(codes.shape, torch.uint8), poison(scales.shape, torch.uint8))
+        moe.moe_mx_quantize(dev, form, num_rows=num, out=out)
+        for got, want in zip(out, (codes, scales)):
+            got = got.cpu().numpy()
+            assert np.array_equal(got[:n], want[:n]) and np.all(got[n:] == 0xAB), count
+        back = poison((G * O, H + 8), torch.bfloat16)
+        moe.moe_mx_dequantize(q, form, num_rows=num, out=back[:, :H])
+        got = bf16_bits(back)
+        assert np.array_equal(got[:n, :H], values[:n]) and np.all(got[n:] == 0xABAB) and np.all(got[:, H:] == 0xABAB), count
+    if form == E4M3:
+        return
+    counts = [3, 0, 0, 7] + [0] * 12 + [5]
+    base = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    a = mx_random(rng, (int(base[-1]), H), 0, 0)
+    got = moe.moe_mx_product(moe.MxRows(*map(to_dev, a)), moe.MxRows(q.codes.view(G, O, H // 2), q.scales.view(G, O, 1)), to_dev(base))
+    av, wv = oracle.mx_values(*a, E2M1), oracle.mx_values(codes, scales, E2M1).reshape(G, O, H)
+    want, size = oracle.mx_product(av, wv, base), oracle.mx_product(np.abs(av), np.abs(wv), base)
+    # 32 roundings or truncations of partial sums, then half a bf16 step
+    assert np.all(np.abs(oracle.bf16_bits_to_f32(bf16_bits(got)).astype(np.float64) - want) <= H * 2.0**-23 * size + 2.0**-8 * np.abs(want))
+
+
+def test_more_rows_on_a_stream_and_refused(moe):  # noqa: F811
+    """The same with a stream of its own, behind a delayed count, and buffers that overlap in different parts."""
+    rng = np.random.default_rng(41)
+    n, H = 2**20 + 64, 32
+    rows = bits(rng.standard_normal((n, H)))
+    codes, scales = oracle.mx_quantize(rows, E4M3)
+    dev, num, most = bf16_dev(rows), torch.zeros(1, dtype=torch.int32, device=DEV), torch.tensor([n - 3], dtype=torch.int32, device=DEV)
+    out = moe.MxRows(poison(codes.shape, torch.uint8), poison(scales.shape, torch.uint8))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        num.copy_(most)
+    moe.moe_mx_quantize(dev, E4M3, num_rows=num, out=out, stream=side)
+    side.synchronize()
+    for got, want in zip(out, (codes, scales)):
+        got = got.cpu().numpy()
+        assert np.array_equal(got[: n - 3], want[: n - 3]) and np.all(got[n - 3 :] == 0xAB)
+    both = torch.zeros(n * H * 2 + n * H - 64 * H, dtype=torch.uint8, device=DEV)
+    x = both[: n * H * 2].view(torch.bfloat16).view(n, H)
+    over = both[n * H * 2 - 64 * H :].view(n, H)  # its first rows lie over the last of x
+    with pytest.raises(ValueError, match="overlap"):
+        moe.moe_mx_quantize(x, E4M3, out=moe.MxRows(over, out.scales))
+    with pytest.raises(ValueError, match="overlap"):
+        moe.moe_mx_dequantize(moe.MxRows(over, out.scales), E4M3, out=x)
+    with pytest.raises(ValueError):
+        moe.moe_mx_quantize(torch.zeros((n, 48), dtype=torch.bfloat16, device=DEV), E4M3)
+    with pytest.raises(ValueError):
+        moe.moe_mx_quantize(dev, 3)
+    torch.cuda.synchronize()
+    assert not both.any()
