@@ -834,21 +834,6 @@ def moe_unpack_padded(window, expert_slot_base, S, K, H, quant=MOE_QUANT_NONE, e
     return out
 
 
-__all__ = [
-    "MOE_OK", "MOE_ERR_ARG", "MOE_ERR_ALIGN", "MOE_ERR_WINDOW", "MOE_ERR_UNSUPPORTED",
-    "MOE_ERR_HIP", "MOE_QUANT_NONE", "MOE_QUANT_FP8_E4M3_DYN", "MOE_QUANT_INT8_DYN", "MOE_LAYOUT_AUTO",
-    "MOE_LAYOUT_MULTI", "MOE_LAYOUT_SINGLE", "MoeError", "Layout",
-    "empty_layout", "moe_slot_bytes", "moe_window_bytes", "moe_slot_offsets", "moe_layout",
-    "moe_dispatch", "moe_dispatch_workspace_bytes", "moe_dispatch_ws", "moe_dispatch_noalloc", "MOE_ERR_SCRATCH",
-    "moe_layout_dispatch_workspace_bytes", "moe_layout_ws", "moe_dispatch_planned", "moe_layout_dispatch_ws",
-    "MOE_NOALLOC_SCRATCH_BYTES", "moe_layout_dispatch", "moe_combine", "moe_combine_scatter", "moe_combine_staged", "moe_unpack", "Unpacked", "moe_unpack_padded", "PaddedUnpacked",
-    "moe_dedup_window_bytes", "moe_rank_rows", "RankRows", "moe_dispatch_dedup", "moe_expand_dedup",
-    "moe_status_string", "Plan", "plan_layout", "plan_dispatch_ws", "plan_layout_dispatch", "plan_combine",
-    "plan_layout_ws", "plan_dispatch_planned",
-    "MOE_PLAN_BYTES",
-]
-
-
 # ---------------------------------------------------------------- gradients and MX rows
 
 
@@ -1163,3 +1148,21 @@ def moe_mx_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=Non
         _launch(dev, stream, _lib.moe_mx_product, a_codes, a_scales, n, base_ptr, G, wc_ptr, ws_ptr, O, H, epilogue,
                 out.data_ptr(), out_stride)
     return out
+
+
+__all__ = [
+    "MOE_OK", "MOE_ERR_ARG", "MOE_ERR_ALIGN", "MOE_ERR_WINDOW", "MOE_ERR_UNSUPPORTED",
+    "MOE_ERR_HIP", "MOE_QUANT_NONE", "MOE_QUANT_FP8_E4M3_DYN", "MOE_QUANT_INT8_DYN", "MOE_LAYOUT_AUTO",
+    "MOE_LAYOUT_MULTI", "MOE_LAYOUT_SINGLE", "MoeError", "Layout",
+    "empty_layout", "moe_slot_bytes", "moe_window_bytes", "moe_slot_offsets", "moe_layout",
+    "moe_dispatch", "moe_dispatch_workspace_bytes", "moe_dispatch_ws", "moe_dispatch_noalloc", "MOE_ERR_SCRATCH",
+    "moe_layout_dispatch_workspace_bytes", "moe_layout_ws", "moe_dispatch_planned", "moe_layout_dispatch_ws",
+    "MOE_NOALLOC_SCRATCH_BYTES", "moe_layout_dispatch", "moe_combine", "moe_combine_scatter", "moe_combine_staged", "moe_unpack", "Unpacked", "moe_unpack_padded", "PaddedUnpacked",
+    "moe_dedup_window_bytes", "moe_rank_rows", "RankRows", "moe_dispatch_dedup", "moe_expand_dedup",
+    "moe_status_string", "Plan", "plan_layout", "plan_dispatch_ws", "plan_layout_dispatch", "plan_combine",
+    "plan_layout_ws", "plan_dispatch_planned",
+    "MOE_PLAN_BYTES",
+    "MOE_MX_E2M1", "MOE_MX_E4M3", "MOE_MX_PLAIN", "MOE_MX_GATED", "MxRows", "moe_combine_backward",
+    "moe_combine_checkpoint", "moe_combine_backward_mx", "moe_dispatch_backward", "moe_mx_row_bytes",
+    "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_product",
+]
