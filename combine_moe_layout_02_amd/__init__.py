@@ -877,7 +877,8 @@ def _out(rows, columns, dtype, dev, stream):
 def _torch_stream(stream, dev):
     if isinstance(stream, torch.cuda.Stream):
         return stream
-    return torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+    handle = _stream(None, stream)
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
 
 
 def _dense(t, name, dtype, shape, dev):

@@ -217,3 +217,53 @@ def test_more_rows_on_a_stream_and_refused(moe):  # noqa: F811
         moe.moe_mx_quantize(dev, 3)
     torch.cuda.synchronize()
     assert not both.any()
+
+
+# ---------------------------------------------------------------- the stream argument
+
+
+class Handle:
+    """A stream of another library: an object with the raw handle."""
+
+    def __init__(self, stream):
+        self.stream, self.cuda_stream = stream, stream.cuda_stream
+
+
+@pytest.mark.parametrize("kind", [lambda s: s, lambda s: s.cuda_stream, Handle], ids=["stream", "handle", "object"])
+def test_every_call_runs_on_the_stream_it_is_given(moe, kind):  # noqa: F811
+    """The inputs are produced late on a stream, the calls are given that stream while the current one is idle, and
+    only that stream is waited for: a call on any other reads the inputs' old contents."""
+    S, K, E, H, G, O = 64, 4, 8, 512, 3, 96
+
+    def inputs(seed):
+        rng = np.random.default_rng(seed)
+        slot = table(rng, S, K, E, 0.1)
+        a, w = mx_random(rng, (S * K, H), -1, 1), mx_random(rng, (G, O, H), -1, 1)
+        return [bf16_dev(spread_rows(rng, S * K, H)), bf16_dev(spread_rows(rng, S, H)), to_dev(slot), to_dev(rng.random((S, K), dtype=np.float32)),
+                *map(to_dev, a), *map(to_dev, w), to_dev(np.array([0, 100, 120, S * K], dtype=np.int32)),
+                to_dev(rng.integers(0, 127, (S * K, H)).astype(np.uint8)), to_dev(rng.integers(100, 140, (S * K, H // 32)).astype(np.uint8))]
+
+    calls = {
+        "combine_backward": lambda v, **kw: moe.moe_combine_backward(v[1], v[0], v[2], v[3], **kw)[1:],
+        "combine_checkpoint": lambda v, **kw: moe.moe_combine_checkpoint(v[0], v[2], v[3], **kw)[:1],
+        "combine_backward_mx": lambda v, **kw: moe.moe_combine_backward_mx(v[1], (v[9], v[10]), v[2], v[3], **kw)[1:],
+        "dispatch_backward": lambda v, **kw: (moe.moe_dispatch_backward(v[0], v[2], **kw),),
+        "quantize": lambda v, **kw: moe.moe_mx_quantize(v[0], E2M1, **kw),
+        "dequantize": lambda v, **kw: (moe.moe_mx_dequantize((v[9], v[10]), E4M3, **kw),),
+        "product": lambda v, **kw: (moe.moe_mx_product((v[4], v[5]), (v[6], v[7]), v[8], **kw),),
+    }
+    old, new = inputs(50), inputs(51)
+    want = {name: [t.clone() for t in call(new)] for name, call in calls.items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        for mine, fresh in zip(old, new):
+            mine.copy_(fresh)
+    got = {name: call(old, stream=kind(side)) for name, call in calls.items()}
+    late = not side.query()
+    side.synchronize()
+    assert late, "the producer was done before the calls were made"
+    for name in calls:
+        for g, w in zip(got[name], want[name]):
+            assert torch.equal(g.view(torch.uint8), w.view(torch.uint8)), name
