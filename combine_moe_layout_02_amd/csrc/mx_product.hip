@@ -590,7 +590,9 @@ hipError_t few_rows(const void *a_codes, const void *a_scales, int64_t a_rows, c
 
 constexpr int kUnits = 256;  // compute units of an MI355X
 
-template <int TM, int TN, int WMC, int WNC, int PAIRS>
+// MIN_H: the least H that the caller's rule has for this tile; rows of scales below 16 bytes (H < 512) have their kernel
+// only where it can come to them.
+template <int TM, int TN, int WMC, int WNC, int PAIRS, int MIN_H = 32>
 hipError_t tiles(const void *a_codes, const void *a_scales, int64_t a_rows, const int32_t *group_base,
                  int32_t G, const void *w_codes, const void *w_scales, int32_t O, int32_t H, bool gated,
                  void *out, int64_t out_stride, bool wide, hipStream_t stream) {
@@ -600,10 +602,13 @@ hipError_t tiles(const void *a_codes, const void *a_scales, int64_t a_rows, cons
     const int64_t row_tiles = a_rows / TM + (a_rows < G ? a_rows : G);  // at most
     const int64_t need = (row_tiles * ncol + 7) / 8 * 8;
     const int64_t grid = PAIRS > 2 || need < resident ? need : resident;
-    auto *kernel = H >= 512 ? (gated ? product_tile_kernel<TM, TN, WMC, WNC, PAIRS, true, false>
-                                     : product_tile_kernel<TM, TN, WMC, WNC, PAIRS, false, false>)
-                            : (gated ? product_tile_kernel<TM, TN, WMC, WNC, PAIRS, true, true>
-                                     : product_tile_kernel<TM, TN, WMC, WNC, PAIRS, false, true>);
+    auto *kernel = gated ? product_tile_kernel<TM, TN, WMC, WNC, PAIRS, true, false>
+                         : product_tile_kernel<TM, TN, WMC, WNC, PAIRS, false, false>;
+    if constexpr (MIN_H < 512) {
+        if (H < 512)
+            kernel = gated ? product_tile_kernel<TM, TN, WMC, WNC, PAIRS, true, true>
+                           : product_tile_kernel<TM, TN, WMC, WNC, PAIRS, false, true>;
+    }
     hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WMC * WNC), 0, stream,
                        static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales),
                        a_rows, group_base, G, static_cast<const uint8_t *>(w_codes),
@@ -660,11 +665,11 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
         return tiles<64, 64, 4, 1, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
                                       out_stride_bytes, wide, stream);
     if (H >= 2048 && tiles_of(64, 128) <= kUnits)
-        return tiles<64, 128, 2, 2, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
-                                       out_stride_bytes, wide, stream);
+        return tiles<64, 128, 2, 2, 4, 2048>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                             out_stride_bytes, wide, stream);
     if (H >= 4096 && tiles_of(128, 128) <= kUnits)
-        return tiles<128, 128, 2, 2, 4>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
-                                        out_stride_bytes, wide, stream);
+        return tiles<128, 128, 2, 2, 4, 4096>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
+                                              out_stride_bytes, wide, stream);
     const int64_t large = tiles_of(256, 256);
     if (mean >= 160 && (large >= 4 * kUnits || (H >= 4096 && large >= 192 && large <= kUnits)))
         return tiles<256, 256, 2, 4, 2>(a_codes, a_scales, a_rows, group_base, G, w_codes, w_scales, O, H, gated, out,
