@@ -856,6 +856,8 @@ _bf16, _fp32, _int32, _uint8 = torch.bfloat16, torch.float32, torch.int32, torch
 
 def _launch(dev, stream, fn, *args):
     """fn(*args, stream handle) with dev as the current device: a null stream is the current device's."""
+    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, expected cuda:{dev}")  # its kernels run there
     if dev == _current_device():
         rc = fn(*args, _raw_stream(dev) if stream is None and _raw_stream is not None
                 else _stream(torch.device("cuda", dev), stream))
