@@ -81,6 +81,20 @@ def test_checkpoint_gradient_of_the_largest_values(moe, S, K, H):  # noqa: F811
     assert np.all(np.abs(got[1].cpu().numpy() - want_w) <= weight_error_bound(magnitude))
 
 
+@pytest.mark.parametrize("R,O,H", [(20, 40, 256), (300, 300, 544), (900, 3000, 1056)])
+def test_product_of_scales_far_apart(moe, R, O, H):  # noqa: F811
+    """Scales near both ends of E8M0 whose products are near 1: exact sums as with scales near 1, bit for bit."""
+    rng = np.random.default_rng(R)
+    (a, _), (w, _) = mx_random(rng, (R, H), 0, 0), mx_random(rng, (2, O, H), 0, 0)
+    far = rng.integers(-125, 126, H // 32)
+    a_scales = (127 + far + rng.integers(-1, 2, (R, H // 32))).astype(np.uint8)
+    w_scales = (127 - far + rng.integers(-1, 2, (2, O, H // 32))).astype(np.uint8)
+    base = np.array([0, R // 3, R], dtype=np.int32)
+    got = moe.moe_mx_product(moe.MxRows(to_dev(a), to_dev(a_scales)), moe.MxRows(to_dev(w), to_dev(w_scales)), to_dev(base))
+    want = oracle.mx_product(oracle.mx_values(a, a_scales, E2M1), oracle.mx_values(w, w_scales, E2M1), base)
+    same_bits(bf16_bits(got), bits(want.astype(np.float32)), "scales far apart")
+
+
 # ---------------------------------------------------------------- gates far below zero, and not finite ones
 
 
