@@ -5,12 +5,21 @@
 // so one pass over a token's K rows reads them once (bf16, or E4M3 blocks kept by the forward) and writes
 // K gradient rows. The dispatch copies x[t] to K rows, so its gradient is their sum.
 //
-// All of it is HBM traffic with a few operations a value. What bounds it is that the rows of a token lie all
-// over the buffers: with rows in token order instead the combine's gradient took 180 us for 998 MB (S = 4096,
-// H = 7168, K = 8) instead of 213, the checkpointed combine 145 instead of 164. Two ways to visit the rows in
-// slot order, through an inverse of slot_idx that a first kernel writes, came to 196 us (a workgroup a row) and
-// 205 us (a workgroup a quarter row, sums joined by a third kernel): the gain is spent on the second read of
-// dy for every row, the chain from slot to token to dy, and the launches; a call would need a workspace too.
+// All of it is HBM traffic with a few operations a value, and the order of the rows costs 14 to 17%: S = 4096, H =
+// 7168, K = 8, rows in the layout's order and in token order: the combine's gradient 199 and 170 us (998 MB), from a
+// checkpoint 161 and 144, the checkpointed combine 146 and 128. The scattered reads alone cost less: the combine reads the
+// same rows in 84 us, 77 in token order, and the planned pack, which writes such rows in slot order, takes
+// 84 too, so what is lost here is lost by token-order writes among the reads. A pass that only reads and a second that
+// writes in slot order from the layout's records have not been tried. Two ways to do both in slot order, through an inverse
+// of slot_idx that a first kernel writes, came to 196 us (a workgroup a row) and 205 us (a workgroup a quarter row, sums
+// joined by a third kernel) where this kernel took 213: the gain is spent on the second read of dy for every row, the
+// chain from slot to token to dy, and the launches; a call would need a workspace too.
+//
+// Below that size occupancy and the last round of workgroups count: 1531 tokens of 2080, K = 6, move their 62 MB at 3.5
+// to 3.7 TB/s. combine_backward_kernel holds a slot and descriptors for every row in scalar registers, of which some
+// spill to vector lanes (bf16 rows and a checkpoint's: 24 and 72 with KMAX = 8, 210 and 346 with 16); with KMAX = 4
+// on bf16 rows the compiler keeps a small array in 16 KB of LDS, so nine waves fit a compute unit where rows are short
+// (8192 tokens of 512, K = 4: 27.6 us, its bytes 11.4).
 
 #include "mx_blocks.h"
 
@@ -22,14 +31,16 @@ using namespace mx;
 constexpr int kLoadPolicy = 2;              // nt: rows are read once
 constexpr int kStorePolicy = 1 | 16;        // sc0 sc1
 constexpr int kStreamPolicy = 1 | 16 | 2;   // sc0 sc1 nt: a checkpoint's codes stream to HBM
-// nt: gradient rows (S = 4096, K = 8; bf16, then from a checkpoint: H = 7168 211 and 166 us, with kStreamPolicy 217
-// and 169, write-back 214 and 175; H = 2048 61 and 47.8, 62.7 and 48.9; 1024 tokens of 7168 53 and 56).
+// nt: gradient rows, chosen with the calls that follow in the stream (S = 4096, H = 7168, K = 8, us with nt, kStreamPolicy
+// and write-back): the gradient alone 199.9, 201.7 and 206.8, with the dispatch's gradient of the rows behind it 286.2,
+// 286.2 and 270.3, with a copy of 400 MB 361.3, 361.5 and 361.8; from a checkpoint 161.1, 162.4 and 171.6, between the
+// checkpointed combine and the dispatch's gradient 392.8, 393.0 and 395.7, before the copy 325.4, 325.4 and 336.2.
 constexpr int kRowPolicy = 2;
 // A checkpoint's values are taken at half their size, and the sums doubled: a block's largest can be 2^128, past
 // fp32, whose product with a small or zero gradient is finite.
 constexpr float kHalf = 0.5f;
-// 16-byte vectors of a part, a lane each. S = 4096, H = 7168, K = 8: the dispatch's gradient takes 87.9 us with
-// 32, 89.1 with 64 and 90.2 with 128; the checkpointed combine 164, 153 and 153 (a row's codes are half as wide).
+// 16-byte vectors of a part, a lane each. S = 4096, H = 7168, K = 8: the dispatch's gradient takes 84.5 us with
+// 32, 86.0 with 64 and 85.9 with 128; the checkpointed combine 159, 146 and 146 (a row's codes are half as wide).
 template <bool KEEP>
 constexpr int part_threads() { return KEEP ? 64 : 32; }
 
@@ -61,9 +72,9 @@ __device__ inline float wave_sums(float (&v)[N]) {
 
 // grid = S; workgroup t takes token t, its lanes vectors threadIdx.x, + blockDim.x, ... of the rows (at most two
 // rounds: nvec <= 2048 and 1024 lanes; a lane a vector where they suffice, so that all of a token's loads are
-// under way at once. S = 4096, K = 8: 211 to 217 us at H = 7168 and 112 at H = 4096; with 64 lanes and more rounds 205
-// and 153, with 256 lanes 210 and 124; 64 tokens 9 us, 20 and 10). An eighth of the tokens in order for each XCD
-// takes 202 us at H = 7168, but 115 at H = 4096, and 228 for 218 with 8192 tokens there.
+// under way at once. S = 4096, K = 8, this, 64 lanes with more rounds and 256: 199, 198 and 200 us at H = 7168, 111, 123 and
+// 110 at 4096, 57, 67 and 57 at 2048; 8192 tokens of 4096 219, 258 and 225; 64 tokens of 7168 9.2, 21.6 and 10.4). An eighth
+// of the tokens in order for each XCD takes 199, 114 and 57 us at those H, and 225 with 8192 tokens.
 // MX: the rows are E4M3 codes and scales (stride = H). d_weights: a lane's sum over its values in order, the wave's
 // lanes by a fixed tree, the waves in order, all in fp32.
 template <int KMAX, bool MX>

@@ -197,10 +197,16 @@ __device__ inline Tile find_tile(const TileTable &table, int G, int ncol, int t)
 // PAIRS == 2, many tiles: a workgroup takes tile after tile, the next tile's first pair behind a tile's last, so that
 // the loads never pause and a tile's results are stored while the next one's rows arrive.
 //
-// 32768 rows on 32 groups, 7168 -> 4096 gated: the matrix cores alone take 290 to 350 us on random codes (the
-// card's power holds them at 6.5 PFLOP/s), the loads alone 450, the products with their reads of LDS 500, together
-// 636. Four waves of 128 x 128 results read a third less of LDS, but took 700, and 718 with the next stage's operands
-// read ahead: one wave a SIMD leaves its loads and reads uncovered.
+// 32768 rows on 32 groups, 7168 -> 4096 gated, take 541 to 566 us in a stream of such calls (groups of uneven size; 504
+// where every group fills its tiles), half of it with matrix instructions under way, and 570 to 650 in runs of 20 calls
+// behind a pause. In a copy of the kernel with parts taken out, in such runs, where the whole took 636: the matrix cores alone 290 to 350 on random codes (the card's power
+// holds them at 6.5 PFLOP/s), the loads alone 450, the products with their reads of LDS 500. Four waves of 128 x 128
+// results read a third less of LDS, but took 700 there, and 718 with the next stage's operands read ahead: one wave a
+// SIMD leaves its loads and reads uncovered.
+//
+// Row tiles are whole: one of a few rows takes the time of a full one and its weights again, so uneven groups whose mean
+// fills the tiles cost more than even ones (7168 -> 4096 gated, uneven and even, us: 8 groups of 128 rows 41 and 33, 32
+// of 128 149 and 125, of 256 203 and 153, of 512 336 and 266).
 //
 // PAIRS > 2, tiles for every compute unit once at most: a workgroup takes one tile, whose time is its pairs' way
 // from memory and through the matrix cores: 0.55 us a pair with one under way and 0.45 with three at 64 x 128, 0.31
@@ -630,7 +636,8 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
     const bool wide = width % 8 == 0 && out_stride_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                       out_stride_bytes <= (1 << 22);
     // Which kernel, by the tiles it would have if the rows were spread over as many groups as they can reach, a
-    // quarter of them more in the fuller ones. Measured with weights from memory (us; groups x rows a group):
+    // quarter of them more in the fuller ones. One run over the kernels, weights from memory, uneven groups (us; groups x
+    // rows a group):
     //   7168 -> 4096 gated   1x8    1x64   1x256  1x512  4x16   4x32   8x32   8x64   4x128  8x128  32x16  32x64  32x256
     //   few_rows             6.9    17.6                 32.2   36.5   68.7                        221
     //   32 x 64, four pairs  11.6   11.9   15.8   28.6   16.8   23.9   45.1   58.4   48.7   82.7   100    198    536
