@@ -36,6 +36,12 @@ MOE_MX_E4M3 = 2  # 8-bit codes
 MOE_MX_PLAIN = 0
 MOE_MX_GATED = 1
 
+MOE_BF16 = 1  # element types of a norm's weight and of the router's logits
+MOE_FP32 = 2
+
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+
 MOE_LAYOUT_AUTO = 0
 MOE_LAYOUT_MULTI = 1
 MOE_LAYOUT_SINGLE = 2
@@ -50,6 +56,9 @@ EXPORTED = (
     "moe_plan_layout_dispatch", "moe_plan_combine", "moe_plan_layout_ws", "moe_plan_dispatch_planned", "moe_plan_run",
     "moe_combine_backward", "moe_combine_backward_mx", "moe_dispatch_backward", "moe_combine_checkpoint",
     "moe_mx_row_bytes", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_product",
+    "moe_row_quantize", "moe_row_dequantize", "moe_int8_product", "moe_rms_norm", "moe_rms_norm_backward",
+    "moe_rms_norm_backward_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
+    "moe_balance_loss_workspace_bytes",
 )
 
 # include/moe_probe.h: bandwidth probes for the measurement, not part of the path
@@ -67,7 +76,7 @@ def _load():
     if missing:
         raise ImportError(f"{_LIB_PATH} is stale (missing {missing}); rebuild it with "
                           "`python combine_moe_layout_02_amd/build.py`")
-    P, I32, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    P, I32, I64, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     sig = {
         "moe_slot_bytes": (I64, [I32]),
         "moe_window_bytes": (I64, [I32, I32, I32]),
@@ -114,6 +123,15 @@ def _load():
         "moe_mx_quantize": (ctypes.c_int, [P, I64, P, I64, I32, I32, P, P, P]),
         "moe_mx_dequantize": (ctypes.c_int, [P, P, P, I64, I32, I32, P, I64, P]),
         "moe_mx_product": (ctypes.c_int, [P, P, I64, P, I32, P, P, I32, I32, I32, P, I64, P]),
+        "moe_row_quantize": (ctypes.c_int, [P, I64, P, I64, I32, I32, P, P, P]),
+        "moe_row_dequantize": (ctypes.c_int, [P, P, P, I64, I32, I32, P, I64, P]),
+        "moe_int8_product": (ctypes.c_int, [P, P, I64, P, I32, P, P, I32, I32, I32, P, I64, P]),
+        "moe_rms_norm": (ctypes.c_int, [P, I64, P, I64, P, I32, F32, I64, I32, I32, P, I64, P, P, P, P]),
+        "moe_rms_norm_backward_workspace_bytes": (I64, [I64, I32]),
+        "moe_rms_norm_backward": (ctypes.c_int, [P, I64, P, I64, P, I32, F32, P, I64, I64, I32, P, P, P, I64, P]),
+        "moe_balance_loss_workspace_bytes": (I64, [I32, I32]),
+        "moe_balance_loss": (ctypes.c_int, [P, I64, I32, P, I32, I32, I32, I32, F32, P, P, P, P, I64, P]),
+        "moe_balance_loss_backward": (ctypes.c_int, [P, P, I64, I32, P, P, P, I32, I32, I32, I32, F32, P, P]),
         "moe_probe_fill": (ctypes.c_int, [P, I64, P]),
         "moe_probe_read": (ctypes.c_int, [P, I64, P, P]),
         "moe_probe_copy": (ctypes.c_int, [P, P, I64, P]),
@@ -1153,6 +1171,251 @@ def moe_mx_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=Non
     return out
 
 
+# ---------------------------------------------------------------- the layer in 8 bits
+
+
+class ScaledRows(NamedTuple):
+    """Rows in 8 bits with one scale a row: codes uint8 [..., R, H] (INT8 codes may be int8) and scales fp32 [..., R],
+    as moe_unpack leaves them in expand_x and expand_scales."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+_int8 = torch.int8
+
+
+def _row8_args(rows8, name, shape, dev):
+    """Pointers of the codes [*shape] and scales [*shape[:-1]]."""
+    codes, scales = rows8
+    kind = _int8 if isinstance(codes, _Tensor) and codes.dtype is _int8 else _uint8
+    return _dense(codes, f"{name}.codes", kind, shape, dev), _dense(scales, f"{name}.scales", _fp32, shape[:-1], dev)
+
+
+def _row8_empty(rows, H, dev, stream):
+    if stream is None:
+        return ScaledRows(_empty(rows, H, dtype=_uint8, device=dev), _empty(rows, dtype=_fp32, device=dev))
+    return ScaledRows(_out(rows, H, _uint8, dev, stream), _out(rows, 1, _fp32, dev, stream).view(rows))
+
+
+def moe_row_quantize(rows, quant, num_rows=None, out=None, stream=None):
+    """ScaledRows of bf16 rows [R, H] (any row stride) in MOE_QUANT_INT8_DYN or MOE_QUANT_FP8_E4M3_DYN, as moe_dispatch
+    computes them. num_rows: None, or the device count of rows to take (e.g. layout.expert_slot_base[E:]); the
+    outputs' other rows keep their contents (undefined where they are allocated here)."""
+    dev, n, H = _matrix(rows, "rows", _bf16)
+    if out is None:
+        out = _row8_empty(n, H, dev, stream)
+        codes, scales = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        codes, scales = _row8_args(out, "out", (n, H), dev)
+    count = _count_arg(num_rows, dev)
+    ptr, stride = _rows_arg(rows, "rows", H, dev)[:2] if n else (None, 2 * H)
+    _launch(dev, stream, _lib.moe_row_quantize, ptr, stride, count, n, H, quant, codes, scales)
+    return ScaledRows(*out)
+
+
+def moe_row_dequantize(rows8, quant, num_rows=None, out=None, stream=None):
+    """The values of ScaledRows [R, H] as bf16 rows (out: any row stride)."""
+    codes_t = rows8[0]
+    dev, n, H = _matrix(codes_t, "rows8.codes", _int8 if isinstance(codes_t, _Tensor) and codes_t.dtype is _int8 else _uint8)
+    codes, scales = _row8_args(rows8, "rows8", (n, H), dev)
+    if out is None:
+        out = _out(n, H, _bf16, dev, stream)
+    elif not isinstance(out, _Tensor) or out.shape != (n, H):
+        raise ValueError(f"out must be bfloat16 {(n, H)}")
+    count = _count_arg(num_rows, dev)
+    ptr, stride = _rows_arg(out, "out", H, dev)[:2] if n else (None, 2 * H)
+    _launch(dev, stream, _lib.moe_row_dequantize, codes, scales, count, n, H, quant, ptr, stride)
+    return out
+
+
+def moe_int8_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=None):
+    """The experts' product of INT8 rows a (ScaledRows [R, H], e.g. of moe_unpack's expand_x and expand_scales) with
+    INT8 weights w (ScaledRows [G, O, H], a scale for each output): row r of group g (group_base int32 [G + 1] on the
+    device, e.g. layout.expert_slot_base; [0, R] with G = 1 for a shared expert) gives bf16 [O], or [O / 2] of
+    silu(gate) * up with MOE_MX_GATED. Rows outside every group keep their contents (undefined where out is allocated
+    here)."""
+    a_codes = a[0]
+    dev, n, H = _matrix(a_codes, "a.codes", _int8 if isinstance(a_codes, _Tensor) and a_codes.dtype is _int8 else _uint8)
+    a_ptr, as_ptr = _row8_args(a, "a", (n, H), dev)
+    w_codes = w[0]
+    shape = w_codes.shape if isinstance(w_codes, _Tensor) else ()
+    if len(shape) != 3 or shape[2] != H:
+        raise ValueError(f"w must be codes [G, O, {H}] and scales [G, O]")
+    G, O, _ = shape
+    w_ptr, ws_ptr = _row8_args(w, "w", (G, O, H), dev)
+    base_ptr = _dense(group_base, "group_base", _int32, (G + 1,), dev)
+    width = O // 2 if epilogue == MOE_MX_GATED else O
+    if out is None:
+        out = _out(n, width, _bf16, dev, stream)
+        out_stride = 2 * width
+    else:
+        if not isinstance(out, _Tensor) or out.dtype is not _bf16 or out.get_device() != dev or out.shape != (n, width):
+            raise ValueError(f"out must be bfloat16 {(n, width)} on cuda:{dev}")
+        if n and (width > 1 and out.stride(1) != 1 or n > 1 and out.stride(0) < width):
+            raise ValueError("out must have contiguous rows that do not overlap")
+        out_stride = 2 * out.stride(0) if n > 1 else 2 * width
+    _launch(dev, stream, _lib.moe_int8_product, a_ptr, as_ptr, n, base_ptr, G, w_ptr, ws_ptr, O, H, epilogue,
+            out.data_ptr(), out_stride)
+    return out
+
+
+class RmsNorm(NamedTuple):
+    out: torch.Tensor  # bf16 [S, H]; None with a quant unless it was passed
+    sum: torch.Tensor  # bf16 [S, H]: what was normed, x + residual, or x itself without a residual
+    rows8: ScaledRows  # the normed rows in 8 bits; None with MOE_QUANT_NONE
+
+
+def _weight_arg(weight, H, dev):
+    """Pointer and moe_float of a norm's weight."""
+    kind = weight.dtype if isinstance(weight, _Tensor) else None
+    if kind is _bf16:
+        return _dense(weight, "weight", _bf16, (H,), dev), MOE_BF16
+    return _dense(weight, "weight", _fp32, (H,), dev), MOE_FP32
+
+
+def moe_rms_norm(x, weight, eps=1e-6, residual=None, quant=MOE_QUANT_NONE, out=None, sum=None, rows8=None, stream=None):
+    """The root-mean-square norm of bf16 rows x [S, H], or of x + residual, times weight (bf16 or fp32 [H]): bf16 rows,
+    with a quant (MOE_QUANT_INT8_DYN, MOE_QUANT_FP8_E4M3_DYN) rows in 8 bits instead, and both where out is passed too.
+    x, residual and sum may have any row stride; sum may be x or residual itself (an addition in place)."""
+    dev, n, H = _matrix(x, "x", _bf16)
+    ptr, stride = _rows_arg(x, "x", H, dev)[:2] if n else (None, 2 * H)
+    res_ptr, res_stride, sum_ptr, sum_stride = None, 0, None, 0
+    if residual is not None:
+        if not isinstance(residual, _Tensor) or residual.shape != (n, H):
+            raise ValueError(f"residual must be bfloat16 {(n, H)}")
+        if sum is None:
+            sum = _out(n, H, _bf16, dev, stream)
+        elif not isinstance(sum, _Tensor) or sum.shape != (n, H):
+            raise ValueError(f"sum must be bfloat16 {(n, H)}")
+        if n:
+            res_ptr, res_stride, _ = _rows_arg(residual, "residual", H, dev)
+            sum_ptr, sum_stride, _ = _rows_arg(sum, "sum", H, dev)
+    elif sum is not None:
+        raise ValueError("sum is written only with a residual")
+    else:
+        sum = x
+    w_ptr, kind = _weight_arg(weight, H, dev)
+    out_ptr, codes, scales = None, None, None
+    if quant != MOE_QUANT_NONE:
+        if rows8 is None:
+            rows8 = _row8_empty(n, H, dev, stream)
+            codes, scales = rows8[0].data_ptr(), rows8[1].data_ptr()
+        else:
+            codes, scales = _row8_args(rows8, "rows8", (n, H), dev)
+            rows8 = ScaledRows(*rows8)
+    elif rows8 is not None:
+        raise ValueError("rows8 is written only with a quant")
+    elif out is None:
+        out = _out(n, H, _bf16, dev, stream)
+    if out is not None:
+        out_ptr = _dense(out, "out", _bf16, (n, H), dev)
+    _launch(dev, stream, _lib.moe_rms_norm, ptr, stride, res_ptr, res_stride, w_ptr, kind, eps, n, H, quant, sum_ptr,
+            sum_stride, out_ptr, codes, scales)
+    return RmsNorm(out, sum, rows8)
+
+
+def moe_rms_norm_backward_workspace_bytes(rows, H):
+    v = _lib.moe_rms_norm_backward_workspace_bytes(int(rows), int(H))
+    if v < 0:
+        _check(int(v))
+    return int(v)
+
+
+def _workspace(workspace, need, dev, stream):
+    """Pointer and bytes of a call's workspace, and the tensor, which is allocated here where none is passed."""
+    if workspace is None:
+        workspace = _out(need, 1, _uint8, dev, stream)
+        return workspace.data_ptr(), need, workspace
+    _need(workspace, "workspace", device=torch.device("cuda", dev))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def moe_rms_norm_backward(dy, sum, weight, eps=1e-6, d_sum=None, dx=None, d_weight=None, workspace=None, stream=None):
+    """The gradients of moe_rms_norm's bf16 output: (dx bf16 [S, H], for x and the residual alike, and d_weight fp32 [H])
+    of dy, the rows that the forward normed (its sum), weight and eps. d_sum: the gradient that reaches the sum on its
+    other ways, added to dx. dy, sum and d_sum may have any row stride. workspace: a device buffer of at least
+    moe_rms_norm_backward_workspace_bytes(S, H) bytes, or None to have one allocated."""
+    dev, n, H = _matrix(sum, "sum", _bf16)
+    for t, name in ((dy, "dy"), (d_sum, "d_sum")):
+        if t is not None and (not isinstance(t, _Tensor) or t.shape != (n, H)):
+            raise ValueError(f"{name} must be bfloat16 {(n, H)}")
+    ptr, stride = _rows_arg(sum, "sum", H, dev)[:2] if n else (None, 2 * H)
+    dy_ptr, dy_stride = _rows_arg(dy, "dy", H, dev)[:2] if n else (None, 2 * H)
+    ds_ptr, ds_stride = _rows_arg(d_sum, "d_sum", H, dev)[:2] if n and d_sum is not None else (None, 0)
+    w_ptr, kind = _weight_arg(weight, H, dev)
+    if dx is None:
+        dx = _out(n, H, _bf16, dev, stream)
+    dx_ptr = _dense(dx, "dx", _bf16, (n, H), dev)
+    if d_weight is None:
+        d_weight = _out(1, H, _fp32, dev, stream).view(H)
+    dw_ptr = _dense(d_weight, "d_weight", _fp32, (H,), dev)
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, moe_rms_norm_backward_workspace_bytes(n, H), dev, stream)
+    _launch(dev, stream, _lib.moe_rms_norm_backward, dy_ptr, dy_stride, ptr, stride, w_ptr, kind, eps, ds_ptr, ds_stride,
+            n, H, dx_ptr, dw_ptr, ws_ptr, ws_bytes)
+    return dx, d_weight
+
+
+class BalanceLoss(NamedTuple):
+    loss: torch.Tensor  # fp32 [1]
+    num_tokens_per_expert: torch.Tensor  # int32 [E], the layout's
+    num_tokens: torch.Tensor  # int32 [1], tokens with a valid entry
+
+
+def _router_args(logits, topk_idx):
+    """Device, S, K, E, and the logits' pointer, row stride in bytes and type, and the entries' pointer."""
+    dev, S, K, table = _table_arg(topk_idx)
+    kind = logits.dtype if isinstance(logits, _Tensor) else None
+    rows, E = _matrix(logits, "logits", _bf16 if kind is _bf16 else _fp32)[1:]
+    if logits.get_device() != dev or rows != S:
+        raise ValueError(f"logits must have {S} rows on cuda:{dev}")
+    step, col = logits.stride()
+    if E > 1 and col != 1 or S > 1 and step < E:
+        raise ValueError("logits must have contiguous rows that do not overlap")
+    size = 2 if kind is _bf16 else 4
+    return (dev, S, K, E, logits.data_ptr(), size * (step if S > 1 else E), MOE_BF16 if kind is _bf16 else MOE_FP32, table)
+
+
+def moe_balance_loss_workspace_bytes(S, E):
+    v = _lib.moe_balance_loss_workspace_bytes(int(S), int(E))
+    if v < 0:
+        _check(int(v))
+    return int(v)
+
+
+def moe_balance_loss(logits, topk_idx, coef, score=MOE_SCORE_SOFTMAX, out=None, workspace=None, stream=None):
+    """BalanceLoss of the router's logits (bf16 or fp32 [S, E], any row stride) and its choice topk_idx (int32 [S, K], -1
+    for padding and dropped entries): coef * E / (N * T) * sum_e count_e * sum_t score[t, e] over the T tokens that have a
+    valid entry, N of those in all. score: MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID. workspace: a device buffer of at
+    least moe_balance_loss_workspace_bytes(S, E) bytes, or None to have one allocated."""
+    dev, S, K, E, ptr, stride, kind, table = _router_args(logits, topk_idx)
+    if out is None:
+        out = BalanceLoss(_out(1, 1, _fp32, dev, stream).view(1), _out(1, E, _int32, dev, stream).view(E),
+                          _out(1, 1, _int32, dev, stream).view(1))
+    loss, counts, tokens = (_dense(t, name, kind_, shape, dev) for t, name, kind_, shape in
+                            zip(out, BalanceLoss._fields, (_fp32, _int32, _int32), ((1,), (E,), (1,))))
+    ws_ptr, ws_bytes, workspace = _workspace(workspace, moe_balance_loss_workspace_bytes(S, E), dev, stream)
+    _launch(dev, stream, _lib.moe_balance_loss, ptr, stride, kind, table, S, K, E, score, coef, loss, counts, tokens, ws_ptr,
+            ws_bytes)
+    return BalanceLoss(*out)
+
+
+def moe_balance_loss_backward(d_loss, logits, topk_idx, num_tokens_per_expert, num_tokens, coef, score=MOE_SCORE_SOFTMAX,
+                              d_logits=None, stream=None):
+    """The balance loss's gradient d_logits ([S, E] of the logits' type) of d_loss (fp32 [1]), with the forward's
+    arguments and counts."""
+    dev, S, K, E, ptr, stride, kind, table = _router_args(logits, topk_idx)
+    dl_ptr = _dense(d_loss, "d_loss", _fp32, (1,), dev)
+    counts = _dense(num_tokens_per_expert, "num_tokens_per_expert", _int32, (E,), dev)
+    tokens = _dense(num_tokens, "num_tokens", _int32, (1,), dev)
+    if d_logits is None:
+        d_logits = _out(S, E, logits.dtype, dev, stream)
+    out_ptr = _dense(d_logits, "d_logits", logits.dtype, (S, E), dev)
+    _launch(dev, stream, _lib.moe_balance_loss_backward, dl_ptr, ptr, stride, kind, table, counts, tokens, S, K, E, score,
+            coef, out_ptr)
+    return d_logits
+
+
 __all__ = [
     "MOE_OK", "MOE_ERR_ARG", "MOE_ERR_ALIGN", "MOE_ERR_WINDOW", "MOE_ERR_UNSUPPORTED",
     "MOE_ERR_HIP", "MOE_QUANT_NONE", "MOE_QUANT_FP8_E4M3_DYN", "MOE_QUANT_INT8_DYN", "MOE_LAYOUT_AUTO",
@@ -1168,4 +1431,7 @@ __all__ = [
     "MOE_MX_E2M1", "MOE_MX_E4M3", "MOE_MX_PLAIN", "MOE_MX_GATED", "MxRows", "moe_combine_backward",
     "moe_combine_checkpoint", "moe_combine_backward_mx", "moe_dispatch_backward", "moe_mx_row_bytes",
     "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_product",
+    "MOE_BF16", "MOE_FP32", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "ScaledRows", "moe_row_quantize", "moe_row_dequantize",
+    "moe_int8_product", "RmsNorm", "moe_rms_norm", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace_bytes",
+    "BalanceLoss", "moe_balance_loss", "moe_balance_loss_backward", "moe_balance_loss_workspace_bytes",
 ]

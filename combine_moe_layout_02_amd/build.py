@@ -19,8 +19,8 @@ LIB = os.path.join(PKG, "libmoe.so")
 ARCH = "gfx950"
 
 SOURCES = ["layout.hip", "layout_small.hip", "pack.hip", "pack_planned.hip", "combine.hip", "unpack.hip",
-           "backward.hip", "mx_quant.hip", "mx_product.hip", "probe.hip", "noalloc.hip", "moe_api.cpp",
-           "expert_api.cpp"]
+           "backward.hip", "mx_quant.hip", "mx_product.hip", "row_quant.hip", "int8_product.hip", "norm.hip", "balance.hip",
+           "probe.hip", "noalloc.hip", "moe_api.cpp", "expert_api.cpp", "layer_api.cpp"]
 
 # -ffp-contract=off: combine rounds every product and sum to fp32 on its own (no fused multiply-add).
 # -packed-fp32-ops off: scalar fp32 only; no packed fp32 instructions are generated.

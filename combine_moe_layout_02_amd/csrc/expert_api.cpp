@@ -22,41 +22,6 @@ bool valid_format(int32_t format) { return format == MOE_MX_E2M1 || format == MO
 
 int64_t row_bytes(int32_t H, int32_t format) { return format == MOE_MX_E2M1 ? H / 2 : H; }
 
-// A buffer's bytes [base, base + bytes), for the overlap checks. Rows at a stride end with the last row.
-struct Span {
-    const void *base;
-    int64_t bytes;
-};
-
-Span rows_span(const void *base, int64_t rows, int64_t stride, int64_t row) {
-    return Span{base, rows > 0 ? (rows - 1) * stride + row : 0};
-}
-
-bool overlap(const Span &a, const Span &b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.base), y = reinterpret_cast<uintptr_t>(b.base);
-    if (a.bytes <= 0 || b.bytes <= 0) return false;
-    return x < y ? y - x < (uint64_t)a.bytes : x - y < (uint64_t)b.bytes;
-}
-
-// True when an output overlaps an input or another output.
-template <int NI, int NO>
-bool outputs_overlap(const Span (&in)[NI], const Span (&out)[NO]) {
-    for (int i = 0; i < NO; ++i) {
-        for (const Span &s : in)
-            if (overlap(out[i], s)) return true;
-        for (int j = 0; j < i; ++j)
-            if (overlap(out[i], out[j])) return true;
-    }
-    return false;
-}
-
-// bf16 rows of H values at a stride.
-int check_rows(const void *rows, int64_t stride, int64_t count, int32_t H) {
-    if (count < 0 || stride < 2 * (int64_t)H || !extent_fits(count, stride)) return MOE_ERR_ARG;
-    if (stride % 16 != 0 || !aligned(rows, 16)) return MOE_ERR_ALIGN;
-    return MOE_OK;
-}
-
 int check_sizes(int32_t S, int32_t H, int32_t K, bool mx) {
     const int st = check_tokens(S, K);
     if (st != MOE_OK) return st;

@@ -247,4 +247,57 @@ hipError_t launch_mx_product(const void *a_codes, const void *a_scales, int64_t 
                              const void *w_scales, int32_t O, int32_t H, int32_t epilogue, void *out,
                              int64_t out_stride_bytes, hipStream_t stream);
 
+// The 8-bit layer around the dispatch (row_quant.hip, int8_product.hip, norm.hip, balance.hip); arguments as in moe.h,
+// checked by layer_api.cpp.
+hipError_t launch_row_quantize(const void *rows, int64_t row_stride_bytes, const int32_t *num_rows,
+                               int64_t max_rows, int32_t H, int32_t quant, void *codes,
+                               float *scales, hipStream_t stream);
+
+hipError_t launch_row_dequantize(const void *codes, const float *scales, const int32_t *num_rows,
+                                 int64_t max_rows, int32_t H, int32_t quant, void *rows,
+                                 int64_t row_stride_bytes, hipStream_t stream);
+
+hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64_t a_rows,
+                               const int32_t *group_base, int32_t G, const void *w_codes,
+                               const float *w_scales, int32_t O, int32_t H, int32_t epilogue,
+                               void *out, int64_t out_stride_bytes, hipStream_t stream);
+
+hipError_t launch_rms_norm(const void *x, int64_t x_stride_bytes, const void *residual,
+                           int64_t residual_stride_bytes, const void *weight, int32_t weight_type,
+                           float eps, int64_t rows, int32_t H, int32_t quant, void *sum,
+                           int64_t sum_stride_bytes, void *out, void *codes, float *scales,
+                           hipStream_t stream);
+
+// Parts that the norm's gradient splits its rows into, each with H sums of d_weight in the workspace.
+inline int64_t norm_parts(int64_t rows) { return rows < 512 ? rows : 512; }
+
+hipError_t launch_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *sum,
+                                    int64_t sum_stride_bytes, const void *weight,
+                                    int32_t weight_type, float eps, const void *d_sum,
+                                    int64_t d_sum_stride_bytes, int64_t rows, int32_t H, void *dx,
+                                    float *d_weight, void *workspace, hipStream_t stream);
+
+// Parts that the balance loss splits its tokens into. Each has E sums of scores and E counts in the workspace, behind
+// them every part's number of tokens; a single part needs none.
+constexpr int kBalanceTokens = 32;  // tokens of a part at least
+constexpr int kBalanceParts = 256;
+inline int balance_parts(int32_t S) {
+    const int parts = (S + kBalanceTokens - 1) / kBalanceTokens;
+    return parts < kBalanceParts ? parts : kBalanceParts;
+}
+
+hipError_t launch_balance_loss(const void *logits, int64_t logits_stride_bytes, int32_t logits_type,
+                               const int32_t *topk_idx, int32_t S, int32_t K, int32_t E,
+                               int32_t score, float coef, float *loss,
+                               int32_t *num_tokens_per_expert, int32_t *num_tokens, void *workspace,
+                               hipStream_t stream);
+
+hipError_t launch_balance_loss_backward(const float *d_loss, const void *logits,
+                                        int64_t logits_stride_bytes, int32_t logits_type,
+                                        const int32_t *topk_idx,
+                                        const int32_t *num_tokens_per_expert,
+                                        const int32_t *num_tokens, int32_t S, int32_t K, int32_t E,
+                                        int32_t score, float coef, void *d_logits,
+                                        hipStream_t stream);
+
 }  // namespace moe

@@ -33,8 +33,8 @@ typedef enum {
     MOE_OK = 0,
     MOE_ERR_ARG = -1,         /* null pointer or a size outside its documented range          */
     MOE_ERR_ALIGN = -2,       /* a pointer or stride is not aligned as documented             */
-    MOE_ERR_WINDOW = -3,      /* window_bytes < moe_window_bytes(S, K, H), or a staging buffer
-                                 shorter than its S*K rows                                    */
+    MOE_ERR_WINDOW = -3,      /* window_bytes < moe_window_bytes(S, K, H), or a staging buffer or
+                                 workspace that is too short                                  */
     MOE_ERR_UNSUPPORTED = -4, /* E % P != 0, H % 16 != 0, S above MOE_MAX_TOKENS, H % 32 != 0 for
                                  MX rows, or an odd O for a gated product                     */
     MOE_ERR_HIP = -5,         /* the HIP runtime reported an error for a launch               */
@@ -644,6 +644,150 @@ int moe_mx_product(const void *a_codes, const void *a_scales, int64_t a_rows,
                    const int32_t *group_base, int32_t G, const void *w_codes, const void *w_scales,
                    int32_t O, int32_t H, int32_t epilogue, void *out, int64_t out_stride_bytes,
                    hipStream_t stream);
+
+/* ---- The layer in 8 bits around the dispatch -------------------------------------------------------
+ *
+ * Rows in 8 bits with one fp32 scale a row, as the quantised dispatch leaves them (moe_quant: INT8 or E4M3FN
+ * codes, value = code * scale). In all of these calls rows of bf16 are 16-byte aligned, their strides a
+ * multiple of 16 and at least 2H, H is a multiple of 16 in [16, MOE_MAX_HIDDEN]; codes are dense, uint8 [rows, H],
+ * 16-byte aligned, scales dense fp32 [rows]. rows is in [0, MOE_MAX_OUT_ROWS]; buffers of no rows may be NULL.
+ * Unless said otherwise, no output may overlap an input or another output (MOE_ERR_ARG).
+ *
+ * moe_row_quantize: rows 0..N-1 of a bf16 buffer, N = min(*num_rows, max_rows), or max_rows where num_rows is NULL (a
+ *      DEVICE pointer, e.g. &expert_slot_base[E]; negative counts are 0), to codes and scales, exactly as
+ *      moe_dispatch computes them for rows of finite values: scale = amax / top by IEEE division (top = 448 for
+ *      E4M3, 127 for INT8), codes from the correctly rounded fp32 quotient value / scale, to nearest even; a row of
+ *      zeros has scale 0 and zero codes. A row that holds a NaN or an infinity has a NaN for its scale and zero
+ *      codes, so that all of it reads back as NaN.
+ * moe_row_dequantize: bf16(fp32(code * scale)), row r at r * row_stride_bytes; the way back for experts that compute
+ *      in bf16, from moe_unpack's expand_x and expand_scales.
+ * quant is MOE_QUANT_FP8_E4M3_DYN or MOE_QUANT_INT8_DYN (MOE_ERR_ARG otherwise). Rows N..max_rows-1 of the outputs
+ * keep their contents, and so do the bytes between rows. max_rows 0 enqueues nothing. One kernel each. */
+int moe_row_quantize(const void *rows, int64_t row_stride_bytes, const int32_t *num_rows,
+                     int64_t max_rows, int32_t H, int32_t quant, void *codes, float *scales,
+                     hipStream_t stream);
+
+int moe_row_dequantize(const void *codes, const float *scales, const int32_t *num_rows,
+                       int64_t max_rows, int32_t H, int32_t quant, void *rows,
+                       int64_t row_stride_bytes, hipStream_t stream);
+
+/* The experts' product of INT8 rows, one scale a row, with INT8 weights, one scale an output channel: the grouped
+ * GEMM of what moe_unpack leaves of an INT8 dispatch ("HCCL Window 模式 (Non-SHMEM) 代码深度剖析", section 3.9
+ * ShareToOutput). With G = 1 and group_base {0, a_rows} it is a shared expert's or a dense layer's product.
+ *
+ *   c[r, o] = sum over h of A[r, h] * W[g, o, h], exact in int32, for the group g with
+ *             group_base[g] <= r < group_base[g + 1]
+ *   v[r, o] = fp32(fp32(fp32(c[r, o]) * a_scales[r]) * w_scales[g, o]), each step rounded to nearest even
+ *   MOE_MX_PLAIN: out[r, o] = bf16(v[r, o]), o in [0, O)
+ *   MOE_MX_GATED: out[r, o] = bf16(silu(v[r, o]) * v[r, O/2 + o]), o in [0, O/2), with moe_mx_product's silu
+ *
+ * In:  a_codes   int8 [a_rows, H] (two's complement, any of the 256 values), a_scales fp32 [a_rows];
+ *                a_rows in [0, MOE_MAX_OUT_ROWS]; 0 enqueues nothing.
+ *      group_base, G as for moe_mx_product.
+ *      w_codes   int8 [G, O, H], 16-byte aligned; w_scales fp32 [G, O]; O in [1, MOE_MAX_OUTPUTS], even for
+ *                MOE_MX_GATED (MOE_ERR_UNSUPPORTED otherwise).
+ *      epilogue  MOE_MX_PLAIN or MOE_MX_GATED.
+ * Out: out       bf16, row r at r * out_stride_bytes (2-byte aligned, stride even and at least a row of results).
+ *                Rows outside every group, and the bytes between rows, keep their contents.
+ * Enqueues one kernel. */
+int moe_int8_product(const void *a_codes, const float *a_scales, int64_t a_rows,
+                     const int32_t *group_base, int32_t G, const void *w_codes,
+                     const float *w_scales, int32_t O, int32_t H, int32_t epilogue, void *out,
+                     int64_t out_stride_bytes, hipStream_t stream);
+
+/* Element types of a norm's weight and of the router's logits. */
+typedef enum {
+    MOE_BF16 = 1,
+    MOE_FP32 = 2
+} moe_float;
+
+/* The residual's addition and the root-mean-square norm of its sum, on the way from one layer's combine to the next
+ * layer's router and dispatch:
+ *
+ *   sum[t] = bf16(fp32(x[t] + residual[t])), or x[t] where residual is NULL
+ *   y[t]   = fp32(fp32(sum[t] * r) * weight),  r = fp32(1 / sqrt(mean over h of sum[t, h]^2 + eps))
+ *   out[t] = bf16(y[t]);  codes[t], scales[t] = y[t] in 8 bits, as moe_row_quantize has them of its rows
+ *
+ * The mean and the root are taken in 64 bits, so that r is the correctly rounded value but for sums within about 2^-50
+ * of a border, and codes do not depend on an order of additions; y is not rounded to bf16 before it is quantised.
+ *
+ * In:  x          bf16, row t at t * x_stride_bytes; residual likewise, or NULL.
+ *      weight     [H] of weight_type (moe_float), 16-byte aligned.
+ *      eps        above 0 and finite (MOE_ERR_ARG otherwise).
+ *      quant      MOE_QUANT_NONE, or the type of the codes.
+ * Out: sum        bf16, row t at t * sum_stride_bytes: needed with a residual, NULL without. It may be x's or
+ *                 residual's own rows (the same address and stride): the addition is then in place.
+ *      out        bf16 [rows, H], dense, 16-byte aligned; may be NULL with a quant that is not MOE_QUANT_NONE.
+ *      codes, scales  needed with a quant, NULL without.
+ * Enqueues one kernel (none for no rows). */
+int moe_rms_norm(const void *x, int64_t x_stride_bytes, const void *residual,
+                 int64_t residual_stride_bytes, const void *weight, int32_t weight_type, float eps,
+                 int64_t rows, int32_t H, int32_t quant, void *sum, int64_t sum_stride_bytes,
+                 void *out, void *codes, float *scales, hipStream_t stream);
+
+/* Its gradients, of the bf16 output: with g = weight * dy[t] and n = sum[t] * r,
+ *
+ *   dx[t]    = bf16(r * (g - n * mean over h of g * n) + d_sum[t])   (the gradient of x and of residual alike)
+ *   d_weight = sum over t of dy[t] * n
+ *
+ * in fp32 (the row's two means in 64 bits), d_weight's sum in an order fixed by rows and H.
+ * In:  dy         bf16, row t at t * dy_stride_bytes.
+ *      sum        what the forward normed: its sum, or x without a residual; weight, weight_type, eps as there.
+ *      d_sum      the gradient that reaches the sum on its other ways, bf16 rows, or NULL.
+ *      workspace  16-byte aligned, moe_rms_norm_backward_workspace_bytes(rows, H) at least (MOE_ERR_WINDOW); its
+ *                 contents do not matter. Calls that may run at once need one each.
+ * Out: dx         bf16 [rows, H], dense, 16-byte aligned.
+ *      d_weight   fp32 [H], 16-byte aligned, fully overwritten (zeros for no rows).
+ * Enqueues two kernels. */
+int64_t moe_rms_norm_backward_workspace_bytes(int64_t rows, int32_t H);
+
+int moe_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *sum,
+                          int64_t sum_stride_bytes, const void *weight, int32_t weight_type,
+                          float eps, const void *d_sum, int64_t d_sum_stride_bytes, int64_t rows,
+                          int32_t H, void *dx, float *d_weight, void *workspace,
+                          int64_t workspace_bytes, hipStream_t stream);
+
+/* The router's balance loss over the experts' counts, and its gradient.
+ *
+ *   s[t]  = softmax over the experts of logits[t] (MOE_SCORE_SOFTMAX), or sigmoid(logits[t]) over its sum
+ *           (MOE_SCORE_SIGMOID)
+ *   n[e]  = valid entries of topk_idx that name expert e (moe_layout's num_tokens_per_expert), N = sum of n
+ *   T     = tokens with a valid entry; the others (padding) count nowhere, whatever their logits hold
+ *   loss  = coef * E / (N * T) * sum over e of n[e] * (sum over those tokens of s[t, e]);  0 where T is 0
+ *   d_logits[t, e] = d_loss * coef * E / (N * T) * s[t, e] * (n[e] - sum over j of n[j] * s[t, j])
+ *                    (times 1 - sigmoid(logits[t, e]) for MOE_SCORE_SIGMOID); 0 for padding
+ *
+ * The counts have no gradient. Logits of -inf (experts a token may not go to) have score 0 and gradient 0; a token
+ * whose logits are all -inf has no scores. Everything in fp32, the sums over tokens in an order fixed by S and E.
+ * moe_balance_loss
+ * In:  logits     [S, E] of logits_type (moe_float), row t at t * logits_stride_bytes (a multiple of the element and at
+ *                 least E of them), aligned to the element.
+ *      topk_idx   int32 [S, K]; ids outside [0, E) are not valid; an id that stands twice in a row counts twice.
+ *      S in [1, MOE_MAX_TOKENS], K in [1, MOE_MAX_K], E in [1, MOE_MAX_EXPERTS]; coef finite.
+ *      workspace  16-byte aligned, moe_balance_loss_workspace_bytes(S, E) at least (MOE_ERR_WINDOW); its contents
+ *                 do not matter. Calls that may run at once need one each.
+ * Out: loss fp32 [1], num_tokens_per_expert int32 [E], num_tokens int32 [1] (T). Enqueues at most two kernels.
+ * moe_balance_loss_backward
+ * In:  d_loss fp32 [1] and the forward's arguments and counts, all DEVICE pointers. (Counts that are summed over
+ *      several GPUs give the gradient of the loss over them, with num_tokens the local T.)
+ * Out: d_logits   [S, E] of logits_type, dense. Enqueues one kernel. */
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0,
+    MOE_SCORE_SIGMOID = 1
+} moe_score;
+
+int64_t moe_balance_loss_workspace_bytes(int32_t S, int32_t E);
+
+int moe_balance_loss(const void *logits, int64_t logits_stride_bytes, int32_t logits_type,
+                     const int32_t *topk_idx, int32_t S, int32_t K, int32_t E, int32_t score,
+                     float coef, float *loss, int32_t *num_tokens_per_expert, int32_t *num_tokens,
+                     void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+int moe_balance_loss_backward(const float *d_loss, const void *logits, int64_t logits_stride_bytes,
+                              int32_t logits_type, const int32_t *topk_idx,
+                              const int32_t *num_tokens_per_expert, const int32_t *num_tokens,
+                              int32_t S, int32_t K, int32_t E, int32_t score, float coef,
+                              void *d_logits, hipStream_t stream);
 
 /* Static description of a moe_status value (never NULL). */
 const char *moe_status_string(int status);

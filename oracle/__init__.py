@@ -46,6 +46,16 @@ from .unpack import aligned_row_base, unpack, unpack_padded
 from .dedup import dispatch_dedup, expand_dedup, rank_rows
 from .backward import combine_backward, dispatch_backward
 from .mx import mx_product, mx_quantize, mx_values
+from .layer import (
+    balance,
+    int8_product,
+    int8_sums,
+    rms_norm,
+    rms_norm_backward,
+    row_quantize,
+    row_quantize_f32,
+    row_values,
+)
 
 __all__ = [
     "bf16_bits_to_f32",
@@ -76,4 +86,12 @@ __all__ = [
     "mx_quantize",
     "mx_values",
     "mx_product",
+    "balance",
+    "int8_product",
+    "int8_sums",
+    "rms_norm",
+    "rms_norm_backward",
+    "row_quantize",
+    "row_quantize_f32",
+    "row_values",
 ]
