@@ -17,37 +17,290 @@ __device__ inline i32x4 mfma(const i32x4 &a, const i32x4 &b, const i32x4 &c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// A wave takes 16 rows of a group and 32 weight rows (16 outputs when GATED).
+// fp32(fp32(c * a) * w): a result's value from its sum and its two scales.
+__device__ inline float scaled(int c, float a, float w) { return (float)c * a * w; }
+
+// Tiles of TM rows x TN weight rows (TN / 2 outputs when GATED), WMC x WNC waves, through LDS. The 8 XCDs get
+// contiguous eighths of the tiles (workgroup b runs on XCD b % 8).
+//
+// Codes go from memory straight to LDS in pairs of stages of 64 values, 128 bytes of a row (whole lines), through PAIRS
+// buffers: while one is multiplied the others fill. One barrier a pair: it follows each wave's wait for its own loads of
+// the pair and for its LDS reads of the last one, so behind it the pair is whole and the last pair's buffer is free.
+//
+// PAIRS == 2, many tiles: a workgroup takes tile after tile, the next tile's first pair behind a tile's last, so that
+// the loads never pause and a tile's results are stored while the next one's rows arrive.
+//
+// PAIRS > 2, tiles for every compute unit once at most: a workgroup takes one tile, whose time is its pairs' way
+// from memory and through the matrix cores.
+template <int TM, int TN, int WMC, int WNC, int PAIRS, bool GATED>
+__global__ __launch_bounds__(64 * WMC * WNC) void int8_tile_kernel(
+    const uint8_t *__restrict__ a_codes, const float *__restrict__ a_scales, int64_t a_rows,
+    const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
+    const float *__restrict__ w_scales, int O, int H, int ncol, uint8_t *__restrict__ out, int64_t out_stride,
+    bool wide) {
+    constexpr int NW = WMC * WNC;
+    constexpr int ROWS = TM + TN, WM = TM / WMC, WN = TN / WNC, MI = WM / 16, NI = WN / 16;
+    constexpr int LOADS = ROWS / 8 / NW;     // 8 rows of a pair of stages a load
+    constexpr int OF = GATED ? NI / 2 : NI;  // column fragments of results
+    constexpr int STORES = MI * OF / 2;      // stores of a wave, 16 bytes a lane
+    static_assert((PAIRS == 2 || PAIRS == 4) && LOADS * 8 * NW == ROWS && OF % 2 == 0 && MI * 16 * WMC == TM && NI * 16 * WNC == TN, "shape");
+    // the buffers are objects of their own, so that the compiler sees the reads of one and the loads into the
+    // other apart and puts no wait between them
+    __shared__ __align__(1024) uint8_t pair0[ROWS * 128], pair1[ROWS * 128];
+    __shared__ __align__(1024) uint8_t pair2[PAIRS > 2 ? ROWS * 128 : 16], pair3[PAIRS > 2 ? ROWS * 128 : 16];
+    uint8_t *const codes[4] = {pair0, pair1, pair2, pair3};
+    __shared__ TileTable table;
+
+    const int width = GATED ? O / 2 : O;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (wave == 0) fill_table<TM>(table, base, G, a_rows);
+    __syncthreads();
+    const int all = __builtin_amdgcn_readfirstlane(table.end[G - 1]) * ncol, share = (all + 7) >> 3;
+    const int xcd_end = min(((int)(blockIdx.x & 7) + 1) * share, all), step = gridDim.x >> 3;
+    int t = (int)(blockIdx.x & 7) * share + (int)(blockIdx.x >> 3);
+    if (t >= xcd_end) return;
+
+    // Load l of a wave takes tile rows 8 (wave + l * NW) .. + 7, a lane 16 bytes: place lane % 8 of row lane / 8.
+    // Place p of row r holds block p ^ (r % 8): eight neighbouring rows' reads of one block then cover all the
+    // banks.
+    const int r8 = lane >> 3, blk = (lane & 7) ^ r8;
+    struct Source {
+        __amdgpu_buffer_rsrc_t a, w;
+        int base[LOADS];  // byte offset of the load's first row, the same for the whole wave
+    };
+    const auto source_of = [&](const Tile &tile) {
+        Source src;
+        src.a = rsrc(a_codes + (int64_t)tile.first * H, (int64_t)tile.rows * H);
+        src.w = rsrc(w_codes + (int64_t)tile.group * O * H, (int64_t)O * H);
+        const int o0 = tile.col * (GATED ? TN / 2 : TN);
+        // Row of the weights behind tile row j: plain, neighbours; gated, each wave's share of the tile has its
+        // gate rows first, then the up rows of the same outputs. Rows past the matrix read as zero, rows past the
+        // gates are up rows: neither's results are stored.
+        const auto weight_row = [&](int j) {
+            if (!GATED) return o0 + j;
+            const int part = j / WN, jj = j % WN, o = o0 + part * (WN / 2) + jj % (WN / 2);
+            return jj < WN / 2 ? o : width + o;
+        };
+#pragma unroll
+        for (int l = 0; l < LOADS; ++l) {
+            const int r = 8 * (wave + l * NW);
+            src.base[l] = (r < TM ? r : weight_row(r - TM)) * H;
+        }
+        return src;
+    };
+    const int place = r8 * H + blk * 16;
+    const auto load_codes = [&](const Source &src, int pair, uint8_t *buf, bool none) {
+        const bool past = none || pair * 128 + blk * 16 >= H;  // blocks behind the row's end read as zero
+#pragma unroll
+        for (int l = 0; l < LOADS; ++l)
+            load_to_lds(8 * (wave + l * NW) < TM ? src.a : src.w, &buf[(wave + l * NW) * 1024],
+                        past ? 0x7FFFFFF0 : src.base[l] + place, pair * 128);
+    };
+
+    const int wm = (wave % WMC) * WM, wn = TM + (wave / WMC) * WN;
+    const int fr = lane & 15, q = lane >> 4;
+    const int at0 = fr * 128 + (q ^ (fr & 7)) * 16, at1 = fr * 128 + ((q + 4) ^ (fr & 7)) * 16;
+    const int stages = (H + 63) / 64, pairs = (stages + 1) / 2;
+
+    i32x4 acc[MI][NI];
+    i32x4 a[MI], w[NI];
+    const auto read_codes = [&](const uint8_t *buf, int at) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j) w[j] = *reinterpret_cast<const i32x4 *>(&buf[(wn + j * 16) * 128 + at]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) a[i] = *reinterpret_cast<const i32x4 *>(&buf[(wm + i * 16) * 128 + at]);
+    };
+    const auto multiply = [&]() {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = mfma(w[j], a[i], acc[i][j]);
+    };
+
+    Tile tile = find_tile<TM>(table, G, ncol, t);
+    Source cur = source_of(tile);
+#pragma unroll
+    for (int i = 0; i < PAIRS - 1; ++i) load_codes(cur, i, codes[i], false);
+    bool stored = false;  // the stores of the tile before are still in flight, STORES of them
+    for (;;) {
+        t += step;
+        const bool more = PAIRS == 2 && t < xcd_end;
+        Tile next = tile;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+        // a round is a pair in each buffer, so that a buffer's number is a constant
+        for (int p0 = 0; p0 < pairs; p0 += PAIRS) {
+            const bool last = p0 + PAIRS >= pairs;
+#pragma unroll
+            for (int b = 0; b < PAIRS; ++b) {
+                const int p = p0 + b;
+                if (PAIRS == 2 && b == 0 && p0 == 0 && stored) stage_barrier<STORES>();
+                else stage_barrier<(PAIRS - 2) * LOADS>();
+                read_codes(codes[b], at0);
+                if (PAIRS > 2) {
+                    load_codes(cur, p + PAIRS - 1, codes[(b + PAIRS - 1) % PAIRS], false);
+                } else if (b == 0) {
+                    load_codes(cur, p + 1, codes[1], false);
+                    if (last && more) {
+                        next = find_tile<TM>(table, G, ncol, t);
+                        cur = source_of(next);
+                    }
+                } else {
+                    // behind the tile's last pair comes the next tile's first one
+                    load_codes(cur, last ? 0 : p + 1, codes[0], last && !more);
+                }
+                __builtin_amdgcn_sched_barrier(0);  // the reads and loads are under way before the products
+                if (p < pairs) multiply();
+                __builtin_amdgcn_sched_barrier(0);
+                read_codes(codes[b], at1);
+                if (2 * p + 1 < stages) multiply();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+
+        // A lane holds four neighbouring results of a row; swapping 16-lane rows between two column fragments
+        // gives it eight, 16 bytes. With aligned rows every store goes out, past the tile's end to nowhere, so
+        // that the next stages' waits know how many there are.
+        const int o0 = tile.col * (GATED ? TN / 2 : TN) + (wave / WMC) * (GATED ? WN / 2 : WN);
+        const __amdgpu_buffer_rsrc_t dst = rsrc(out + tile.first * out_stride, wide ? tile.rows * out_stride : 0);
+        const __amdgpu_buffer_rsrc_t sa_src = rsrc(a_scales + tile.first, tile.rows * 4);
+        const __amdgpu_buffer_rsrc_t sw_src = rsrc(w_scales + (int64_t)tile.group * O, (int64_t)O * 4);
+        float sa[MI];
+        float sw[NI][4];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            sa[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sa_src, (wm + i * 16 + fr) * 4, 0, 0));
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sw[j][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                    sw_src, (o0 + (j % OF) * 16 + 4 * q + e + (j >= OF ? width : 0)) * 4, 0, 0));
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int r = wm + i * 16 + fr;
+#pragma unroll
+            for (int j = 0; j < OF; j += 2) {
+                uint32_t v[2][2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float f[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int up = (j + k + OF) % NI;
+                        f[e] = scaled(acc[i][j + k][e], sa[i], sw[j + k][e]);
+                        if (GATED) f[e] = silu_times(f[e], scaled(acc[i][up][e], sa[i], sw[up][e]));
+                    }
+                    v[k][0] = bf16_pair(f[0], f[1]);
+                    v[k][1] = bf16_pair(f[2], f[3]);
+                }
+                const auto lo = __builtin_amdgcn_permlane16_swap(v[0][0], v[1][0], false, false);
+                const auto hi = __builtin_amdgcn_permlane16_swap(v[0][1], v[1][1], false, false);
+                const u32x4 r8 = {lo[0], hi[0], lo[1], hi[1]};
+                const int o = o0 + (j + (q & 1)) * 16 + (q >> 1) * 8;
+                if (wide) {
+                    const bool in = r < tile.rows && o < width;
+                    __builtin_amdgcn_raw_buffer_store_b128(r8, dst, in ? r * (int)out_stride + o * 2 : 0x7FFFFFF0, 0, 0);
+                } else if (r < tile.rows) {
+                    uint16_t *to = reinterpret_cast<uint16_t *>(out + ((int64_t)tile.first + r) * out_stride) + o;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (o + e < width) to[e] = (uint16_t)(r8[e >> 1] >> (16 * (e & 1)));
+                }
+            }
+        }
+        stored = wide;
+        if (!more) break;
+        tile = next;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the wave's end
+}
+
+// Few rows a group: the weights' bytes bound the product. A workgroup takes 16 rows of a group and 32 weight
+// rows (16 outputs when GATED), its four waves a quarter of H each, and every wave streams its quarter
+// through a ring of its own in LDS, waiting for nobody; the partial sums meet in LDS. LDS turns the loads' order (four
+// lanes to a row, 64 bytes) into the matrix cores' (a lane to a row).
+constexpr int kSmallWaves = 4;
+constexpr int kRing = 4;  // buffers of a wave's ring, of 64 values each
+
 template <bool GATED>
-__global__ __launch_bounds__(64) void product_kernel(const uint8_t *__restrict__ a_codes, const float *__restrict__ a_scales, int64_t a_rows,
-                                                     const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
-                                                     const float *__restrict__ w_scales, int O, int H, uint8_t *__restrict__ out, int64_t out_stride) {
+__global__ __launch_bounds__(64 * kSmallWaves) void int8_small_kernel(
+    const uint8_t *__restrict__ a_codes, const float *__restrict__ a_scales, int64_t a_rows,
+    const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
+    const float *__restrict__ w_scales, int O, int H, uint8_t *__restrict__ out, int64_t out_stride) {
+    constexpr int F = 3;  // fragments of 16 rows: the rows, then two of the weights
+    __shared__ __align__(1024) uint8_t ring0[kSmallWaves][F * 1024], ring1[kSmallWaves][F * 1024], ring2[kSmallWaves][F * 1024],
+        ring3[kSmallWaves][F * 1024];
     int g;
     int64_t first, last;
+    const int col = blockIdx.y;
     if (!find_rows<16>(base, G, a_rows, blockIdx.x, g, first, last)) return;
     g = __builtin_amdgcn_readfirstlane(g);
     first = __builtin_amdgcn_readfirstlane((int)first);
     last = __builtin_amdgcn_readfirstlane((int)last);
-    const int lane = threadIdx.x & 63, fr = lane & 15, q = lane >> 4, rows = (int)(last - first);
-    const int width = GATED ? O / 2 : O, o0 = blockIdx.y * (GATED ? 16 : 32);
-    const uint8_t *arow = a_codes + (first + min(fr, rows - 1)) * H;
-    const uint8_t *wrow[2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, q = lane >> 4;
+    const int width = GATED ? O / 2 : O, o0 = col * (GATED ? 16 : 32);
+    uint8_t *const codes[kRing] = {ring0[wave], ring1[wave], ring2[wave], ring3[wave]};
+    const int rows = (int)(last - first);
+    const __amdgpu_buffer_rsrc_t a_src = rsrc(a_codes + first * H, (int64_t)rows * H);
+    const __amdgpu_buffer_rsrc_t w_src = rsrc(w_codes + (int64_t)g * O * H, (int64_t)O * H);
+    // row r of the tile's, in its own matrix; rows past the end repeat the last one
+    const auto row_of = [&](int r) {
+        if (r < 16) return min(r, rows - 1);
+        const int j = r - 16;
+        return GATED ? min(o0 + (j & 15), width - 1) + (j >> 4) * width : min(o0 + j, width - 1);
+    };
+    const int r4 = lane >> 2, blk = (lane & 3) ^ ((r4 >> 1) & 3);  // places against bank conflicts, as in the tiles
+    int voff[F];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int o = GATED ? min(o0 + fr, width - 1) + j * width : min(o0 + 16 * j + fr, width - 1);
-        wrow[j] = w_codes + ((int64_t)g * O + o) * H;
-    }
+    for (int f = 0; f < F; ++f) voff[f] = row_of(16 * f + r4) * H + blk * 16;
+
+    const int steps = (H + 63) / 64;
+    const int share = (steps + kSmallWaves - 1) / kSmallWaves;
+    const int begin = min(wave * share, steps), count = min(share, steps - begin);
+    const auto load_codes = [&](int i, uint8_t *buf) {  // step i of the wave's
+        const bool past = i >= count || (begin + i) * 64 + blk * 16 >= H;
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            load_to_lds(f == 0 ? a_src : w_src, &buf[f * 1024], past ? 0x7FFFFFF0 : voff[f], (begin + i) * 64);
+    };
     i32x4 acc[2] = {i32x4{0, 0, 0, 0}, i32x4{0, 0, 0, 0}};
-    for (int k = 0; k < H; k += 64) {
-        const int at = k + 16 * q;
-        i32x4 a = {0, 0, 0, 0}, w[2] = {a, a};
-        if (at < H) {
-            a = *reinterpret_cast<const i32x4 *>(arow + at);
-            w[0] = *reinterpret_cast<const i32x4 *>(wrow[0] + at);
-            w[1] = *reinterpret_cast<const i32x4 *>(wrow[1] + at);
+#pragma unroll
+    for (int s = 0; s < kRing - 1; ++s) load_codes(s, codes[s]);
+    const int at = fr * 64 + (q ^ ((fr >> 1) & 3)) * 16;
+    for (int i0 = 0; i0 < count; i0 += kRing) {
+#pragma unroll
+        for (int s = 0; s < kRing; ++s) {
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kRing - 2) * F) : "memory");
+            load_codes(i0 + s + kRing - 1, codes[(s + kRing - 1) % kRing]);
+            i32x4 v[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f) v[f] = *reinterpret_cast<const i32x4 *>(&codes[s][f * 1024 + at]);
+            // behind the wave's steps the codes are zero
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[j] = mfma(v[1 + j], v[0], acc[j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        acc[0] = mfma(w[0], a, acc[0]);
-        acc[1] = mfma(w[1], a, acc[1]);
+    }
+    // every load has arrived before the rings hold sums, and before the wave ends
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    i32x4 *const partial = reinterpret_cast<i32x4 *>(&ring0[0][0]);  // [wave][fragment][lane]
+#pragma unroll
+    for (int j = 0; j < 2; ++j) partial[(wave * 2 + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    // the first wave adds and stores gate and up, the first two a fragment each of a plain product
+    if (wave >= (GATED ? 1 : 2)) return;
+    i32x4 sum = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < kSmallWaves; ++k) {
+        sum += partial[(k * 2 + wave) * 64 + lane];
+        if (GATED) up += partial[(k * 2 + 1) * 64 + lane];
     }
     if (fr >= rows) return;
     const float sa = a_scales[first + fr];
@@ -55,19 +308,53 @@ __global__ __launch_bounds__(64) void product_kernel(const uint8_t *__restrict__
     uint16_t *dst = reinterpret_cast<uint16_t *>(out + (first + fr) * out_stride);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if (GATED) {
-            const int o = o0 + 4 * q + e;
-            if (o >= width) continue;
-            const float gate = (float)acc[0][e] * sa * sw[o], up = (float)acc[1][e] * sa * sw[width + o];
-            dst[o] = (uint16_t)bf16_pair(silu_times(gate, up), 0.0f);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int o = o0 + 16 * j + 4 * q + e;
-                if (o < width) dst[o] = (uint16_t)bf16_pair((float)acc[j][e] * sa * sw[o], 0.0f);
-            }
-        }
+        const int o = o0 + 16 * wave + 4 * q + e;
+        if (o >= width) continue;
+        float v = scaled(sum[e], sa, sw[o]);
+        if (GATED) v = silu_times(v, scaled(up[e], sa, sw[width + o]));
+        dst[o] = (uint16_t)bf16_pair(v, 0.0f);
     }
+}
+
+struct Args {
+    const uint8_t *a_codes;
+    const float *a_scales;
+    int64_t a_rows;
+    const int32_t *base;
+    int G;
+    const uint8_t *w_codes;
+    const float *w_scales;
+    int O, H;
+    bool gated;
+    uint8_t *out;
+    int64_t out_stride;
+    bool wide;
+    hipStream_t stream;
+};
+
+hipError_t few_rows(const Args &p) {
+    const int64_t row_tiles = p.a_rows / 16 + (p.a_rows < p.G ? p.a_rows : p.G);  // at most
+    const int ncol = p.gated ? (p.O / 2 + 15) / 16 : (p.O + 31) / 32;
+    auto *kernel = p.gated ? int8_small_kernel<true> : int8_small_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)row_tiles, ncol), dim3(64 * kSmallWaves), 0, p.stream, p.a_codes,
+                       p.a_scales, p.a_rows, p.base, p.G, p.w_codes, p.w_scales, p.O, p.H, p.out, p.out_stride);
+    return hipGetLastError();
+}
+
+constexpr int kUnits = 256;  // compute units of an MI355X
+
+template <int TM, int TN, int WMC, int WNC, int PAIRS>
+hipError_t tiles(const Args &p) {
+    constexpr int resident = (TM + TN) * PAIRS > 640 ? kUnits : 2 * kUnits;  // workgroups that run at once, by their LDS
+    const int width = p.gated ? p.O / 2 : p.O, tn = p.gated ? TN / 2 : TN;
+    const int ncol = (width + tn - 1) / tn;
+    const int64_t row_tiles = p.a_rows / TM + (p.a_rows < p.G ? p.a_rows : p.G);  // at most
+    const int64_t need = (row_tiles * ncol + 7) / 8 * 8;
+    const int64_t grid = PAIRS > 2 || need < resident ? need : resident;
+    auto *kernel = p.gated ? int8_tile_kernel<TM, TN, WMC, WNC, PAIRS, true> : int8_tile_kernel<TM, TN, WMC, WNC, PAIRS, false>;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WMC * WNC), 0, p.stream, p.a_codes, p.a_scales, p.a_rows,
+                       p.base, p.G, p.w_codes, p.w_scales, p.O, p.H, ncol, p.out, p.out_stride, p.wide);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -78,13 +365,27 @@ hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64
                                void *out, int64_t out_stride_bytes, hipStream_t stream) {
     if (a_rows == 0) return hipSuccess;
     const bool gated = epilogue == MOE_MX_GATED;
-    const int64_t row_tiles = a_rows / 16 + (a_rows < G ? a_rows : G);  // at most
-    const int ncol = gated ? (O / 2 + 15) / 16 : (O + 31) / 32;
-    auto *kernel = gated ? product_kernel<true> : product_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)row_tiles, ncol), dim3(64), 0, stream, static_cast<const uint8_t *>(a_codes),
-                       a_scales, a_rows, group_base, G, static_cast<const uint8_t *>(w_codes), w_scales, O, H,
-                       static_cast<uint8_t *>(out), out_stride_bytes);
-    return hipGetLastError();
+    const int width = gated ? O / 2 : O;
+    // rows of whole 16-byte pieces, and a tile of them within a buffer descriptor's range
+    const bool wide = width % 8 == 0 && out_stride_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
+                      out_stride_bytes <= (1 << 22);
+    const Args p = {static_cast<const uint8_t *>(a_codes), a_scales, a_rows, group_base, G,
+                    static_cast<const uint8_t *>(w_codes), w_scales, O, H, gated, static_cast<uint8_t *>(out),
+                    out_stride_bytes, wide, stream};
+    const int64_t hit = a_rows < G ? a_rows : G, mean = (a_rows + hit - 1) / hit;
+    const int64_t most = hit > 1 ? mean + mean / 4 : mean;
+    const auto tiles_of = [&](int tm, int tn) {
+        const int outs = gated ? tn / 2 : tn;
+        return hit * ((most + tm - 1) / tm) * ((width + outs - 1) / outs);
+    };
+    if (tiles_of(16, 32) * ((most < 16 ? most : 16) + 32) <= 320 * 48) return few_rows(p);
+    if (tiles_of(32, 64) <= (most <= 32 ? 448 : kUnits)) return tiles<32, 64, 2, 1, 4>(p);
+    if (tiles_of(64, 64) <= kUnits) return tiles<64, 64, 4, 1, 4>(p);
+    if (tiles_of(64, 128) <= kUnits) return tiles<64, 128, 2, 2, 4>(p);
+    const int64_t large = tiles_of(256, 256);
+    if (mean >= 160 && (large >= 4 * kUnits || (H >= 4096 && large >= 192 && large <= kUnits))) return tiles<256, 256, 2, 4, 2>(p);
+    if (mean >= 40 && tiles_of(128, 128) >= 300) return tiles<128, 128, 2, 2, 2>(p);
+    return tiles<64, 128, 2, 2, 2>(p);
 }
 
 }  // namespace moe
