@@ -3,116 +3,125 @@
 // A wave takes a token: lane l holds experts l, l + 64, ... of it, so that its scores are two reductions over the wave's
 // lanes, and their sums over tokens stay in its registers. All of it is a few bytes and operations a logit.
 
-#include "moe_internal.h"
+#include "wave_ops.h"
 
 namespace moe {
 namespace {
 
 typedef __bf16 bf16_t;
 
+constexpr int kPartThreads = 1024, kPartWaves = kPartThreads / 64;
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kFinishThreads = 1024;
+constexpr int kBackwardGrid = 1024;
 
-__device__ inline float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
+// exp(x) for x <= 0 to 2 ulp, from the hardware's exp2 of x * log2(e) and the rest of that product; 0 from -200 down, NaN of a
+// NaN. A third of the library function's instructions, which bound these kernels.
+__device__ inline float exp_of(float x) {
+    constexpr float kLog2e = 1.44269502e+00f, kLog2eRest = 1.92596299e-08f, kLn2 = 6.93147182e-01f;
+    x = x < -200.0f ? -200.0f : x;
+    const float t = x * kLog2e;
+    const float rest = __builtin_fmaf(x, kLog2eRest, __builtin_fmaf(x, kLog2e, -t));
+    const float y = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(y, rest * kLn2, y);
 }
 
-__device__ inline int wave_sum(int v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
-}
-
-__device__ inline float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
-}
-
-// The scores of one token from its logits (-inf past E): exp(l - max) over their sum, or sigmoids over theirs. Those are
-// taken as exp(min(l, 0) - min(max, 0)) / (1 + exp(-|l|)), sigmoid(l) but for one factor, so that a token whose
-// logits are all far below zero keeps its scores. With no logit above -inf there are none.
+// The scores of one token from its logits (-inf past E): exp(l - max) over their sum, or sigmoids over theirs. A token whose
+// logits are all far below zero, where sigmoid(l) is exp(l) to fp32, keeps its scores: they are taken against the
+// largest. With no logit above -inf there are none. turn: 1 - sigmoid(l), for MOE_SCORE_SIGMOID.
 template <int N, int SCORE>
-__device__ inline void scores_of(const float (&l)[N], float (&s)[N]) {
+__device__ inline void scores_of(const float (&l)[N], float (&s)[N], float (&turn)[N]) {
     float top = l[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmaxf(top, l[i]);
-    top = wave_max(top);
+    top = wave::most(top);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        s[i] = SCORE == MOE_SCORE_SIGMOID ? expf(fminf(l[i], 0.0f) - fminf(top, 0.0f)) / (1.0f + expf(-fabsf(l[i])))
-                                          : expf(l[i] - top);
+        if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+            const float far = exp_of(-fabsf(l[i])), share = __builtin_amdgcn_rcpf(1.0f + far);
+            turn[i] = (l[i] > 0.0f ? far : 1.0f) * share;
+            s[i] = top < -60.0f ? exp_of(l[i] - top) : (l[i] > 0.0f ? 1.0f : far) * share;
+        } else {
+            s[i] = exp_of(l[i] - top);
+        }
         sum += s[i];
     }
-    sum = wave_sum(sum);
     const bool none = top == -__builtin_inff();
+    const float each = 1.0f / wave::sum(sum);
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = none ? 0.0f : s[i] / sum;
+    for (int i = 0; i < N; ++i) s[i] = none ? 0.0f : s[i] * each;
 }
 
+// A token's logits (-inf past E) and entries (-1 past K) in a wave's lanes; nothing of tokens past the end.
 template <int N, class T>
-__device__ inline void load_logits(const uint8_t *__restrict__ row, int E, float (&l)[N]) {
-    const int lane = threadIdx.x & 63;
+struct Token {
+    float l[N];
+    int id;
+    __device__ void load(const uint8_t *__restrict__ logits, int64_t stride, const int32_t *__restrict__ topk, int t, int end, int K, int E) {
+        const int lane = threadIdx.x & 63;
+        const T *row = reinterpret_cast<const T *>(logits + t * stride);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = e < E ? (float)reinterpret_cast<const T *>(row)[e] : -__builtin_inff();
+        for (int i = 0; i < N; ++i) l[i] = t < end && lane + 64 * i < E ? (float)row[lane + 64 * i] : -__builtin_inff();
+        id = t < end && lane < K ? topk[(int64_t)t * K + lane] : -1;
     }
-}
+};
 
 // loss from the counts and the sums of scores; n entries and tokens in all. Every lane of a wave calls this with its
 // share of sum over e of count * score sum.
 __device__ inline float loss_of(double share, int64_t n, int tokens, int E, float coef) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) share += __shfl_xor(share, d, 64);
+    share = wave::sum(share);
     return tokens ? (float)(share * ((double)coef * E / ((double)n * tokens))) : 0.0f;
 }
 
-// Part p takes tokens [p * per, ...), its waves every fourth of them. A single part finishes by itself; several leave
-// their sums, counts and tokens in the workspace.
+// Part p takes tokens [p * per, ...), its waves every sixteenth of them, the next one's loads under way. A single part
+// finishes by itself; several leave their sums, counts and tokens in the workspace.
 template <int N, int SCORE, class T>
-__global__ __launch_bounds__(kThreads) void balance_parts_kernel(
+__global__ __launch_bounds__(kPartThreads) void balance_parts_kernel(
     const uint8_t *__restrict__ logits, int64_t stride, const int32_t *__restrict__ topk, int S, int K, int E,
     int per, float coef, float *__restrict__ loss, int32_t *__restrict__ counts, int32_t *__restrict__ tokens,
     float *__restrict__ part_sums, int32_t *__restrict__ part_counts, int32_t *__restrict__ part_tokens) {
-    __shared__ int32_t count[MOE_MAX_EXPERTS];
-    __shared__ float sums[kWaves][MOE_MAX_EXPERTS];
-    __shared__ int32_t live[kWaves];
+    __shared__ int32_t count[64 * N];
+    __shared__ float sums[kPartWaves][64 * N];
+    __shared__ int32_t live[kPartWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int e = tid; e < E; e += kThreads) count[e] = 0;
+    for (int e = tid; e < 64 * N; e += kPartThreads) count[e] = 0;
     __syncthreads();
     float acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     int lives = 0;
     const int end = min(S, (int)(blockIdx.x + 1) * per);
-    for (int t = blockIdx.x * per + wave; t < end; t += kWaves) {
-        float l[N], s[N];
-        load_logits<N, T>(logits + t * stride, E, l);
-        const int e = lane < K ? topk[(int64_t)t * K + lane] : -1;
-        const bool valid = e >= 0 && e < E;
-        if (valid) atomicAdd(&count[e], 1);
+    int t = blockIdx.x * per + wave;
+    Token<N, T> next;
+    next.load(logits, stride, topk, t, end, K, E);
+    for (; t < end; t += kPartWaves) {
+        const Token<N, T> token = next;
+        next.load(logits, stride, topk, t + kPartWaves, end, K, E);
+        const bool valid = token.id >= 0 && token.id < E;
+        if (valid) atomicAdd(&count[token.id], 1);
         if (!__any(valid)) continue;
         ++lives;
-        scores_of<N, SCORE>(l, s);
+        float s[N], turn[N];
+        scores_of<N, SCORE>(token.l, s, turn);
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += s[i];
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (lane + 64 * i < E) sums[wave][lane + 64 * i] = acc[i];
+    for (int i = 0; i < N; ++i) sums[wave][lane + 64 * i] = acc[i];
     if (lane == 0) live[wave] = lives;
     __syncthreads();
     int all = 0;
-    for (int w = 0; w < kWaves; ++w) all += live[w];
+    for (int w = 0; w < kPartWaves; ++w) all += live[w];
+    const auto sum_of = [&](int e) {
+        float s = sums[0][e];
+#pragma unroll
+        for (int w = 1; w < kPartWaves; ++w) s += sums[w][e];
+        return s;
+    };
     if (gridDim.x > 1) {
-        for (int e = tid; e < E; e += kThreads) {
-            float s = sums[0][e];
-            for (int w = 1; w < kWaves; ++w) s += sums[w][e];
-            part_sums[(int64_t)blockIdx.x * E + e] = s;
+        for (int e = tid; e < E; e += kPartThreads) {
+            part_sums[(int64_t)blockIdx.x * E + e] = sum_of(e);
             part_counts[(int64_t)blockIdx.x * E + e] = count[e];
         }
         if (tid == 0) part_tokens[blockIdx.x] = all;
@@ -122,13 +131,11 @@ __global__ __launch_bounds__(kThreads) void balance_parts_kernel(
     double share = 0.0;
     int n = 0;
     for (int e = lane; e < E; e += 64) {
-        float s = sums[0][e];
-        for (int w = 1; w < kWaves; ++w) s += sums[w][e];
-        share += (double)count[e] * (double)s;
+        share += (double)count[e] * (double)sum_of(e);
         n += count[e];
         counts[e] = count[e];
     }
-    const float value = loss_of(share, wave_sum(n), all, E, coef);
+    const float value = loss_of(share, wave::sum(n), all, E, coef);
     if (lane == 0) *loss = value, *tokens = all;
 }
 
@@ -144,6 +151,7 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
     float s = 0.0f;
     int c = 0;
     if (e < E)
+#pragma unroll 8
         for (int p = slice; p < parts; p += slices) {
             s += part_sums[(int64_t)p * E + e];
             c += part_counts[(int64_t)p * E + e];
@@ -166,8 +174,8 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
         counts[at] = all;
     }
     for (int p = tid; p < parts; p += 64) lives += part_tokens[p];
-    lives = wave_sum(lives);
-    const float value = loss_of(share, wave_sum(n), lives, E, coef);
+    lives = wave::sum(lives);
+    const float value = loss_of(share, wave::sum(n), lives, E, coef);
     if (tid == 0) *loss = value, *tokens = lives;
 }
 
@@ -185,32 +193,32 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(
         n[i] = lane + 64 * i < E ? counts[lane + 64 * i] : 0;
         sum += n[i];
     }
-    sum = wave_sum(sum);
+    sum = wave::sum(sum);
     const int mean = sum / E;
     const double all = (double)sum * (double)*tokens;
     const float each = all > 0.0 ? (float)((double)coef * E / all) * *d_loss : 0.0f;
-    for (int t = blockIdx.x * kWaves + (threadIdx.x >> 6); t < S; t += step) {
-        float l[N], s[N], g[N];
-        load_logits<N, T>(logits + t * stride, E, l);
-        const int id = lane < K ? topk[(int64_t)t * K + lane] : -1;
-        const bool lives = __any(id >= 0 && id < E);
-        scores_of<N, SCORE>(l, s);
+    int t = blockIdx.x * kWaves + (threadIdx.x >> 6);
+    Token<N, T> next;
+    next.load(logits, stride, topk, t, S, K, E);
+    for (; t < S; t += step) {
+        const Token<N, T> token = next;
+        next.load(logits, stride, topk, t + step, S, K, E);
+        const bool lives = __any(token.id >= 0 && token.id < E);
+        float s[N], turn[N], g[N];
+        scores_of<N, SCORE>(token.l, s, turn);
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             g[i] = (float)(n[i] - mean);
             dot += lane + 64 * i < E ? g[i] * s[i] : 0.0f;
         }
-        dot = wave_sum(dot);
+        dot = wave::sum(dot);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e = lane + 64 * i;
             if (e >= E) continue;
             float d = each * (s[i] * (g[i] - dot));
-            if (SCORE == MOE_SCORE_SIGMOID) {
-                const float far = expf(-fabsf(l[i]));
-                d *= (l[i] > 0.0f ? far : 1.0f) / (1.0f + far);
-            }
+            if (SCORE == MOE_SCORE_SIGMOID) d *= turn[i];
             d_logits[(int64_t)t * E + e] = (T)(lives ? d : 0.0f);
         }
     }
@@ -246,7 +254,7 @@ hipError_t launch_balance_loss(const void *logits, int64_t logits_stride_bytes, 
     int32_t *tokens = parts > 1 ? counts + (int64_t)parts * E : nullptr;
     dispatch(E, logits_type, score, [&](auto n, auto s, auto element) {
         hipLaunchKernelGGL((balance_parts_kernel<decltype(n)::value, decltype(s)::value, decltype(element)>), dim3(parts),
-                           dim3(kThreads), 0, stream, static_cast<const uint8_t *>(logits), logits_stride_bytes, topk_idx,
+                           dim3(kPartThreads), 0, stream, static_cast<const uint8_t *>(logits), logits_stride_bytes, topk_idx,
                            S, K, E, per, coef, loss, num_tokens_per_expert, num_tokens, sums, counts, tokens);
     });
     hipError_t e = hipGetLastError();
@@ -265,7 +273,7 @@ hipError_t launch_balance_loss_backward(const float *d_loss, const void *logits,
                                         const int32_t *num_tokens, int32_t S, int32_t K, int32_t E,
                                         int32_t score, float coef, void *d_logits,
                                         hipStream_t stream) {
-    const int need = (S + kWaves - 1) / kWaves, grid = need < 2048 ? need : 2048;
+    const int need = (S + kWaves - 1) / kWaves, grid = need < kBackwardGrid ? need : kBackwardGrid;
     dispatch(E, logits_type, score, [&](auto n, auto s, auto element) {
         using T = decltype(element);
         hipLaunchKernelGGL((balance_backward_kernel<decltype(n)::value, decltype(s)::value, T>), dim3(grid), dim3(kThreads),

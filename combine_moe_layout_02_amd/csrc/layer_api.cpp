@@ -156,7 +156,7 @@ int64_t moe_rms_norm_backward_workspace_bytes(int64_t rows, int32_t H) {
     int st = check_hidden(H);
     if (st == MOE_OK) st = check_count(rows);
     if (st != MOE_OK) return st;
-    return moe::norm_parts(rows) * H * 4;
+    return moe::norm_workspace(rows, H);
 }
 
 int moe_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *sum,
@@ -170,7 +170,7 @@ int moe_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *s
     if (st != MOE_OK) return st;
     if (!weight || !valid_float(weight_type) || !d_weight) return MOE_ERR_ARG;
     if (!(eps > 0.0f) || !std::isfinite(eps)) return MOE_ERR_ARG;
-    if (rows > 0 && (!dy || !sum || !dx || !workspace)) return MOE_ERR_ARG;
+    if (rows > 0 && (!dy || !sum || !dx)) return MOE_ERR_ARG;
     const int64_t row = 2 * (int64_t)H;
     st = check_rows(dy, dy_stride_bytes, rows, H);
     if (st == MOE_OK) st = check_rows(sum, sum_stride_bytes, rows, H);
@@ -178,8 +178,9 @@ int moe_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *s
     if (st != MOE_OK) return st;
     if (!aligned(weight, 16) || !aligned(dx, 16) || !aligned(d_weight, 16) || !aligned(workspace, 16))
         return MOE_ERR_ALIGN;
-    const int64_t need = moe::norm_parts(rows) * H * 4;
+    const int64_t need = moe::norm_workspace(rows, H);
     if (workspace_bytes < need) return MOE_ERR_WINDOW;
+    if (need > 0 && !workspace) return MOE_ERR_ARG;
     const Span in[] = {rows_span(dy, rows, dy_stride_bytes, row), rows_span(sum, rows, sum_stride_bytes, row),
                        {weight, H * float_bytes(weight_type)},
                        rows_span(d_sum, d_sum ? rows : 0, d_sum_stride_bytes, row)};

@@ -268,8 +268,23 @@ hipError_t launch_rms_norm(const void *x, int64_t x_stride_bytes, const void *re
                            int64_t sum_stride_bytes, void *out, void *codes, float *scales,
                            hipStream_t stream);
 
-// Parts that the norm's gradient splits its rows into, each with H sums of d_weight in the workspace.
-inline int64_t norm_parts(int64_t rows) { return rows < 512 ? rows : 512; }
+// Waves that take a row of the norm or of the rows to 8 bits: two vectors of 8 values a lane, four where eight waves do not suffice.
+inline int row_waves(int32_t H) {
+    const int nvec = H / 8, vpl = nvec <= 64 ? 1 : nvec <= 1024 ? 2 : 4;
+    return (nvec + 64 * vpl - 1) / (64 * vpl);
+}
+
+// Parts that the norm's gradient splits its rows into, each with H sums of d_weight in the workspace (a single one
+// writes d_weight itself): rows that so many waves take at once, 4 to 8 a compute unit.
+inline int64_t norm_parts(int64_t rows, int32_t H) {
+    const int waves = row_waves(H), parts = 256 * (waves >= 4 ? 1 : waves == 3 ? 2 : 4);
+    return rows < parts ? rows : parts;
+}
+
+inline int64_t norm_workspace(int64_t rows, int32_t H) {
+    const int64_t parts = norm_parts(rows, H);
+    return parts > 1 ? parts * H * 4 : 0;
+}
 
 hipError_t launch_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *sum,
                                     int64_t sum_stride_bytes, const void *weight,
@@ -277,11 +292,13 @@ hipError_t launch_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, con
                                     int64_t d_sum_stride_bytes, int64_t rows, int32_t H, void *dx,
                                     float *d_weight, void *workspace, hipStream_t stream);
 
-// Parts that the balance loss splits its tokens into. Each has E sums of scores and E counts in the workspace, behind
-// them every part's number of tokens; a single part needs none.
-constexpr int kBalanceTokens = 32;  // tokens of a part at least
+// Parts that the balance loss splits its tokens into, one compute unit each. Each has E sums of scores and E counts in the
+// workspace, behind them every part's number of tokens; a single part needs none, nor a second kernel.
+constexpr int kBalanceAlone = 128;  // tokens that a single part takes
+constexpr int kBalanceTokens = 64;  // tokens of several parts at least
 constexpr int kBalanceParts = 256;
 inline int balance_parts(int32_t S) {
+    if (S <= kBalanceAlone) return 1;
     const int parts = (S + kBalanceTokens - 1) / kBalanceTokens;
     return parts < kBalanceParts ? parts : kBalanceParts;
 }

@@ -3,6 +3,7 @@
 
 #include "mx_blocks.h"
 #include "pack_rows.h"
+#include "wave_ops.h"
 
 namespace moe {
 namespace {
@@ -11,38 +12,61 @@ using mx::bf16_pair;
 using mx::u32x2;
 using rows::u32x4;
 
+constexpr int kMaxThreads = 512;  // of a workgroup that takes a row
+constexpr int kRowsAlone = 4;      // rows of a workgroup whose waves take one each
+constexpr int kPartThreads = 64;
+constexpr int kVecs = 2;                       // vectors of a lane on the way back
+constexpr int kLoadPolicy = 2;                 // nt
+constexpr int kStorePolicy = 2;                // nt
+constexpr int kWideStorePolicy = 1 | 16 | 2;   // sc0 sc1 nt
+
 __device__ inline int64_t row_count(const int32_t *num_rows, int64_t max_rows) {
     if (!num_rows) return max_rows;
     const int64_t n = *num_rows;
     return n < 0 ? 0 : min(n, max_rows);
 }
 
-// grid = max_rows; workgroup r takes row r, a lane 16 values (ngroups = H / 16 <= 1024). The largest magnitude is taken
-// on bf16 bits, where infinities and NaNs are above all numbers.
-template <int QUANT>
-__global__ __launch_bounds__(1024) void row_quantize_kernel(
+// A workgroup a row, or a wave a row (waves == 1), vectors u + i * lanes of 8 values a lane. The largest magnitude is taken
+// on bf16 bits, where infinities and NaNs are above all numbers. The loads are issued before the count arrives: every
+// row below max_rows lies in the buffer.
+template <int VPL, int QUANT>
+__global__ __launch_bounds__(kMaxThreads) void row_quantize_kernel(
     const uint8_t *__restrict__ rows, int64_t stride, const int32_t *__restrict__ num_rows, int64_t max_rows,
-    int ngroups, uint8_t *__restrict__ codes, float *__restrict__ scales) {
-    __shared__ uint32_t wave_max[16];
-    const int64_t r = blockIdx.x;
-    const int u = threadIdx.x;
-    const __amdgpu_buffer_rsrc_t src = rows::rsrc(rows + r * stride, ngroups << 5);
-    const u32x4 a = rows::load16(src, u << 5), b = rows::load16(src, (u << 5) + 16);
-    if (r >= row_count(num_rows, max_rows)) return;
-    uint32_t top = max(mx::amax_bits(a), mx::amax_bits(b));
+    int nvec, int waves, uint8_t *__restrict__ codes, float *__restrict__ scales) {
+    __shared__ uint32_t wave_top[kMaxThreads / 64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool alone = waves == 1;
+    const int lanes = waves << 6, u = alone ? lane : (int)threadIdx.x;
+    const int64_t r = alone ? (int64_t)blockIdx.x * kRowsAlone + wave : blockIdx.x;
+    if (r >= max_rows) return;
+    const __amdgpu_buffer_rsrc_t src = rows::rsrc(rows + r * stride, nvec << 4);
+    u32x4 x[VPL];
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
-    if ((u & 63) == 0) wave_max[u >> 6] = top;
-    __syncthreads();
-    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) top = max(top, wave_max[w]);
+    for (int i = 0; i < VPL; ++i) x[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (u + i * lanes) << 4, 0, kLoadPolicy);
+    if (r >= row_count(num_rows, max_rows)) return;
+    uint32_t top = mx::amax_bits(x[0]);
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) top = max(top, mx::amax_bits(x[i]));
+    top = wave::most(top);
+    if (!alone) {
+        if (lane == 0) wave_top[wave] = top;
+        __syncthreads();
+        for (int w = 0; w < waves; ++w) top = max(top, wave_top[w]);
+    }
     const float scale = top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
                                        : __uint_as_float(top << 16) / rows::code_max<QUANT>();
-    u32x4 c = {0u, 0u, 0u, 0u};
-    if (top > 0 && top < 0x7F80u)
-        c = scale >= rows::kFastDivMinScale ? rows::quant16<QUANT, true>(a, b, scale, 1.0f / scale)
-                                            : rows::quant16<QUANT, false>(a, b, scale, 0.0f);
-    const __amdgpu_buffer_rsrc_t dst = rows::rsrc(codes + r * (ngroups << 4), ngroups << 4);
-    __builtin_amdgcn_raw_buffer_store_b128(c, dst, u << 4, 0, 0);
+    const bool fast = scale >= rows::kFastDivMinScale;
+    const float inv = 1.0f / scale;
+    const __amdgpu_buffer_rsrc_t dst = rows::rsrc(codes + r * (nvec << 3), nvec << 3);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        u32x2 c = {0u, 0u};
+        if (fast)
+            c = u32x2{rows::quant4<QUANT, true>(x[i][0], x[i][1], scale, inv), rows::quant4<QUANT, true>(x[i][2], x[i][3], scale, inv)};
+        else if (scale > 0.0f)
+            c = u32x2{rows::quant4<QUANT, false>(x[i][0], x[i][1], scale, inv), rows::quant4<QUANT, false>(x[i][2], x[i][3], scale, inv)};
+        __builtin_amdgcn_raw_buffer_store_b64(c, dst, (u + i * lanes) << 3, 0, kStorePolicy);
+    }
     if (u == 0) scales[r] = scale;
 }
 
@@ -59,24 +83,29 @@ __device__ inline void values4(uint32_t codes, float scale, float (&v)[4]) {
     }
 }
 
-constexpr int kPartThreads = 64;
-
-// grid = max_rows * nparts; workgroup (r, q) takes the q-th 64 groups of 8 values of row r.
+// grid = max_rows * nparts; workgroup (r, q) takes vectors [q, q + 1) * kVecs * kPartThreads of row r.
 template <int QUANT>
 __global__ __launch_bounds__(kPartThreads) void row_dequantize_kernel(
     const uint8_t *__restrict__ codes, const float *__restrict__ scales, const int32_t *__restrict__ num_rows,
     int64_t max_rows, int nvec, int nparts, uint8_t *__restrict__ rows, int64_t stride) {
     const int64_t r = blockIdx.x / nparts;
-    const int v = (int)(blockIdx.x - r * nparts) * kPartThreads + threadIdx.x;
+    const int v0 = (int)(blockIdx.x - r * nparts) * kVecs * kPartThreads + threadIdx.x;
     const __amdgpu_buffer_rsrc_t src = rows::rsrc(codes + r * (nvec << 3), nvec << 3);
-    const u32x2 c = __builtin_amdgcn_raw_buffer_load_b64(src, v << 3, 0, 0);
+    u32x2 c[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+        c[i] = __builtin_amdgcn_raw_buffer_load_b64(src, (v0 + i * kPartThreads) << 3, 0, kLoadPolicy);
     const float scale = scales[r];
     if (r >= row_count(num_rows, max_rows)) return;
-    float lo[4], hi[4];
-    values4<QUANT>(c.x, scale, lo);
-    values4<QUANT>(c.y, scale, hi);
-    const u32x4 out = {bf16_pair(lo[0], lo[1]), bf16_pair(lo[2], lo[3]), bf16_pair(hi[0], hi[1]), bf16_pair(hi[2], hi[3])};
-    __builtin_amdgcn_raw_buffer_store_b128(out, rows::rsrc(rows + r * stride, nvec << 4), v << 4, 0, 0);
+    const __amdgpu_buffer_rsrc_t dst = rows::rsrc(rows + r * stride, nvec << 4);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        float lo[4], hi[4];
+        values4<QUANT>(c[i].x, scale, lo);
+        values4<QUANT>(c[i].y, scale, hi);
+        const u32x4 out = {bf16_pair(lo[0], lo[1]), bf16_pair(lo[2], lo[3]), bf16_pair(hi[0], hi[1]), bf16_pair(hi[2], hi[3])};
+        __builtin_amdgcn_raw_buffer_store_b128(out, dst, (v0 + i * kPartThreads) << 4, 0, kWideStorePolicy);
+    }
 }
 
 }  // namespace
@@ -85,10 +114,16 @@ hipError_t launch_row_quantize(const void *rows, int64_t row_stride_bytes, const
                                int64_t max_rows, int32_t H, int32_t quant, void *codes,
                                float *scales, hipStream_t stream) {
     if (max_rows == 0) return hipSuccess;
-    auto *kernel = quant == MOE_QUANT_INT8_DYN ? row_quantize_kernel<MOE_QUANT_INT8_DYN>
-                                               : row_quantize_kernel<MOE_QUANT_FP8_E4M3_DYN>;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)max_rows), dim3((H / 16 + 63) / 64 * 64), 0, stream,
-                       static_cast<const uint8_t *>(rows), row_stride_bytes, num_rows, max_rows, H / 16,
+    const int nvec = H / 8, waves = row_waves(H);
+    const auto pick = [&](auto type) {
+        constexpr int Q = decltype(type)::value;
+        return nvec <= 64 ? row_quantize_kernel<1, Q> : nvec <= 1024 ? row_quantize_kernel<2, Q> : row_quantize_kernel<4, Q>;
+    };
+    auto *kernel = quant == MOE_QUANT_INT8_DYN ? pick(std::integral_constant<int, MOE_QUANT_INT8_DYN>{})
+                                               : pick(std::integral_constant<int, MOE_QUANT_FP8_E4M3_DYN>{});
+    const int64_t grid = waves == 1 ? (max_rows + kRowsAlone - 1) / kRowsAlone : max_rows;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * (waves == 1 ? kRowsAlone : waves)), 0, stream,
+                       static_cast<const uint8_t *>(rows), row_stride_bytes, num_rows, max_rows, nvec, waves,
                        static_cast<uint8_t *>(codes), scales);
     return hipGetLastError();
 }
@@ -97,7 +132,7 @@ hipError_t launch_row_dequantize(const void *codes, const float *scales, const i
                                  int64_t max_rows, int32_t H, int32_t quant, void *rows,
                                  int64_t row_stride_bytes, hipStream_t stream) {
     if (max_rows == 0) return hipSuccess;
-    const int nvec = H / 8, nparts = (nvec + kPartThreads - 1) / kPartThreads;
+    const int nvec = H / 8, nparts = (nvec + kVecs * kPartThreads - 1) / (kVecs * kPartThreads);
     auto *kernel = quant == MOE_QUANT_INT8_DYN ? row_dequantize_kernel<MOE_QUANT_INT8_DYN>
                                                : row_dequantize_kernel<MOE_QUANT_FP8_E4M3_DYN>;
     hipLaunchKernelGGL(kernel, dim3((uint32_t)(max_rows * nparts)), dim3(kPartThreads), 0, stream,

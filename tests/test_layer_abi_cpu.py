@@ -179,8 +179,9 @@ def test_refusals(name, kw, err):
 def test_workspaces():
     for n, H in ((1, 16), (64, 1024), (4096, 7168), (1 << 20, 16384)):
         need = moe.moe_rms_norm_backward_workspace_bytes(n, H)
-        assert need > 0 and need % 16 == 0
-        assert call("moe_rms_norm_backward", n=n, H=H, stride=2 * H, sum_stride=2 * H, ds_stride=2 * H, bytes=need - 1) == WINDOW
+        assert need >= 0 and need % 16 == 0
+        if need:
+            assert call("moe_rms_norm_backward", n=n, H=H, stride=2 * H, sum_stride=2 * H, ds_stride=2 * H, bytes=need - 1) == WINDOW
     assert moe.moe_rms_norm_backward_workspace_bytes(0, 1024) >= 0
     for S, E in ((1, 1), (500, 64), (65536, 512)):
         need = moe.moe_balance_loss_workspace_bytes(S, E)
