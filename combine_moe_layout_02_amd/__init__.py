@@ -10,6 +10,7 @@ is no other code path. Importing this package fails if the library is not built
 """
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -1185,17 +1186,41 @@ class ScaledRows(NamedTuple):
 _int8 = torch.int8
 
 
+def _line(n, dtype, dev, stream):
+    """A new output of n values for a call on `stream`."""
+    if stream is None:
+        return _empty(n, dtype=dtype, device=dev)
+    with torch.cuda.stream(_torch_stream(stream, dev)):
+        return _empty(n, dtype=dtype, device=dev)
+
+
+def _code_type(codes):
+    return _int8 if isinstance(codes, _Tensor) and codes.dtype is _int8 else _uint8
+
+
 def _row8_args(rows8, name, shape, dev):
     """Pointers of the codes [*shape] and scales [*shape[:-1]]."""
     codes, scales = rows8
-    kind = _int8 if isinstance(codes, _Tensor) and codes.dtype is _int8 else _uint8
-    return _dense(codes, f"{name}.codes", kind, shape, dev), _dense(scales, f"{name}.scales", _fp32, shape[:-1], dev)
+    return (_dense(codes, f"{name}.codes", _code_type(codes), shape, dev),
+            _dense(scales, f"{name}.scales", _fp32, shape[:-1], dev))
+
+
+def _row8_matrix(rows8, name):
+    """Device, shape and pointers of the codes [R, H] and scales [R]."""
+    codes = rows8[0]
+    dev, n, H = _matrix(codes, f"{name}.codes", _code_type(codes))
+    return (dev, n, H, *_row8_args(rows8, name, (n, H), dev))
 
 
 def _row8_empty(rows, H, dev, stream):
-    if stream is None:
-        return ScaledRows(_empty(rows, H, dtype=_uint8, device=dev), _empty(rows, dtype=_fp32, device=dev))
-    return ScaledRows(_out(rows, H, _uint8, dev, stream), _out(rows, 1, _fp32, dev, stream).view(rows))
+    return ScaledRows(_out(rows, H, _uint8, dev, stream), _line(rows, _fp32, dev, stream))
+
+
+def _some_rows(t, name, n, H, dev):
+    """Pointer and row stride in bytes of bf16 rows [n, H], of which there may be none."""
+    if not isinstance(t, _Tensor) or t.shape != (n, H):
+        raise ValueError(f"{name} must be bfloat16 {(n, H)}")
+    return _rows_arg(t, name, H, dev)[:2] if n else (None, 2 * H)
 
 
 def moe_row_quantize(rows, quant, num_rows=None, out=None, stream=None):
@@ -1209,22 +1234,20 @@ def moe_row_quantize(rows, quant, num_rows=None, out=None, stream=None):
     else:
         codes, scales = _row8_args(out, "out", (n, H), dev)
     count = _count_arg(num_rows, dev)
-    ptr, stride = _rows_arg(rows, "rows", H, dev)[:2] if n else (None, 2 * H)
+    ptr, stride = _some_rows(rows, "rows", n, H, dev)
     _launch(dev, stream, _lib.moe_row_quantize, ptr, stride, count, n, H, quant, codes, scales)
     return ScaledRows(*out)
 
 
 def moe_row_dequantize(rows8, quant, num_rows=None, out=None, stream=None):
     """The values of ScaledRows [R, H] as bf16 rows (out: any row stride)."""
-    codes_t = rows8[0]
-    dev, n, H = _matrix(codes_t, "rows8.codes", _int8 if isinstance(codes_t, _Tensor) and codes_t.dtype is _int8 else _uint8)
-    codes, scales = _row8_args(rows8, "rows8", (n, H), dev)
+    dev, n, H, codes, scales = _row8_matrix(rows8, "rows8")
     if out is None:
         out = _out(n, H, _bf16, dev, stream)
-    elif not isinstance(out, _Tensor) or out.shape != (n, H):
-        raise ValueError(f"out must be bfloat16 {(n, H)}")
+        ptr, stride = out.data_ptr(), 2 * H
+    else:
+        ptr, stride = _some_rows(out, "out", n, H, dev)
     count = _count_arg(num_rows, dev)
-    ptr, stride = _rows_arg(out, "out", H, dev)[:2] if n else (None, 2 * H)
     _launch(dev, stream, _lib.moe_row_dequantize, codes, scales, count, n, H, quant, ptr, stride)
     return out
 
@@ -1235,9 +1258,7 @@ def moe_int8_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=N
     device, e.g. layout.expert_slot_base; [0, R] with G = 1 for a shared expert) gives bf16 [O], or [O / 2] of
     silu(gate) * up with MOE_MX_GATED. Rows outside every group keep their contents (undefined where out is allocated
     here)."""
-    a_codes = a[0]
-    dev, n, H = _matrix(a_codes, "a.codes", _int8 if isinstance(a_codes, _Tensor) and a_codes.dtype is _int8 else _uint8)
-    a_ptr, as_ptr = _row8_args(a, "a", (n, H), dev)
+    dev, n, H, a_ptr, as_ptr = _row8_matrix(a, "a")
     w_codes = w[0]
     shape = w_codes.shape if isinstance(w_codes, _Tensor) else ()
     if len(shape) != 3 or shape[2] != H:
@@ -1279,42 +1300,40 @@ def moe_rms_norm(x, weight, eps=1e-6, residual=None, quant=MOE_QUANT_NONE, out=N
     with a quant (MOE_QUANT_INT8_DYN, MOE_QUANT_FP8_E4M3_DYN) rows in 8 bits instead, and both where out is passed too.
     x, residual and sum may have any row stride; sum may be x or residual itself (an addition in place)."""
     dev, n, H = _matrix(x, "x", _bf16)
-    ptr, stride = _rows_arg(x, "x", H, dev)[:2] if n else (None, 2 * H)
-    res_ptr, res_stride, sum_ptr, sum_stride = None, 0, None, 0
+    ptr, stride = _some_rows(x, "x", n, H, dev)
+    res_ptr, res_stride, sum_ptr, sum_stride, out_ptr, codes, scales = None, 0, None, 0, None, None, None
     if residual is not None:
-        if not isinstance(residual, _Tensor) or residual.shape != (n, H):
-            raise ValueError(f"residual must be bfloat16 {(n, H)}")
+        res_ptr, res_stride = _some_rows(residual, "residual", n, H, dev)
         if sum is None:
             sum = _out(n, H, _bf16, dev, stream)
-        elif not isinstance(sum, _Tensor) or sum.shape != (n, H):
-            raise ValueError(f"sum must be bfloat16 {(n, H)}")
-        if n:
-            res_ptr, res_stride, _ = _rows_arg(residual, "residual", H, dev)
-            sum_ptr, sum_stride, _ = _rows_arg(sum, "sum", H, dev)
+            sum_ptr, sum_stride = sum.data_ptr(), 2 * H
+        else:
+            sum_ptr, sum_stride = _some_rows(sum, "sum", n, H, dev)
     elif sum is not None:
         raise ValueError("sum is written only with a residual")
     else:
         sum = x
     w_ptr, kind = _weight_arg(weight, H, dev)
-    out_ptr, codes, scales = None, None, None
-    if quant != MOE_QUANT_NONE:
-        if rows8 is None:
-            rows8 = _row8_empty(n, H, dev, stream)
-            codes, scales = rows8[0].data_ptr(), rows8[1].data_ptr()
-        else:
-            codes, scales = _row8_args(rows8, "rows8", (n, H), dev)
-            rows8 = ScaledRows(*rows8)
-    elif rows8 is not None:
-        raise ValueError("rows8 is written only with a quant")
-    elif out is None:
-        out = _out(n, H, _bf16, dev, stream)
-    if out is not None:
+    if quant == MOE_QUANT_NONE:
+        if rows8 is not None:
+            raise ValueError("rows8 is written only with a quant")
+        if out is None:
+            out = _out(n, H, _bf16, dev, stream)
+            out_ptr = out.data_ptr()
+    elif rows8 is None:
+        rows8 = _row8_empty(n, H, dev, stream)
+        codes, scales = rows8[0].data_ptr(), rows8[1].data_ptr()
+    else:
+        codes, scales = _row8_args(rows8, "rows8", (n, H), dev)
+        rows8 = ScaledRows(*rows8)
+    if out is not None and out_ptr is None:
         out_ptr = _dense(out, "out", _bf16, (n, H), dev)
     _launch(dev, stream, _lib.moe_rms_norm, ptr, stride, res_ptr, res_stride, w_ptr, kind, eps, n, H, quant, sum_ptr,
             sum_stride, out_ptr, codes, scales)
     return RmsNorm(out, sum, rows8)
 
 
+@functools.lru_cache(maxsize=256)
 def moe_rms_norm_backward_workspace_bytes(rows, H):
     v = _lib.moe_rms_norm_backward_workspace_bytes(int(rows), int(H))
     if v < 0:
@@ -1323,12 +1342,14 @@ def moe_rms_norm_backward_workspace_bytes(rows, H):
 
 
 def _workspace(workspace, need, dev, stream):
-    """Pointer and bytes of a call's workspace, and the tensor, which is allocated here where none is passed."""
+    """A call's workspace with its pointer and bytes: one is allocated where none is passed and the call needs one."""
     if workspace is None:
-        workspace = _out(need, 1, _uint8, dev, stream)
-        return workspace.data_ptr(), need, workspace
+        if not need:
+            return None, None, 0
+        workspace = _line(need, _uint8, dev, stream)
+        return workspace, workspace.data_ptr(), need
     _need(workspace, "workspace", device=torch.device("cuda", dev))
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def moe_rms_norm_backward(dy, sum, weight, eps=1e-6, d_sum=None, dx=None, d_weight=None, workspace=None, stream=None):
@@ -1337,20 +1358,21 @@ def moe_rms_norm_backward(dy, sum, weight, eps=1e-6, d_sum=None, dx=None, d_weig
     other ways, added to dx. dy, sum and d_sum may have any row stride. workspace: a device buffer of at least
     moe_rms_norm_backward_workspace_bytes(S, H) bytes, or None to have one allocated."""
     dev, n, H = _matrix(sum, "sum", _bf16)
-    for t, name in ((dy, "dy"), (d_sum, "d_sum")):
-        if t is not None and (not isinstance(t, _Tensor) or t.shape != (n, H)):
-            raise ValueError(f"{name} must be bfloat16 {(n, H)}")
-    ptr, stride = _rows_arg(sum, "sum", H, dev)[:2] if n else (None, 2 * H)
-    dy_ptr, dy_stride = _rows_arg(dy, "dy", H, dev)[:2] if n else (None, 2 * H)
-    ds_ptr, ds_stride = _rows_arg(d_sum, "d_sum", H, dev)[:2] if n and d_sum is not None else (None, 0)
+    ptr, stride = _some_rows(sum, "sum", n, H, dev)
+    dy_ptr, dy_stride = _some_rows(dy, "dy", n, H, dev)
+    ds_ptr, ds_stride = (None, 0) if d_sum is None else _some_rows(d_sum, "d_sum", n, H, dev)
     w_ptr, kind = _weight_arg(weight, H, dev)
     if dx is None:
         dx = _out(n, H, _bf16, dev, stream)
-    dx_ptr = _dense(dx, "dx", _bf16, (n, H), dev)
+        dx_ptr = dx.data_ptr()
+    else:
+        dx_ptr = _dense(dx, "dx", _bf16, (n, H), dev)
     if d_weight is None:
-        d_weight = _out(1, H, _fp32, dev, stream).view(H)
-    dw_ptr = _dense(d_weight, "d_weight", _fp32, (H,), dev)
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, moe_rms_norm_backward_workspace_bytes(n, H), dev, stream)
+        d_weight = _line(H, _fp32, dev, stream)
+        dw_ptr = d_weight.data_ptr()
+    else:
+        dw_ptr = _dense(d_weight, "d_weight", _fp32, (H,), dev)
+    workspace, ws_ptr, ws_bytes = _workspace(workspace, moe_rms_norm_backward_workspace_bytes(n, H), dev, stream)
     _launch(dev, stream, _lib.moe_rms_norm_backward, dy_ptr, dy_stride, ptr, stride, w_ptr, kind, eps, ds_ptr, ds_stride,
             n, H, dx_ptr, dw_ptr, ws_ptr, ws_bytes)
     return dx, d_weight
@@ -1365,17 +1387,22 @@ class BalanceLoss(NamedTuple):
 def _router_args(logits, topk_idx):
     """Device, S, K, E, and the logits' pointer, row stride in bytes and type, and the entries' pointer."""
     dev, S, K, table = _table_arg(topk_idx)
-    kind = logits.dtype if isinstance(logits, _Tensor) else None
-    rows, E = _matrix(logits, "logits", _bf16 if kind is _bf16 else _fp32)[1:]
-    if logits.get_device() != dev or rows != S:
+    if isinstance(logits, _Tensor) and logits.dtype is _bf16:
+        size, kind = 2, MOE_BF16
+    else:
+        size, kind = 4, MOE_FP32
+    at, rows, E = _matrix(logits, "logits", _bf16 if kind == MOE_BF16 else _fp32)
+    if at != dev or rows != S:
         raise ValueError(f"logits must have {S} rows on cuda:{dev}")
+    if logits.is_contiguous():
+        return dev, S, K, E, logits.data_ptr(), size * E, kind, table
     step, col = logits.stride()
     if E > 1 and col != 1 or S > 1 and step < E:
         raise ValueError("logits must have contiguous rows that do not overlap")
-    size = 2 if kind is _bf16 else 4
-    return (dev, S, K, E, logits.data_ptr(), size * (step if S > 1 else E), MOE_BF16 if kind is _bf16 else MOE_FP32, table)
+    return dev, S, K, E, logits.data_ptr(), size * (step if S > 1 else E), kind, table
 
 
+@functools.lru_cache(maxsize=256)
 def moe_balance_loss_workspace_bytes(S, E):
     v = _lib.moe_balance_loss_workspace_bytes(int(S), int(E))
     if v < 0:
@@ -1390,14 +1417,17 @@ def moe_balance_loss(logits, topk_idx, coef, score=MOE_SCORE_SOFTMAX, out=None, 
     least moe_balance_loss_workspace_bytes(S, E) bytes, or None to have one allocated."""
     dev, S, K, E, ptr, stride, kind, table = _router_args(logits, topk_idx)
     if out is None:
-        out = BalanceLoss(_out(1, 1, _fp32, dev, stream).view(1), _out(1, E, _int32, dev, stream).view(E),
-                          _out(1, 1, _int32, dev, stream).view(1))
-    loss, counts, tokens = (_dense(t, name, kind_, shape, dev) for t, name, kind_, shape in
-                            zip(out, BalanceLoss._fields, (_fp32, _int32, _int32), ((1,), (E,), (1,))))
-    ws_ptr, ws_bytes, workspace = _workspace(workspace, moe_balance_loss_workspace_bytes(S, E), dev, stream)
+        out = BalanceLoss(_line(1, _fp32, dev, stream), _line(E, _int32, dev, stream), _line(1, _int32, dev, stream))
+        loss, counts, tokens = out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()
+    else:
+        out = BalanceLoss(*out)
+        loss = _dense(out.loss, "loss", _fp32, (1,), dev)
+        counts = _dense(out.num_tokens_per_expert, "num_tokens_per_expert", _int32, (E,), dev)
+        tokens = _dense(out.num_tokens, "num_tokens", _int32, (1,), dev)
+    workspace, ws_ptr, ws_bytes = _workspace(workspace, moe_balance_loss_workspace_bytes(S, E), dev, stream)
     _launch(dev, stream, _lib.moe_balance_loss, ptr, stride, kind, table, S, K, E, score, coef, loss, counts, tokens, ws_ptr,
             ws_bytes)
-    return BalanceLoss(*out)
+    return out
 
 
 def moe_balance_loss_backward(d_loss, logits, topk_idx, num_tokens_per_expert, num_tokens, coef, score=MOE_SCORE_SOFTMAX,
@@ -1410,7 +1440,9 @@ def moe_balance_loss_backward(d_loss, logits, topk_idx, num_tokens_per_expert, n
     tokens = _dense(num_tokens, "num_tokens", _int32, (1,), dev)
     if d_logits is None:
         d_logits = _out(S, E, logits.dtype, dev, stream)
-    out_ptr = _dense(d_logits, "d_logits", logits.dtype, (S, E), dev)
+        out_ptr = d_logits.data_ptr()
+    else:
+        out_ptr = _dense(d_logits, "d_logits", logits.dtype, (S, E), dev)
     _launch(dev, stream, _lib.moe_balance_loss_backward, dl_ptr, ptr, stride, kind, table, counts, tokens, S, K, E, score,
             coef, out_ptr)
     return d_logits
