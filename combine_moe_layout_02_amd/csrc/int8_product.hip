@@ -20,6 +20,54 @@ __device__ inline i32x4 mfma(const i32x4 &a, const i32x4 &b, const i32x4 &c) {
 // fp32(fp32(c * a) * w): a result's value from its sum and its two scales.
 __device__ inline float scaled(int c, float a, float w) { return (float)c * a * w; }
 
+// As find_tile, but a group's rows are shared evenly among its tiles, in steps of STEP, so that they take the same time, in
+// step with one another over the weights they share; and of a tile's rows the piece-th of `pieces` shares.
+template <int TM, int STEP>
+__device__ inline Tile find_even_tile(const TileTable &table, int G, int ncol, int t, int piece, int pieces) {
+    Tile tile = find_tile<TM>(table, G, ncol, t);
+    const int lo = __builtin_amdgcn_readfirstlane(table.lo[tile.group]), hi = __builtin_amdgcn_readfirstlane(table.hi[tile.group]);
+    const int n = hi - lo, tiles = (n + TM - 1) / TM;
+    const int height = ((n + tiles - 1) / tiles + STEP - 1) / STEP * STEP;  // (tiles - 1) * height <= (tiles - 1) * TM < n
+    const int first = lo + (tile.first - lo) / TM * height, rows = min(height, hi - first);
+    const int part = ((rows + pieces - 1) / pieces + STEP - 1) / STEP * STEP;
+    tile.first = first + piece * part;
+    tile.rows = max(min(part, rows - piece * part), 0);  // less, or none, where the shares before have taken all
+    return tile;
+}
+
+// Which tiles a workgroup takes: of its XCD's, begin .. end, every step-th from its own on; of a last round that would leave
+// workgroups without one, each tile in as many pieces as there are workgroups for it.
+struct Turns {
+    int end, step, whole, mine;  // rounds that are whole, and the workgroup's number in its XCD
+    int t, piece, pieces;
+
+    __device__ Turns(int all, int most) {
+        const int share = (all + 7) >> 3, begin = min((int)(blockIdx.x & 7) * share, all);
+        end = min(begin + share, all);
+        step = gridDim.x >> 3;
+        mine = blockIdx.x >> 3;
+        whole = begin + (end - begin) / step * step;
+        t = begin + mine - step;
+        piece = 0;
+        pieces = 1;
+        left = end - whole;
+        split = left > 0 ? min(step / left, most) : 1;
+    }
+    // The next turn; false when there is none.
+    __device__ bool next() {
+        if (t + step < whole) {
+            t += step;
+            return true;
+        }
+        if (t >= whole || mine >= left * split) return false;
+        t = whole + mine % left;
+        piece = mine / left;
+        pieces = split;
+        return true;
+    }
+    int left, split;
+};
+
 // Tiles of TM rows x TN weight rows (TN / 2 outputs when GATED), WMC x WNC waves, through LDS. The 8 XCDs get
 // contiguous eighths of the tiles (workgroup b runs on XCD b % 8).
 //
@@ -56,10 +104,8 @@ __global__ __launch_bounds__(64 * WMC * WNC) void int8_tile_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     if (wave == 0) fill_table<TM>(table, base, G, a_rows);
     __syncthreads();
-    const int all = __builtin_amdgcn_readfirstlane(table.end[G - 1]) * ncol, share = (all + 7) >> 3;
-    const int xcd_end = min(((int)(blockIdx.x & 7) + 1) * share, all), step = gridDim.x >> 3;
-    int t = (int)(blockIdx.x & 7) * share + (int)(blockIdx.x >> 3);
-    if (t >= xcd_end) return;
+    Turns turn(__builtin_amdgcn_readfirstlane(table.end[G - 1]) * ncol, PAIRS == 2 ? TM / (16 * WMC) : 1);
+    if (!turn.next()) return;
 
     // Load l of a wave takes tile rows 8 (wave + l * NW) .. + 7, a lane 16 bytes: place lane % 8 of row lane / 8.
     // Place p of row r holds block p ^ (r % 8): eight neighbouring rows' reads of one block then cover all the
@@ -98,68 +144,83 @@ __global__ __launch_bounds__(64 * WMC * WNC) void int8_tile_kernel(
                         past ? 0x7FFFFFF0 : src.base[l] + place, pair * 128);
     };
 
-    const int wm = (wave % WMC) * WM, wn = TM + (wave / WMC) * WN;
+    const int wn = TM + (wave / WMC) * WN;
     const int fr = lane & 15, q = lane >> 4;
     const int at0 = fr * 128 + (q ^ (fr & 7)) * 16, at1 = fr * 128 + ((q + 4) ^ (fr & 7)) * 16;
     const int stages = (H + 63) / 64, pairs = (stages + 1) / 2;
 
     i32x4 acc[MI][NI];
     i32x4 a[MI], w[NI];
-    const auto read_codes = [&](const uint8_t *buf, int at) {
+    // The waves share a tile's rows evenly, mi fragments each: a constant number of them, or (most 0) whatever mi is, whose
+    // tests take 7% longer.
+    int mi, wm;
+    const auto taken = [&](auto most, int i) { return most.value > 0 ? i < most.value : i < mi; };
+    const auto read_codes = [&](auto most, const uint8_t *buf, int at) {
 #pragma unroll
         for (int j = 0; j < NI; ++j) w[j] = *reinterpret_cast<const i32x4 *>(&buf[(wn + j * 16) * 128 + at]);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) a[i] = *reinterpret_cast<const i32x4 *>(&buf[(wm + i * 16) * 128 + at]);
+        for (int i = 0; i < MI; ++i)
+            if (taken(most, i)) a[i] = *reinterpret_cast<const i32x4 *>(&buf[(wm + i * 16) * 128 + at]);
     };
-    const auto multiply = [&]() {
+    const auto multiply = [&](auto most) {
 #pragma unroll
         for (int i = 0; i < MI; ++i)
+            if (taken(most, i)) {
 #pragma unroll
-            for (int j = 0; j < NI; ++j) acc[i][j] = mfma(w[j], a[i], acc[i][j]);
+                for (int j = 0; j < NI; ++j) acc[i][j] = mfma(w[j], a[i], acc[i][j]);
+            }
     };
 
-    Tile tile = find_tile<TM>(table, G, ncol, t);
+    const auto tile_of = [&]() { return find_even_tile<TM, 16 * WMC>(table, G, ncol, turn.t, turn.piece, turn.pieces); };
+    Tile tile = tile_of();
     Source cur = source_of(tile);
 #pragma unroll
     for (int i = 0; i < PAIRS - 1; ++i) load_codes(cur, i, codes[i], false);
     bool stored = false;  // the stores of the tile before are still in flight, STORES of them
     for (;;) {
-        t += step;
-        const bool more = PAIRS == 2 && t < xcd_end;
+        const bool more = PAIRS == 2 && turn.next();
         Tile next = tile;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NI; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+        mi = (tile.rows + 16 * WMC - 1) / (16 * WMC);
+        wm = (wave % WMC) * mi * 16;
         // a round is a pair in each buffer, so that a buffer's number is a constant
-        for (int p0 = 0; p0 < pairs; p0 += PAIRS) {
-            const bool last = p0 + PAIRS >= pairs;
+        const auto all_rounds = [&](auto most) {
+            for (int p0 = 0; p0 < pairs; p0 += PAIRS) {
+                const bool last = p0 + PAIRS >= pairs;
 #pragma unroll
-            for (int b = 0; b < PAIRS; ++b) {
-                const int p = p0 + b;
-                if (PAIRS == 2 && b == 0 && p0 == 0 && stored) stage_barrier<STORES>();
-                else stage_barrier<(PAIRS - 2) * LOADS>();
-                read_codes(codes[b], at0);
-                if (PAIRS > 2) {
-                    load_codes(cur, p + PAIRS - 1, codes[(b + PAIRS - 1) % PAIRS], false);
-                } else if (b == 0) {
-                    load_codes(cur, p + 1, codes[1], false);
-                    if (last && more) {
-                        next = find_tile<TM>(table, G, ncol, t);
-                        cur = source_of(next);
+                for (int b = 0; b < PAIRS; ++b) {
+                    const int p = p0 + b;
+                    if (PAIRS == 2 && b == 0 && p0 == 0 && stored) stage_barrier<STORES>();
+                    else stage_barrier<(PAIRS - 2) * LOADS>();
+                    read_codes(most, codes[b], at0);
+                    if (PAIRS > 2) {
+                        load_codes(cur, p + PAIRS - 1, codes[(b + PAIRS - 1) % PAIRS], false);
+                    } else if (b == 0) {
+                        load_codes(cur, p + 1, codes[1], false);
+                        if (last && more) {
+                            next = tile_of();
+                            cur = source_of(next);
+                        }
+                    } else {
+                        // behind the tile's last pair comes the next tile's first one
+                        load_codes(cur, last ? 0 : p + 1, codes[0], last && !more);
                     }
-                } else {
-                    // behind the tile's last pair comes the next tile's first one
-                    load_codes(cur, last ? 0 : p + 1, codes[0], last && !more);
+                    __builtin_amdgcn_sched_barrier(0);  // the reads and loads are under way before the products
+                    if (p < pairs) multiply(most);
+                    __builtin_amdgcn_sched_barrier(0);
+                    read_codes(most, codes[b], at1);
+                    if (2 * p + 1 < stages) multiply(most);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_sched_barrier(0);  // the reads and loads are under way before the products
-                if (p < pairs) multiply();
-                __builtin_amdgcn_sched_barrier(0);
-                read_codes(codes[b], at1);
-                if (2 * p + 1 < stages) multiply();
-                __builtin_amdgcn_sched_barrier(0);
             }
-        }
+        };
+        if (mi == MI) all_rounds(std::integral_constant<int, MI>{});
+        else if (MI > 1 && mi == MI - 1) all_rounds(std::integral_constant<int, MI - 1>{});
+        else if (MI > 2 && mi == MI - 2) all_rounds(std::integral_constant<int, MI - 2>{});
+        else if (MI > 3) all_rounds(std::integral_constant<int, 0>{});
 
         // A lane holds four neighbouring results of a row; swapping 16-lane rows between two column fragments
         // gives it eight, 16 bytes. With aligned rows every store goes out, past the tile's end to nowhere, so
@@ -202,9 +263,9 @@ __global__ __launch_bounds__(64 * WMC * WNC) void int8_tile_kernel(
                 const u32x4 r8 = {lo[0], hi[0], lo[1], hi[1]};
                 const int o = o0 + (j + (q & 1)) * 16 + (q >> 1) * 8;
                 if (wide) {
-                    const bool in = r < tile.rows && o < width;
+                    const bool in = i < mi && r < tile.rows && o < width;
                     __builtin_amdgcn_raw_buffer_store_b128(r8, dst, in ? r * (int)out_stride + o * 2 : 0x7FFFFFF0, 0, 0);
-                } else if (r < tile.rows) {
+                } else if (i < mi && r < tile.rows) {
                     uint16_t *to = reinterpret_cast<uint16_t *>(out + ((int64_t)tile.first + r) * out_stride) + o;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
