@@ -433,19 +433,43 @@ hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64
     const Args p = {static_cast<const uint8_t *>(a_codes), a_scales, a_rows, group_base, G,
                     static_cast<const uint8_t *>(w_codes), w_scales, O, H, gated, static_cast<uint8_t *>(out),
                     out_stride_bytes, wide, stream};
+    // Which kernel, by the tiles it would have if the rows were spread over as many groups as they can reach, a quarter of
+    // them more in the fuller ones. One run over the kernels, weights from memory, uneven groups (us; groups x rows a group):
+    //   7168 -> 4096 gated   1x8    1x64   1x256  1x512  1x2000*  4x16   4x32   4x128  8x32   8x64   8x128  32x2   32x16  32x64  32x256
+    //   few_rows             13.2   27.3                          48.2
+    //   32 x 64, four pairs  18.2   18.6   26.1                   23.7   32.2          63.2                 144    162
+    //   64 x 64, four        18.9   21.3   20.9   33.0   68.5     23.8   25.0   51.5   47.0   61.9   90.1   138    160    222    517
+    //   64 x 128, four       24.4   30.2   29.3   29.7   52.7     29.9   32.7   58.1   44.3   64.2   87.1   146    162    200    480
+    //   128 x 128, four      27.8   32.0   39.2   39.8   40.6     32.3   34.4   42.9   44.9   49.8   79.9                 184    393
+    //   64 x 128, two                      48.1   48.5   55.6                   57.3   57.9   64.1   103    142    159    195    461
+    //   128 x 128, two                            54.1   55.0                   58.3          62.9   73.9   150    163    182    349
+    //   256 x 256, two                                                                               97.7                 203    313
+    // (* 2048 outputs), and others, in the same order from 64 x 128 with four:
+    //   rows a group         1x12288  1x3000  4x512  8x200   8x256  16x188  20x300  40x63  50x240  64x313  1x32768
+    //   H -> outputs         1024 1024 2048 4096 1024 4096 4096 4096g 2048 7168 1040 1000 3008 512g 2048 2048g 800 640 512 512 256 128
+    //   64 x 128, four       43.9     59.4             68.8            20.5    35.8    48.4
+    //   128 x 128, four      35.3     45.7    30.5     60.7    70.8    15.9    25.9    47.0   33.1    24.9    9.2
+    //   64 x 128, two        32.5     52.1    28.2     65.4    70.3    16.1    30.7    42.5   30.6    21.0    7.6
+    //   128 x 128, two       30.2     42.4    25.7     58.3    62.1    16.3    32.9    48.3   27.6    19.6    8.1
+    //   256 x 256, two       24.1     35.2    23.1     61.1    59.9                           24.8    18.4    11.3
+    // Where the tiles are no more than the compute units, all of a tile's time is its way through one, and small
+    // tiles with more pairs under way shorten it; few_rows, whose waves share H, is ahead while its workgroups read
+    // no more than 15360 rows. With more tiles the two pairs' kernels, which start a tile while they end another,
+    // are ahead, the larger the more rows there are to share the weights: 128 x 128 from 64 rows a group and 300 tiles,
+    // 256 x 256 from 160 rows and 192 tiles (its last round goes out in pieces).
     const int64_t hit = a_rows < G ? a_rows : G, mean = (a_rows + hit - 1) / hit;
     const int64_t most = hit > 1 ? mean + mean / 4 : mean;
     const auto tiles_of = [&](int tm, int tn) {
         const int outs = gated ? tn / 2 : tn;
         return hit * ((most + tm - 1) / tm) * ((width + outs - 1) / outs);
     };
-    if (tiles_of(16, 32) * ((most < 16 ? most : 16) + 32) <= 320 * 48) return few_rows(p);
-    if (tiles_of(32, 64) <= (most <= 32 ? 448 : kUnits)) return tiles<32, 64, 2, 1, 4>(p);
+    if (tiles_of(16, 32) * ((most < 16 ? most : 16) + 32) <= 320 * 48) return few_rows(p);  // rows that its workgroups read
+    if (tiles_of(32, 64) <= (most <= 32 ? 448 : kUnits)) return tiles<32, 64, 2, 1, 4>(p);  // two at once on a unit, and room for a fuller group
     if (tiles_of(64, 64) <= kUnits) return tiles<64, 64, 4, 1, 4>(p);
     if (tiles_of(64, 128) <= kUnits) return tiles<64, 128, 2, 2, 4>(p);
-    const int64_t large = tiles_of(256, 256);
-    if (mean >= 160 && (large >= 4 * kUnits || (H >= 4096 && large >= 192 && large <= kUnits))) return tiles<256, 256, 2, 4, 2>(p);
-    if (mean >= 40 && tiles_of(128, 128) >= 300) return tiles<128, 128, 2, 2, 2>(p);
+    if (mean >= 160 && tiles_of(256, 256) >= 192) return tiles<256, 256, 2, 4, 2>(p);
+    if (H >= 1024 && tiles_of(128, 128) <= kUnits) return tiles<128, 128, 2, 2, 4>(p);  // short rows do not fill four pairs
+    if (mean >= 64 && tiles_of(128, 128) >= 300) return tiles<128, 128, 2, 2, 2>(p);
     return tiles<64, 128, 2, 2, 2>(p);
 }
 
