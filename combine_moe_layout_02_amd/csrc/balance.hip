@@ -13,7 +13,7 @@ typedef __bf16 bf16_t;
 constexpr int kPartThreads = 1024, kPartWaves = kPartThreads / 64;
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kFinishThreads = 1024;
-constexpr int kBackwardGrid = 1024;
+constexpr int kBackwardGrid = 2048;
 
 // exp(x) for x <= 0 to 2 ulp, from the hardware's exp2 of x * log2(e) and the rest of that product; 0 from -200 down, NaN of a
 // NaN. A third of the library function's instructions, which bound these kernels.
@@ -67,10 +67,8 @@ struct Token {
     }
 };
 
-// loss from the counts and the sums of scores; n entries and tokens in all. Every lane of a wave calls this with its
-// share of sum over e of count * score sum.
+// The loss from sum over e of count * score sum, of n entries and tokens in all.
 __device__ inline float loss_of(double share, int64_t n, int tokens, int E, float coef) {
-    share = wave::sum(share);
     return tokens ? (float)(share * ((double)coef * E / ((double)n * tokens))) : 0.0f;
 }
 
@@ -80,7 +78,7 @@ template <int N, int SCORE, class T>
 __global__ __launch_bounds__(kPartThreads) void balance_parts_kernel(
     const uint8_t *__restrict__ logits, int64_t stride, const int32_t *__restrict__ topk, int S, int K, int E,
     int per, float coef, float *__restrict__ loss, int32_t *__restrict__ counts, int32_t *__restrict__ tokens,
-    float *__restrict__ part_sums, int32_t *__restrict__ part_counts, int32_t *__restrict__ part_tokens) {
+    float *__restrict__ part_sums, uint16_t *__restrict__ part_counts, int32_t *__restrict__ part_tokens) {
     __shared__ int32_t count[64 * N];
     __shared__ float sums[kPartWaves][64 * N];
     __shared__ int32_t live[kPartWaves];
@@ -120,9 +118,10 @@ __global__ __launch_bounds__(kPartThreads) void balance_parts_kernel(
         return s;
     };
     if (gridDim.x > 1) {
-        for (int e = tid; e < E; e += kPartThreads) {
-            part_sums[(int64_t)blockIdx.x * E + e] = sum_of(e);
-            part_counts[(int64_t)blockIdx.x * E + e] = count[e];
+        const int wide = (E + 3) / 4 * 4;  // experts up to there have no scores and no entries
+        for (int e = tid; e < wide; e += kPartThreads) {
+            part_sums[blockIdx.x * wide + e] = sum_of(e);
+            part_counts[blockIdx.x * wide + e] = (uint16_t)count[e];  // 256 tokens of 16 entries at most
         }
         if (tid == 0) part_tokens[blockIdx.x] = all;
         return;
@@ -135,48 +134,63 @@ __global__ __launch_bounds__(kPartThreads) void balance_parts_kernel(
         n += count[e];
         counts[e] = count[e];
     }
-    const float value = loss_of(share, wave::sum(n), all, E, coef);
+    const float value = loss_of(wave::sum(share), wave::sum(n), all, E, coef);
     if (lane == 0) *loss = value, *tokens = all;
 }
 
-// One workgroup: expert e = tid % width, slice tid / width of the parts (width = E rounded up to a power of two), then the
-// slices in order.
+// One workgroup: four experts a thread, `groups` threads (E / 4 rounded up to a power of two) to a part's row, as many parts
+// at once as there are threads for them; then the threads' sums in order.
 __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
-    const float *__restrict__ part_sums, const int32_t *__restrict__ part_counts,
-    const int32_t *__restrict__ part_tokens, int parts, int E, int width, float coef, float *__restrict__ loss,
+    const float *__restrict__ part_sums, const uint16_t *__restrict__ part_counts,
+    const int32_t *__restrict__ part_tokens, int parts, int E, int groups, float coef, float *__restrict__ loss,
     int32_t *__restrict__ counts, int32_t *__restrict__ tokens) {
-    __shared__ float sums[kFinishThreads];
-    __shared__ int32_t count[kFinishThreads];
-    const int tid = threadIdx.x, e = tid & (width - 1), slice = tid / width, slices = kFinishThreads / width;
-    float s = 0.0f;
-    int c = 0;
-    if (e < E)
-#pragma unroll 8
+    __shared__ float sums[4 * kFinishThreads];
+    __shared__ int32_t count[4 * kFinishThreads];
+    __shared__ double share[kFinishThreads / 64];
+    __shared__ int32_t entries[kFinishThreads / 64], lives[kFinishThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wide = (E + 3) / 4 * 4, e = (tid & (groups - 1)) * 4, slice = tid / groups, slices = kFinishThreads / groups;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int c[4] = {0, 0, 0, 0}, live = 0;
+    if (e < wide) {
+#pragma unroll 16
         for (int p = slice; p < parts; p += slices) {
-            s += part_sums[(int64_t)p * E + e];
-            c += part_counts[(int64_t)p * E + e];
+            const float4 f = *reinterpret_cast<const float4 *>(part_sums + p * wide + e);
+            const ushort4 n = *reinterpret_cast<const ushort4 *>(part_counts + p * wide + e);
+            s[0] += f.x, s[1] += f.y, s[2] += f.z, s[3] += f.w;
+            c[0] += n.x, c[1] += n.y, c[2] += n.z, c[3] += n.w;
         }
-    sums[tid] = s;
-    count[tid] = c;
-    __syncthreads();
-    if (tid >= 64) return;
-    double share = 0.0;
-    int n = 0, lives = 0;
-    for (int at = tid; at < E; at += 64) {
-        float sum = 0.0f;
-        int all = 0;
-        for (int k = 0; k < slices; ++k) {
-            sum += sums[k * width + at];
-            all += count[k * width + at];
-        }
-        share += (double)all * (double)sum;
-        n += all;
-        counts[at] = all;
     }
-    for (int p = tid; p < parts; p += 64) lives += part_tokens[p];
-    lives = wave::sum(lives);
-    const float value = loss_of(share, wave::sum(n), lives, E, coef);
-    if (tid == 0) *loss = value, *tokens = lives;
+    if (tid < parts) live = part_tokens[tid];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        sums[slice * 4 * groups + e + i] = s[i];
+        count[slice * 4 * groups + e + i] = c[i];
+    }
+    __syncthreads();
+    double part = 0.0;
+    int all = 0;
+    if (tid < E) {
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < slices; ++k) {
+            sum += sums[k * 4 * groups + tid];
+            all += count[k * 4 * groups + tid];
+        }
+        part = (double)all * (double)sum;
+        counts[tid] = all;
+    }
+    part = wave::sum(part);
+    all = wave::sum(all);
+    live = wave::sum(live);
+    if (lane == 0) share[wave] = part, entries[wave] = all, lives[wave] = live;
+    __syncthreads();
+    if (tid > 0) return;
+    int n = 0, live_all = 0;
+    part = 0.0;
+    for (int w = 0; w < kFinishThreads / 64; ++w) part += share[w], n += entries[w], live_all += lives[w];
+    *loss = loss_of(part, n, live_all, E, coef);
+    *tokens = live_all;
 }
 
 // A wave a token, as above. n[e] counts from the mean, which takes nothing from the gradient (the scores' sum is 1), and
@@ -249,9 +263,10 @@ hipError_t launch_balance_loss(const void *logits, int64_t logits_stride_bytes, 
                                int32_t *num_tokens_per_expert, int32_t *num_tokens, void *workspace,
                                hipStream_t stream) {
     const int most = balance_parts(S), per = (S + most - 1) / most, parts = (S + per - 1) / per;
+    const int64_t each = (int64_t)most * ((E + 3) / 4 * 4);
     float *sums = static_cast<float *>(workspace);
-    int32_t *counts = parts > 1 ? reinterpret_cast<int32_t *>(sums + (int64_t)parts * E) : nullptr;
-    int32_t *tokens = parts > 1 ? counts + (int64_t)parts * E : nullptr;
+    uint16_t *counts = parts > 1 ? reinterpret_cast<uint16_t *>(sums + each) : nullptr;
+    int32_t *tokens = parts > 1 ? reinterpret_cast<int32_t *>(counts + each) : nullptr;
     dispatch(E, logits_type, score, [&](auto n, auto s, auto element) {
         hipLaunchKernelGGL((balance_parts_kernel<decltype(n)::value, decltype(s)::value, decltype(element)>), dim3(parts),
                            dim3(kPartThreads), 0, stream, static_cast<const uint8_t *>(logits), logits_stride_bytes, topk_idx,
@@ -259,10 +274,10 @@ hipError_t launch_balance_loss(const void *logits, int64_t logits_stride_bytes, 
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || parts == 1) return e;
-    int width = 1;
-    while (width < E) width *= 2;
+    int groups = 1;
+    while (4 * groups < E) groups *= 2;
     hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(kFinishThreads), 0, stream, sums, counts, tokens, parts, E,
-                       width, coef, loss, num_tokens_per_expert, num_tokens);
+                       groups, coef, loss, num_tokens_per_expert, num_tokens);
     return hipGetLastError();
 }
 

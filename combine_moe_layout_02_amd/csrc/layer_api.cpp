@@ -49,11 +49,6 @@ int check_router(const void *logits, int64_t stride, int32_t type, const int32_t
     return MOE_OK;
 }
 
-int64_t balance_workspace(int32_t S, int32_t E) {
-    const int64_t parts = moe::balance_parts(S);
-    return parts > 1 ? parts * (2 * (int64_t)E + 1) * 4 : 0;
-}
-
 }  // namespace
 
 extern "C" {
@@ -195,7 +190,7 @@ int64_t moe_balance_loss_workspace_bytes(int32_t S, int32_t E) {
     const int st = check_tokens(S, 1);
     if (st != MOE_OK) return st;
     if (E < 1 || E > MOE_MAX_EXPERTS) return MOE_ERR_ARG;
-    return balance_workspace(S, E);
+    return moe::balance_workspace(S, E);
 }
 
 int moe_balance_loss(const void *logits, int64_t logits_stride_bytes, int32_t logits_type,
@@ -208,7 +203,7 @@ int moe_balance_loss(const void *logits, int64_t logits_stride_bytes, int32_t lo
     if (!aligned(loss, 4) || !aligned(num_tokens_per_expert, 4) || !aligned(num_tokens, 4) ||
         !aligned(workspace, 16))
         return MOE_ERR_ALIGN;
-    const int64_t need = balance_workspace(S, E);
+    const int64_t need = moe::balance_workspace(S, E);
     if (workspace_bytes < need) return MOE_ERR_WINDOW;
     if (need > 0 && !workspace) return MOE_ERR_ARG;
     const Span in[] = {rows_span(logits, S, logits_stride_bytes, E * float_bytes(logits_type)),

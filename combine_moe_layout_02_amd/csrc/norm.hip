@@ -227,7 +227,7 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_backward_kernel(
             for (int e = 0; e < 8; ++e) {
                 const double hv = value(h[i], e);
                 square = fma(hv, hv, square);
-                dot = fma(hv, (double)value(g[i], e) * (double)wt[i].value(e), dot);
+                dot = fma(hv, (double)(value(g[i], e) * wt[i].value(e)), dot);
             }
         square = wave::sum(square);
         dot = wave::sum(dot);
