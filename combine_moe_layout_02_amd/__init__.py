@@ -976,8 +976,8 @@ def _mx_width(H, format):
 
 def _mx_args(mx, name, rows, H, format, dev):
     codes, scales = mx
-    return (_dense(codes, f"{name}.codes", _uint8, (rows, _mx_width(H, format)), dev),
-            _dense(scales, f"{name}.scales", _uint8, (rows, H // 32), dev))
+    return (_dense(codes, name + ".codes", _uint8, (rows, _mx_width(H, format)), dev),
+            _dense(scales, name + ".scales", _uint8, (rows, H // 32), dev))
 
 
 def _gradient_outs(S, K, H, rows, topk_weights, d_expert_out, d_topk_weights, dev, stream):
@@ -1071,6 +1071,9 @@ def _mx_empty(rows, H, format, dev, stream):
 def _count_arg(num_rows, dev):
     if num_rows is None:
         return None
+    if (isinstance(num_rows, _Tensor) and num_rows.dtype is _int32 and num_rows.get_device() == dev
+            and num_rows.numel() > 0 and num_rows.is_contiguous()):
+        return num_rows.data_ptr()
     _need(num_rows, "num_rows", torch.int32, device=torch.device("cuda", dev))
     if num_rows.numel() < 1:
         raise ValueError("num_rows must hold a count")
@@ -1201,15 +1204,18 @@ def _code_type(codes):
 def _row8_args(rows8, name, shape, dev):
     """Pointers of the codes [*shape] and scales [*shape[:-1]]."""
     codes, scales = rows8
-    return (_dense(codes, f"{name}.codes", _code_type(codes), shape, dev),
-            _dense(scales, f"{name}.scales", _fp32, shape[:-1], dev))
+    return (_dense(codes, name + ".codes", _code_type(codes), shape, dev),
+            _dense(scales, name + ".scales", _fp32, shape[:-1], dev))
 
 
 def _row8_matrix(rows8, name):
     """Device, shape and pointers of the codes [R, H] and scales [R]."""
-    codes = rows8[0]
-    dev, n, H = _matrix(codes, f"{name}.codes", _code_type(codes))
-    return (dev, n, H, *_row8_args(rows8, name, (n, H), dev))
+    codes, scales = rows8
+    kind = _code_type(codes)
+    dev, n, H = _matrix(codes, name + ".codes", kind)
+    if not codes.is_contiguous():
+        _dense(codes, name + ".codes", kind, (n, H), dev)
+    return dev, n, H, codes.data_ptr(), _dense(scales, name + ".scales", _fp32, (n,), dev)
 
 
 def _row8_empty(rows, H, dev, stream):
@@ -1220,7 +1226,11 @@ def _some_rows(t, name, n, H, dev):
     """Pointer and row stride in bytes of bf16 rows [n, H], of which there may be none."""
     if not isinstance(t, _Tensor) or t.shape != (n, H):
         raise ValueError(f"{name} must be bfloat16 {(n, H)}")
-    return _rows_arg(t, name, H, dev)[:2] if n else (None, 2 * H)
+    if t.dtype is _bf16 and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr(), 2 * H
+    if n == 0:
+        raise ValueError(f"{name} must be bfloat16 on cuda:{dev}, got {t.dtype} on {t.device}")
+    return _rows_arg(t, name, H, dev)[:2]
 
 
 def moe_row_quantize(rows, quant, num_rows=None, out=None, stream=None):
