@@ -1,0 +1,179 @@
+// Host-only run of the C ABI layer of the 8-bit layer around the dispatch (combine_moe_layout_02_amd/csrc/layer_api.cpp)
+// built with the address and undefined-behaviour sanitizers against launchers that only count calls: the extents at the
+// largest accepted sizes and at hostile int64 arguments, the overlap checks at their edges, the workspaces' sizes, and that
+// a rejected call launches nothing. Pointers are fake device addresses that nothing dereferences. Prints "layer_asan ok"
+// and returns 0 when every check holds.
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+#include <limits>
+
+#include "moe_internal.h"
+
+static int launches = 0;
+static hipError_t result = hipSuccess;
+
+namespace moe {
+
+hipError_t launch_row_quantize(const void *, int64_t, const int32_t *, int64_t, int32_t, int32_t, void *, float *, hipStream_t) {
+    ++launches;
+    return result;
+}
+hipError_t launch_row_dequantize(const void *, const float *, const int32_t *, int64_t, int32_t, int32_t, void *, int64_t, hipStream_t) {
+    ++launches;
+    return result;
+}
+hipError_t launch_int8_product(const void *, const float *, int64_t, const int32_t *, int32_t, const void *, const float *, int32_t, int32_t,
+                               int32_t, void *, int64_t, hipStream_t) {
+    ++launches;
+    return result;
+}
+hipError_t launch_rms_norm(const void *, int64_t, const void *, int64_t, const void *, int32_t, float, int64_t, int32_t, int32_t, void *, int64_t,
+                           void *, void *, float *, hipStream_t) {
+    ++launches;
+    return result;
+}
+hipError_t launch_rms_norm_backward(const void *, int64_t, const void *, int64_t, const void *, int32_t, float, const void *, int64_t, int64_t,
+                                    int32_t, void *, float *, void *, hipStream_t) {
+    ++launches;
+    return result;
+}
+hipError_t launch_balance_loss(const void *, int64_t, int32_t, const int32_t *, int32_t, int32_t, int32_t, int32_t, float, float *, int32_t *,
+                               int32_t *, void *, hipStream_t) {
+    ++launches;
+    return result;
+}
+hipError_t launch_balance_loss_backward(const float *, const void *, int64_t, int32_t, const int32_t *, const int32_t *, const int32_t *, int32_t,
+                                        int32_t, int32_t, int32_t, float, void *, hipStream_t) {
+    ++launches;
+    return result;
+}
+
+}  // namespace moe
+
+static int failures = 0;
+
+static void expect(int64_t got, int64_t want, int launched, const char *what) {
+    if (got != want || launches != launched) {
+        std::printf("FAIL: %s: %lld (want %lld), %d launches (want %d)\n", what, (long long)got, (long long)want, launches, launched);
+        ++failures;
+    }
+    launches = 0;
+}
+
+// Buffer number i, 2^50 bytes from the next, plus an offset.
+static char *at(int i, int64_t offset = 0) { return reinterpret_cast<char *>(((uintptr_t)(i + 1) << 50) + (uintptr_t)offset); }
+static int32_t *ints(int i, int64_t offset = 0) { return reinterpret_cast<int32_t *>(at(i, offset)); }
+static float *floats(int i, int64_t offset = 0) { return reinterpret_cast<float *>(at(i, offset)); }
+
+int main() {
+    const int64_t big = INT64_MAX, even = big / 16 * 16, R = MOE_MAX_OUT_ROWS;
+    const int H = MOE_MAX_HIDDEN, I8 = MOE_QUANT_INT8_DYN;
+    const int64_t pitch = 2 * (int64_t)H;
+
+    const auto quantize = [&](int64_t stride, int64_t n, char *codes, float *scales, const int32_t *num) {
+        return moe_row_quantize(at(0), stride, num, n, H, I8, codes, scales, nullptr);
+    };
+    expect(quantize(pitch, R, at(1), floats(2), nullptr), MOE_OK, 1, "rows to 8 bits at the largest sizes");
+    expect(quantize(pitch, R + 1, at(1), floats(2), nullptr), MOE_ERR_ARG, 0, "too many rows");
+    expect(quantize(even, 1, at(1), floats(2), nullptr), MOE_OK, 1, "one row at the largest stride");
+    expect(quantize(even, 2, at(1), floats(2), nullptr), MOE_ERR_ARG, 0, "rows whose extent wraps");
+    expect(quantize(INT64_MIN, 4, at(1), floats(2), nullptr), MOE_ERR_ARG, 0, "negative stride");
+    expect(quantize(pitch, INT64_MIN, at(1), floats(2), nullptr), MOE_ERR_ARG, 0, "negative rows");
+    expect(quantize(pitch, R, at(1), floats(1, R * H), nullptr), MOE_OK, 1, "scales behind the codes");
+    expect(quantize(pitch, R, at(1), floats(1, R * H - 4), nullptr), MOE_ERR_ARG, 0, "scales over the codes");
+    expect(quantize(pitch, R, at(0, (R - 1) * pitch + pitch), floats(2), nullptr), MOE_OK, 1, "codes behind the rows");
+    expect(quantize(pitch, R, at(0, R * pitch - 16), floats(2), nullptr), MOE_ERR_ARG, 0, "codes over the rows");
+    expect(quantize(pitch, 4, at(1), floats(2), ints(2, 16)), MOE_OK, 1, "a count behind the scales");
+    expect(quantize(pitch, 4, at(1), floats(2), ints(2, 12)), MOE_ERR_ARG, 0, "a count that the scales overwrite");
+    expect(moe_row_quantize(nullptr, pitch, nullptr, 0, H, I8, nullptr, nullptr, nullptr), MOE_OK, 1, "no rows, no buffers");
+    expect(moe_row_dequantize(nullptr, nullptr, nullptr, 0, H, I8, nullptr, pitch, nullptr), MOE_OK, 1, "no rows back");
+    expect(moe_row_dequantize(at(0), floats(1), nullptr, R, H, I8, at(2), pitch, nullptr), MOE_OK, 1, "the way back at the largest sizes");
+    expect(moe_row_dequantize(at(0), floats(1), nullptr, R, H, I8, at(0, R * H - 16), pitch, nullptr), MOE_ERR_ARG, 0, "rows over the codes");
+
+    const auto product = [&](int64_t rows, int32_t G, int32_t O, char *out, int64_t stride, int32_t epilogue) {
+        return moe_int8_product(at(0), floats(1), rows, ints(2), G, at(3), floats(4), O, H, epilogue, out, stride, nullptr);
+    };
+    const int G = MOE_MAX_EXPERTS, O = MOE_MAX_OUTPUTS;
+    expect(product(R, G, O, at(6), 2 * O, MOE_MX_PLAIN), MOE_OK, 1, "product at the largest sizes");
+    expect(product(R, G, O, at(6), O, MOE_MX_GATED), MOE_OK, 1, "gated at the largest sizes");
+    expect(product(R, G, O, at(6), 2 * O - 2, MOE_MX_PLAIN), MOE_ERR_ARG, 0, "rows of results that overlap");
+    expect(product(2, G, O, at(6), big - 1, MOE_MX_PLAIN), MOE_ERR_ARG, 0, "results whose extent wraps");
+    expect(product(big, G, O, at(6), 2 * O, MOE_MX_PLAIN), MOE_ERR_ARG, 0, "too many rows");
+    expect(product(4, G, O, at(3, (int64_t)G * O * H), 2 * O, MOE_MX_PLAIN), MOE_OK, 1, "results behind the weights");
+    expect(product(4, G, O, at(3, (int64_t)G * O * H - 2), 2 * O, MOE_MX_PLAIN), MOE_ERR_ARG, 0, "results over the weights");
+    expect(product(4, G, O, at(4, (int64_t)G * O * 4 - 2), 2 * O, MOE_MX_PLAIN), MOE_ERR_ARG, 0, "results over the weights' scales");
+    expect(product(4, G, O, at(2, 4 * G + 4), 2 * O, MOE_MX_PLAIN), MOE_OK, 1, "results behind the bases");
+    expect(product(4, G, O, at(2, 4 * G + 2), 2 * O, MOE_MX_PLAIN), MOE_ERR_ARG, 0, "results over the bases");
+    result = hipErrorInvalidValue;
+    expect(product(4, G, O, at(6), 2 * O, MOE_MX_PLAIN), MOE_ERR_HIP, 1, "a failed launch");
+    result = hipSuccess;
+
+    const auto norm = [&](int64_t rows, int64_t stride, char *sum, int64_t sum_stride, char *out, float eps) {
+        return moe_rms_norm(at(0), stride, at(1), stride, at(2), MOE_FP32, eps, rows, H, I8, sum, sum_stride, out, at(5), floats(6), nullptr);
+    };
+    expect(norm(R, pitch, at(3), pitch, at(4), 1e-6f), MOE_OK, 1, "norm at the largest sizes");
+    expect(norm(R, pitch, at(0), pitch, at(4), 1e-6f), MOE_OK, 1, "the sum in x's place");
+    expect(norm(R, pitch, at(1), pitch, nullptr, 1e-6f), MOE_OK, 1, "the sum in the residual's place, no bf16 output");
+    expect(norm(R, pitch, at(0), pitch + 16, at(4), 1e-6f), MOE_ERR_ARG, 0, "the sum over x at another stride");
+    expect(norm(R, pitch, at(0, pitch), pitch, at(4), 1e-6f), MOE_ERR_ARG, 0, "the sum over other rows of x");
+    expect(norm(R, pitch, at(0, R * pitch), pitch, at(4), 1e-6f), MOE_OK, 1, "the sum behind x");
+    expect(norm(1, even, at(0), even, at(4), 1e-6f), MOE_OK, 1, "one row in place at the largest stride");
+    expect(norm(2, even, at(3), pitch, at(4), 1e-6f), MOE_ERR_ARG, 0, "rows whose extent wraps");
+    expect(norm(R, pitch, at(3), pitch, at(3, R * pitch - 16), 1e-6f), MOE_ERR_ARG, 0, "the output over the sum");
+    expect(norm(R, pitch, at(3), pitch, at(5, -R * pitch + 16), 1e-6f), MOE_ERR_ARG, 0, "the output over the codes");
+    expect(norm(R, pitch, at(3), pitch, at(4), std::numeric_limits<float>::denorm_min()), MOE_OK, 1, "the smallest eps");
+    expect(norm(R, pitch, at(3), pitch, at(4), 0.0f), MOE_ERR_ARG, 0, "no eps");
+    expect(norm(R, pitch, at(3), pitch, at(4), std::nanf("")), MOE_ERR_ARG, 0, "an eps that is no number");
+    expect(moe_rms_norm(nullptr, pitch, nullptr, 0, at(2), MOE_BF16, 1e-6f, 0, H, I8, nullptr, 0, nullptr, nullptr, nullptr, nullptr), MOE_OK, 1,
+           "no rows");
+
+    for (const int64_t rows : {(int64_t)0, (int64_t)1, (int64_t)255, (int64_t)5000, R}) {
+        for (const int h : {16, 512, 1024, 2064, 8192, H}) {
+            const int64_t need = moe_rms_norm_backward_workspace_bytes(rows, h), p = 2 * (int64_t)h;
+            const int64_t parts = moe::norm_parts(rows, h);
+            if (need < 0 || parts > rows || (parts > 1 && need < parts * h * 4)) ++failures, std::printf("FAIL: workspace of %d rows\n", (int)rows);
+            const auto back = [&](int64_t bytes, char *ws, float *dw) {
+                return moe_rms_norm_backward(at(0), p, at(1), p, at(2), MOE_FP32, 1e-6f, at(3), p, rows, h, at(4), dw, ws, bytes, nullptr);
+            };
+            expect(back(need, need ? at(6) : nullptr, floats(5)), MOE_OK, 1, "gradient with its workspace");
+            if (!need) continue;
+            expect(back(need - 1, at(6), floats(5)), MOE_ERR_WINDOW, 0, "gradient with a shorter one");
+            expect(back(need, nullptr, floats(5)), MOE_ERR_ARG, 0, "gradient without one");
+            expect(back(need, at(5, 4 * h), floats(5)), MOE_OK, 1, "workspace behind the weight's gradient");
+            expect(back(need, at(5, 4 * h - 16), floats(5)), MOE_ERR_ARG, 0, "workspace over the weight's gradient");
+            expect(back(need, at(6), floats(4, rows * p - 16)), MOE_ERR_ARG, 0, "the weight's gradient over dx");
+        }
+    }
+    expect(moe_rms_norm_backward_workspace_bytes(R + 1, H), MOE_ERR_ARG, 0, "workspace of too many rows");
+    expect(moe_rms_norm_backward_workspace_bytes(INT64_MIN, H), MOE_ERR_ARG, 0, "workspace of negative rows");
+
+    for (const int S : {1, 128, 129, 5000, (int)MOE_MAX_TOKENS}) {
+        for (const int E : {1, 3, 64, 511, (int)MOE_MAX_EXPERTS}) {
+            const int64_t need = moe_balance_loss_workspace_bytes(S, E);
+            const int64_t parts = moe::balance_parts(S);
+            // the joining kernel's first parts lanes read the parts' tokens; a part's counts fit 16 bits
+            if (need < 0 || parts > 1024 || (S + parts - 1) / parts * MOE_MAX_K > 65535) ++failures, std::printf("FAIL: parts of %d tokens\n", S);
+            const auto loss = [&](int64_t bytes, char *ws) {
+                return moe_balance_loss(at(0), 4 * E, MOE_FP32, ints(1), S, MOE_MAX_K, E, MOE_SCORE_SIGMOID, 0.01f, floats(2), ints(3), ints(4), ws, bytes, nullptr);
+            };
+            expect(loss(need, need ? at(5) : nullptr), MOE_OK, 1, "loss with its workspace");
+            if (need) {
+                expect(loss(need - 1, at(5)), MOE_ERR_WINDOW, 0, "loss with a shorter one");
+                expect(loss(need, nullptr), MOE_ERR_ARG, 0, "loss without one");
+                expect(loss(need, at(3, E * 4 - 4 > 0 ? (E * 4 - 4) / 16 * 16 : 0)), MOE_ERR_ARG, 0, "workspace over the counts");
+            }
+            const auto grad = [&](int64_t stride, char *d) {
+                return moe_balance_loss_backward(floats(6), at(0), stride, MOE_BF16, ints(1), ints(3), ints(4), S, MOE_MAX_K, E, MOE_SCORE_SOFTMAX, -1.0f, d, nullptr);
+            };
+            expect(grad(2 * E, at(5)), MOE_OK, 1, "gradient of the loss");
+            expect(grad(2 * E, at(0, 2 * (int64_t)S * E)), MOE_OK, 1, "gradient behind the logits");
+            expect(grad(2 * E, at(0, 2 * (int64_t)S * E - 2)), MOE_ERR_ARG, 0, "gradient over the logits");
+            expect(grad(big, at(5)), S > 1 ? MOE_ERR_ARG : MOE_ERR_ALIGN, 0, "logits whose extent wraps");
+        }
+    }
+
+    if (failures) return 1;
+    std::printf("layer_asan ok\n");
+    return 0;
+}
