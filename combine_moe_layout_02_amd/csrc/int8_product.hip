@@ -85,12 +85,17 @@ __global__ __launch_bounds__(64 * WMC * WNC) void int8_tile_kernel(
     const uint8_t *__restrict__ a_codes, const float *__restrict__ a_scales, int64_t a_rows,
     const int32_t *__restrict__ base, int G, const uint8_t *__restrict__ w_codes,
     const float *__restrict__ w_scales, int O, int H, int ncol, uint8_t *__restrict__ out, int64_t out_stride,
-    bool wide) {
+    bool wide, bool lines) {
     constexpr int NW = WMC * WNC;
     constexpr int ROWS = TM + TN, WM = TM / WMC, WN = TN / WNC, MI = WM / 16, NI = WN / 16;
     constexpr int LOADS = ROWS / 8 / NW;     // 8 rows of a pair of stages a load
     constexpr int OF = GATED ? NI / 2 : NI;  // column fragments of results
     constexpr int STORES = MI * OF / 2;      // stores of a wave, 16 bytes a lane
+    // Tiles of few rows, whose weights stream past, store whole lines with sc1 nt (decode batch, 1024 rows of 2048 -> 7168 on 32
+    // groups: 89.4 us, and 93.4 written back; with the rows to 8 bits behind it 96.3 and 97.5). Parts of lines are
+    // joined in the caches (3001 rows, 1040 -> 1000: 12.0 us, and 14.6 with sc1 nt), and large tiles' results stay there for
+    // the call that reads them (8192 rows as above 174.8 and 174.7, with the call behind 204.5 and 206.9).
+    constexpr bool STREAMS = TM < 256;
     static_assert((PAIRS == 2 || PAIRS == 4) && LOADS * 8 * NW == ROWS && OF % 2 == 0 && MI * 16 * WMC == TM && NI * 16 * WNC == TN, "shape");
     // the buffers are objects of their own, so that the compiler sees the reads of one and the loads into the
     // other apart and puts no wait between them
@@ -264,7 +269,9 @@ __global__ __launch_bounds__(64 * WMC * WNC) void int8_tile_kernel(
                 const int o = o0 + (j + (q & 1)) * 16 + (q >> 1) * 8;
                 if (wide) {
                     const bool in = i < mi && r < tile.rows && o < width;
-                    __builtin_amdgcn_raw_buffer_store_b128(r8, dst, in ? r * (int)out_stride + o * 2 : 0x7FFFFFF0, 0, 0);
+                    const int at = in ? r * (int)out_stride + o * 2 : 0x7FFFFFF0;
+                    if (STREAMS && lines) __builtin_amdgcn_raw_buffer_store_b128(r8, dst, at, 0, 16 | 2);
+                    else __builtin_amdgcn_raw_buffer_store_b128(r8, dst, at, 0, 0);
                 } else if (i < mi && r < tile.rows) {
                     uint16_t *to = reinterpret_cast<uint16_t *>(out + ((int64_t)tile.first + r) * out_stride) + o;
 #pragma unroll
@@ -389,7 +396,7 @@ struct Args {
     bool gated;
     uint8_t *out;
     int64_t out_stride;
-    bool wide;
+    bool wide, lines;
     hipStream_t stream;
 };
 
@@ -414,7 +421,7 @@ hipError_t tiles(const Args &p) {
     const int64_t grid = PAIRS > 2 || need < resident ? need : resident;
     auto *kernel = p.gated ? int8_tile_kernel<TM, TN, WMC, WNC, PAIRS, true> : int8_tile_kernel<TM, TN, WMC, WNC, PAIRS, false>;
     hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WMC * WNC), 0, p.stream, p.a_codes, p.a_scales, p.a_rows,
-                       p.base, p.G, p.w_codes, p.w_scales, p.O, p.H, ncol, p.out, p.out_stride, p.wide);
+                       p.base, p.G, p.w_codes, p.w_scales, p.O, p.H, ncol, p.out, p.out_stride, p.wide, p.lines);
     return hipGetLastError();
 }
 
@@ -430,9 +437,10 @@ hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64
     // rows of whole 16-byte pieces, and a tile of them within a buffer descriptor's range
     const bool wide = width % 8 == 0 && out_stride_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                       out_stride_bytes <= (1 << 22);
+    const bool lines = wide && out_stride_bytes % 128 == 0 && reinterpret_cast<uintptr_t>(out) % 128 == 0;
     const Args p = {static_cast<const uint8_t *>(a_codes), a_scales, a_rows, group_base, G,
                     static_cast<const uint8_t *>(w_codes), w_scales, O, H, gated, static_cast<uint8_t *>(out),
-                    out_stride_bytes, wide, stream};
+                    out_stride_bytes, wide, lines, stream};
     // Which kernel, by the tiles it would have if the rows were spread over as many groups as they can reach, a quarter of
     // them more in the fuller ones. One run over the kernels, weights from memory, uneven groups (us; groups x rows a group):
     //   7168 -> 4096 gated   1x8    1x64   1x256  1x512  1x2000*  4x16   4x32   4x128  8x32   8x64   8x128  32x2   32x16  32x64  32x256

@@ -5,8 +5,7 @@
 // values, so that every byte is moved once. The sum of squares is taken in 64 bits: the squares of bf16 values are exact
 // there, nothing overflows, and the codes, which lie next to borders, do not depend on the order of the additions.
 
-#include "mx_blocks.h"
-#include "pack_rows.h"
+#include "row_codes.h"
 #include "wave_ops.h"
 
 namespace moe {
@@ -64,23 +63,6 @@ __device__ inline void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-}
-
-// RN(1 / scale) and the corrections of div_by_scale give the correctly rounded quotient unless all bits of the scale's
-// mantissa are set.
-__device__ inline bool fast_scale(float scale) {
-    return scale >= rows::kFastDivMinScale && scale <= 0x1.fffffep127f &&
-           (__float_as_uint(scale) & 0x7FFFFFu) != 0x7FFFFFu;
-}
-
-template <int QUANT, bool FAST>
-__device__ inline uint32_t code4(const float *v, float scale, float y) {
-    const float q0 = rows::quotient<FAST>(v[0], scale, y), q1 = rows::quotient<FAST>(v[1], scale, y);
-    const float q2 = rows::quotient<FAST>(v[2], scale, y), q3 = rows::quotient<FAST>(v[3], scale, y);
-    if constexpr (QUANT == MOE_QUANT_FP8_E4M3_DYN)
-        return rows::e4m3fn_pack4(q0, q1, q2, q3);
-    else
-        return rows::int8_code(q0) | (rows::int8_code(q1) << 8) | (rows::int8_code(q2) << 16) | (rows::int8_code(q3) << 24);
 }
 
 // A workgroup a row, or a wave a row (waves == 1). sum may be x's or residual's rows: a lane stores what it has read.
@@ -162,16 +144,14 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_kernel(
             for (int w = 0; w < waves; ++w) top = max(top, wave_top[w]);
         }
         const float scale = top < 0x7F800000u ? __uint_as_float(top) / rows::code_max<QUANT>() : __uint_as_float(0x7FC00000u);
-        const bool fast = fast_scale(scale);
+        const bool fast = rows::corrected(scale);
         const float inv = 1.0f / scale;
         const __amdgpu_buffer_rsrc_t dst = rows::rsrc(codes + r * (nvec << 3), nvec << 3);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             u32x2 c = {0u, 0u};
-            if (fast)
-                c = u32x2{code4<QUANT, true>(y[i], scale, inv), code4<QUANT, true>(y[i] + 4, scale, inv)};
-            else if (scale > 0.0f)
-                c = u32x2{code4<QUANT, false>(y[i], scale, inv), code4<QUANT, false>(y[i] + 4, scale, inv)};
+            if (fast) c = rows::codes8<QUANT>(y[i], scale, inv);
+            else if (scale > 0.0f) c = rows::divided8<QUANT>(y[i], scale);
             __builtin_amdgcn_raw_buffer_store_b64(c, dst, (u + i * lanes) << 3, 0, kStorePolicy);
         }
         if (u == 0) scales[r] = scale;

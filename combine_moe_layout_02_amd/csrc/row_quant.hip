@@ -1,8 +1,7 @@
 // Rows to 8 bits with one fp32 scale a row, and back, for gfx950 (see moe_row_quantize in moe.h; pack_rows.h has the
 // arithmetic, which is the quantised dispatch's).
 
-#include "mx_blocks.h"
-#include "pack_rows.h"
+#include "row_codes.h"
 #include "wave_ops.h"
 
 namespace moe {
@@ -55,16 +54,17 @@ __global__ __launch_bounds__(kMaxThreads) void row_quantize_kernel(
     }
     const float scale = top >= 0x7F80u ? __uint_as_float(0x7FC00000u)
                                        : __uint_as_float(top << 16) / rows::code_max<QUANT>();
-    const bool fast = scale >= rows::kFastDivMinScale;
+    const bool fast = rows::corrected(scale);
     const float inv = 1.0f / scale;
     const __amdgpu_buffer_rsrc_t dst = rows::rsrc(codes + r * (nvec << 3), nvec << 3);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
+        float v[8];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[2 * w] = rows::bf16_lo(x[i][w]), v[2 * w + 1] = rows::bf16_hi(x[i][w]);
         u32x2 c = {0u, 0u};
-        if (fast)
-            c = u32x2{rows::quant4<QUANT, true>(x[i][0], x[i][1], scale, inv), rows::quant4<QUANT, true>(x[i][2], x[i][3], scale, inv)};
-        else if (scale > 0.0f)
-            c = u32x2{rows::quant4<QUANT, false>(x[i][0], x[i][1], scale, inv), rows::quant4<QUANT, false>(x[i][2], x[i][3], scale, inv)};
+        if (fast) c = rows::codes8<QUANT>(v, scale, inv);
+        else if (scale > 0.0f) c = rows::divided8<QUANT>(v, scale);
         __builtin_amdgcn_raw_buffer_store_b64(c, dst, (u + i * lanes) << 3, 0, kStorePolicy);
     }
     if (u == 0) scales[r] = scale;
