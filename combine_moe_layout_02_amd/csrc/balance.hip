@@ -13,6 +13,7 @@ typedef __bf16 bf16_t;
 constexpr int kPartThreads = 1024, kPartWaves = kPartThreads / 64;
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kFinishThreads = 1024;
+constexpr int kFinishSlices = 32;
 constexpr int kBackwardGrid = 2048;
 
 // exp(x) for x <= 0 to 2 ulp, from the hardware's exp2 of x * log2(e) and the rest of that product; 0 from -200 down, NaN of a
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(kPartThreads) void balance_parts_kernel(
 }
 
 // One workgroup: four experts a thread, `groups` threads (E / 4 rounded up to a power of two) to a part's row, as many parts
-// at once as there are threads for them; then the threads' sums in order.
+// at once as there are threads for them, 32 at most; then the threads' sums in order.
 __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
     const float *__restrict__ part_sums, const uint16_t *__restrict__ part_counts,
     const int32_t *__restrict__ part_tokens, int parts, int E, int groups, float coef, float *__restrict__ loss,
@@ -149,10 +150,10 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
     __shared__ double share[kFinishThreads / 64];
     __shared__ int32_t entries[kFinishThreads / 64], lives[kFinishThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wide = (E + 3) / 4 * 4, e = (tid & (groups - 1)) * 4, slice = tid / groups, slices = kFinishThreads / groups;
+    const int wide = (E + 3) / 4 * 4, e = (tid & (groups - 1)) * 4, slice = tid / groups, slices = min(kFinishThreads / groups, kFinishSlices);
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int c[4] = {0, 0, 0, 0}, live = 0;
-    if (e < wide) {
+    if (e < wide && slice < slices) {
 #pragma unroll 16
         for (int p = slice; p < parts; p += slices) {
             const float4 f = *reinterpret_cast<const float4 *>(part_sums + p * wide + e);
@@ -162,10 +163,12 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
         }
     }
     if (tid < parts) live = part_tokens[tid];
+    if (slice < slices) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        sums[slice * 4 * groups + e + i] = s[i];
-        count[slice * 4 * groups + e + i] = c[i];
+        for (int i = 0; i < 4; ++i) {
+            sums[slice * 4 * groups + e + i] = s[i];
+            count[slice * 4 * groups + e + i] = c[i];
+        }
     }
     __syncthreads();
     double part = 0.0;
