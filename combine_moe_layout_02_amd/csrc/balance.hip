@@ -1,7 +1,11 @@
 // The router's balance loss over the experts' counts, and its gradient, for gfx950 (see moe_balance_loss in moe.h).
 //
 // A wave takes a token: lane l holds experts l, l + 64, ... of it, so that its scores are two reductions over the wave's
-// lanes, and their sums over tokens stay in its registers. All of it is a few bytes and operations a logit.
+// lanes, and their sums over tokens stay in its registers. The exponentials and the reductions' chains bound it, and launches:
+// 8192 tokens of 256 experts (8.4 MB) take 12.9 us forward, 6.0 in the parts and 7 in the one workgroup that joins 256 of
+// them, and 6.5 back, 128 tokens of 16 experts (one part) 7.4 and 4.6. Parts of 128 tokens (64 of them) took 20 + 4.6, of 64
+// 8.0 + 6.4; with the library's expf, divisions and shuffles 13.6 + 20. The gradient with 1024 workgroups the same, 512
+// 7.4, 256 10.8.
 
 #include "wave_ops.h"
 

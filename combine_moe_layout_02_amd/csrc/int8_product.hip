@@ -21,7 +21,8 @@ __device__ inline i32x4 mfma(const i32x4 &a, const i32x4 &b, const i32x4 &c) {
 __device__ inline float scaled(int c, float a, float w) { return (float)c * a * w; }
 
 // As find_tile, but a group's rows are shared evenly among its tiles, in steps of STEP, so that they take the same time, in
-// step with one another over the weights they share; and of a tile's rows the piece-th of `pieces` shares.
+// step with one another over the weights they share; and of a tile's rows the piece-th of `pieces` shares. 32768 rows on 32 uneven
+// groups, 7168 -> 4096 gated: 963 us with whole tiles and a rest, 925 like this.
 template <int TM, int STEP>
 __device__ inline Tile find_even_tile(const TileTable &table, int G, int ncol, int t, int piece, int pieces) {
     Tile tile = find_tile<TM>(table, G, ncol, t);
@@ -76,10 +77,20 @@ struct Turns {
 // the pair and for its LDS reads of the last one, so behind it the pair is whole and the last pair's buffer is free.
 //
 // PAIRS == 2, many tiles: a workgroup takes tile after tile, the next tile's first pair behind a tile's last, so that
-// the loads never pause and a tile's results are stored while the next one's rows arrive.
+// the loads never pause and a tile's results are stored while the next one's rows arrive. 32768 rows on 32 even groups, 7168 -> 4096
+// gated, take 820 to 870 us (2.2 to 2.35 PFLOP/s), uneven ones 910 to 950, with matrix instructions under way for 53% of the cycles
+// at 2.18 GHz and no bank conflict. In copies of the kernel with parts taken out (even groups, 835 whole): the matrix
+// instructions alone 548 (507 on zeros: the card's power), with the reads of LDS 632, the loads alone 700, all of it on
+// rows that stay in an XCD's L2 762, on zeros 754. Not faster: the lines of later pairs brought to L2 ahead (the loads alone
+// 568, the whole the same), loads before the reads, a fragment's second stage read while the first is multiplied, 32 x 32 x 32
+// matrix instructions (1075), tiles of 320 x 256 (923, uneven 980), 256 x 128 and 128 x 256 (1041, 1076).
+//
+// Where the weights' bytes bound it (1024 rows on 32 groups, 2048 -> 7168: 90 us), a bare read of them in this pattern takes 74 and the
+// results' stores 8 to 11; three pairs under way, strips of 64 to 256 weight rows, a first pair that differs from tile to
+// tile, and a last round shared out by outputs took the same or longer.
 //
 // PAIRS > 2, tiles for every compute unit once at most: a workgroup takes one tile, whose time is its pairs' way
-// from memory and through the matrix cores.
+// from memory and through the matrix cores, 0.7 us a pair at 128 x 128.
 template <int TM, int TN, int WMC, int WNC, int PAIRS, bool GATED>
 __global__ __launch_bounds__(64 * WMC * WNC) void int8_tile_kernel(
     const uint8_t *__restrict__ a_codes, const float *__restrict__ a_scales, int64_t a_rows,
@@ -287,7 +298,8 @@ __global__ __launch_bounds__(64 * WMC * WNC) void int8_tile_kernel(
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS after the wave's end
 }
 
-// Few rows a group: the weights' bytes bound the product. A workgroup takes 16 rows of a group and 32 weight
+// Few rows a group: the weights' bytes bound the product, and the way of a wave's share of H (8 rows on one group, 7168 -> 4096
+// gated: 13.2 us; with eight waves 14.2, with two 14.2). A workgroup takes 16 rows of a group and 32 weight
 // rows (16 outputs when GATED), its four waves a quarter of H each, and every wave streams its quarter
 // through a ring of its own in LDS, waiting for nobody; the partial sums meet in LDS. LDS turns the loads' order (four
 // lanes to a row, 64 bytes) into the matrix cores' (a lane to a row).

@@ -1,9 +1,17 @@
 // The residual's addition and the root-mean-square norm, with its output in bf16, in 8 bits or both, and its gradients, for
 // gfx950 (see moe_rms_norm in moe.h).
 //
-// A workgroup takes a row: its lanes hold it in registers from the load to the store, vector v = lane + i * blockDim of 8
-// values, so that every byte is moved once. The sum of squares is taken in 64 bits: the squares of bf16 values are exact
-// there, nothing overflows, and the codes, which lie next to borders, do not depend on the order of the additions.
+// A workgroup takes a row, or a wave a short one: its lanes hold it in registers from the load to the store, vector v = lane +
+// i * lanes of 8 values, so that every byte is moved once. The sum of squares is taken in 64 bits: the squares of bf16 values are
+// exact there, nothing overflows, and the codes, which lie next to borders, do not depend on the order of the additions.
+//
+// HBM bounds all of it (4096 rows of 7168, us and TB/s of what is read and written): to bf16 41.9 and 5.6, to INT8 38.6 and 5.3,
+// the gradients 50.5 and 4.7 with d_weight's second kernel (4.7 of them). Two vectors a lane: to INT8 such rows take
+// 42.0 with two, 42.2 with four, 55 with eight and 77 with one, 1531 rows of 2064 7.8, 8.5, 12.0 and 10.4, 4096 rows
+// of 1024 7.2, 9.6, 21.4 and 9.3, 128 rows of 7168 5.2, 5.4, 6.3 and 6.3. A workgroup that takes row after row with the weights in
+// its registers and the next row's loads under way is no faster (44.9, two rows a compute unit in flight) and its
+// registers cost short rows (1531 rows 9.9 to 14). Stores with nt 42.0, sc0 sc1 nt 42.2, written back 43.8. Reductions through
+// shuffles, an LDS access a step, and four times the waves a row took 72.
 
 #include "row_codes.h"
 #include "wave_ops.h"
@@ -158,8 +166,11 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_kernel(
     }
 }
 
-// Rows first, first + step, ..., a workgroup or a wave each, the next one's loads under way while one is turned; a lane's share of d_weight stays in registers until the end, where each workgroup's, or its waves', go to
-// partial[part].
+// Rows first, first + step, ..., a workgroup or a wave each, the next one's loads under way while one is turned; a lane's share of
+// d_weight stays in registers until the end, where each workgroup's, or its waves', go to partial[part]. 256 parts of rows
+// of 7168 47.0 us for 4096 of them, 512 parts 50.7, 1024 58 (their sums are written and read again); shorter rows leave room for
+// more on a compute unit: 1531 rows of 2064 14.2, 13.8 and 16.3, 4096 of 1024 21.8, 14.7 and 14.0. Several rows a workgroup,
+// their shares of d_weight joined through LDS, took 52.7, 18.4 and 21.2.
 template <int VPL, int WTYPE>
 __global__ __launch_bounds__(kMaxThreads) void rms_norm_backward_kernel(
     const uint8_t *__restrict__ dy, int64_t dy_stride, const uint8_t *__restrict__ sum, int64_t sum_stride,
