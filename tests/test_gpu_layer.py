@@ -8,8 +8,8 @@ Tolerances elsewhere, derived before the first run; u = 2^-24 is fp32's rounding
   then half a step: (2^-8 + 2^-13) |result|, and 2^-133 for what underflows in bf16;
 * the norm's dx = r (g - n m) + d: r, n, g, m are each off by at most 3 roundings, the three sums and products add
   four: 2^-21 (|r g| + |r n m| + |d|), then half a step of the result;
-* d_weight: each term is off by 4 u and passes at most 600 additions (rows of a part, parts of a wave, 16 waves) for up to
-  16384 rows: 2^-14 of the sum of magnitudes at the very most; for S rows (S / 512 + 52 + 4) u is used;
+* d_weight: each term is off by 4 u and passes the additions of its part's rows (S / 256 of them, or one, in 256 to 1024 parts),
+  of every 64th part (16 at most) and of those 64 sums: (S / 256 + 85) u of the sum of magnitudes;
 * scores: exp's argument l - max is rounded (d u for a distance d), exp is good to 2 u, sum and quotient add 16 u:
   (24 + d) u of each score; the loss sums S of them in an order of at most 300 additions, so (324 + max d) u, where d is
   at most 88 for a score that is not 0 in fp32;
@@ -229,6 +229,23 @@ def test_product_strides_and_odd_widths(moe, R, G, H, O, gap, epilogue):
         product_case(moe, rng, spread_base(rng, R, G), R, G, H, O - 1, epilogue, gap, "odd width")
 
 
+@pytest.mark.parametrize("R,G,H,O,epilogue,gap", [
+    (12288, 1, 80, 1024, PLAIN, 0), (9000, 3, 144, 1030, PLAIN, 0), (5000, 4, 208, 4096, GATED, 8),           # tiles of 256 x 256
+    (2500, 7, 3088, 600, PLAIN, 0), (512, 4, 2064, 4096, GATED, 0), (700, 1, 2096, 5000, PLAIN, 3),          # 128 x 128, one a unit
+    (2000, 16, 144, 2050, PLAIN, 0), (1500, 20, 1040, 2048, GATED, 4),                                       # 128 x 128 in turns
+    (1024, 32, 272, 4096, PLAIN, 0), (3001, 16, 1040, 1000, PLAIN, 0), (900, 40, 528, 4100, GATED, 0),       # 64 x 128 in turns
+    (600, 2, 96, 2000, PLAIN, 0), (250, 3, 1088, 1100, GATED, 2), (40, 5, 2000, 2222, PLAIN, 0),            # smaller ones
+    (600, 512, 64, 64, GATED, 0), (9000, 512, 96, 320, PLAIN, 0)])                                           # the most groups
+def test_product_kernels(moe, R, G, H, O, epilogue, gap):
+    """Every tile, with uneven groups, partly filled tiles, odd widths and ends of H inside a stage, and last rounds that leave
+    workgroups without a tile of their own."""
+    rng = np.random.default_rng(R + G)
+    share = rng.dirichlet(np.full(G, 4.0))
+    base = np.concatenate(([0], np.floor(np.cumsum(share) * R).astype(np.int64)))
+    base[-1] = R
+    product_case(moe, rng, base, R, G, H, O, epilogue, gap, "kernels")
+
+
 @pytest.mark.parametrize("R,base", [(50, [3, 3, 20, 20, 44]), (50, [0, 0, 0, 0, 50]), (50, [50, 50, 50, 50, 50]), (50, [-7, 10, 5, 30, 99]),
                                     (50, [30, 10, 20, 45, 40]), (700, [100, 99, 400, 400, 650]), (700, [-5, 300, 200, 690, 800])])
 @pytest.mark.parametrize("epilogue", [PLAIN, GATED])
@@ -356,7 +373,7 @@ def grad_case(moe, S, H, gap, residual, kind, seed, eps=1e-5, scale=1.0):
     n = hv * r
     terms = np.abs(r * g) + np.abs(r * n * (g * n).mean(axis=1, keepdims=True)) + (np.abs(oracle.bf16_bits_to_f32(d_sum)) if residual else 0)
     near(values(dx), want_dx, 2.0**-21 * terms + 2.0**-8 * np.abs(want_dx) + 2.0**-133, "dx")
-    near(values(dw), want_dw, (S / 512 + 56) * U * np.abs(oracle.bf16_bits_to_f32(dy) * n).sum(axis=0), "d_weight")
+    near(values(dw), want_dw, (S / 256 + 85) * U * np.abs(oracle.bf16_bits_to_f32(dy) * n).sum(axis=0), "d_weight")
     return dx, dw
 
 
@@ -628,6 +645,61 @@ def test_graph(moe):
             g.replay()
             torch.cuda.synchronize()
             assert equal(outs, want), k
+
+
+def test_most_rows(moe):
+    """2^20 rows of 16 values: a wave a row, and as many parts of the gradient as there are."""
+    rng = np.random.default_rng(11)
+    R, H = 1 << 20, 16
+    x = bits(rng.standard_normal((R, H)))
+    at = np.concatenate((np.arange(64), rng.integers(0, R, 400), np.arange(R - 64, R)))
+    w, w_dev = norm_weight(rng, H, "fp32")
+    dev = bf16_dev(x)
+    for quant in (INT8, E4M3):
+        note("most rows", quant)
+        got = moe.moe_row_quantize(dev, quant)
+        codes, scales = oracle.row_quantize(x[at], quant)
+        index = to_dev(at)
+        same_rows8(moe.ScaledRows(got.codes[index], got.scales[index]), codes, scales)
+        same_bits(bf16_bits(moe.moe_row_dequantize(got, quant)[index]), bits(oracle.row_values(codes, scales, quant)))
+    n = moe.moe_rms_norm(dev, w_dev, 1e-6, residual=dev)
+    s, y = oracle.rms_norm(x[at], x[at], w, 1e-6)
+    same_bits(bf16_bits(n.sum[index]), s)
+    same_bits(bf16_bits(n.out[index]), bits(y))
+    dx, dw = moe.moe_rms_norm_backward(dev, n.sum, w_dev)
+    total = bits(2 * oracle.bf16_bits_to_f32(x))
+    want_dx, want_dw = oracle.rms_norm_backward(x, total, w, 1e-6)
+    hv, g = oracle.bf16_bits_to_f32(total).astype(np.float64), oracle.bf16_bits_to_f32(x).astype(np.float64)
+    r = 1 / np.sqrt((hv * hv).mean(axis=1, keepdims=True) + 1e-6)
+    terms = np.abs(r * g * w) + np.abs(hv * r * r * (g * w * hv * r).mean(axis=1, keepdims=True))
+    near(values(dx), want_dx, 2.0**-21 * terms + 2.0**-8 * np.abs(want_dx), "dx")
+    # 1024 parts of 1024 rows, 64 sums of 16 parts: 1024 + 16 + 64 additions and 4 roundings of a term
+    near(values(dw), want_dw, 1108 * U * np.abs(g * hv * r).sum(axis=0), "d_weight")
+
+
+def test_most_tokens_and_experts(moe):
+    """The largest router call: counts exactly, the loss and some tokens' gradients."""
+    rng = np.random.default_rng(12)
+    S, E, K = 65536, 512, 16
+    idx = rng.integers(-1, E, (S, K)).astype(np.int32)
+    l = rng.standard_normal((S, E)).astype(np.float32)
+    dev = to_dev(l)
+    note("most tokens")
+    got = moe.moe_balance_loss(dev, to_dev(idx), 0.5)
+    counts = np.bincount(idx[idx >= 0], minlength=E)
+    live = (idx >= 0).any(axis=1)
+    assert np.array_equal(got.num_tokens_per_expert.cpu().numpy(), counts) and int(got.num_tokens) == live.sum()
+    p = np.exp(l.astype(np.float64) - l.max(axis=1, keepdims=True))
+    p = np.where(live[:, None], p / p.sum(axis=1, keepdims=True), 0)
+    each = 0.5 * E / (counts.sum() * float(live.sum()))
+    loss = each * float((p.sum(axis=0) * counts).sum())
+    near(values(got.loss), [loss], 412 * U * loss, "loss")  # 16 tokens a wave, 16 waves, 256 parts over 8 slices: 16 + 16 + 32 + 8 additions
+    d = moe.moe_balance_loss_backward(torch.ones(1, device=DEV), dev, to_dev(idx), got.num_tokens_per_expert, got.num_tokens, 0.5)
+    g = counts - counts.sum() // E
+    at = np.concatenate((np.arange(100), np.arange(S - 100, S)))
+    dot = (p * g).sum(axis=1, keepdims=True)
+    tol = each * U * 96 * p * (np.abs(g) + (p * np.abs(g)).sum(axis=1, keepdims=True))
+    near(values(d)[at], (each * p * (g - dot))[at], tol[at] + 2.0**-148, "d_logits")
 
 
 def test_buffers_past_4_gib(moe):
