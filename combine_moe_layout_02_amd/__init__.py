@@ -57,7 +57,7 @@ EXPORTED = (
     "moe_plan_layout_dispatch", "moe_plan_combine", "moe_plan_layout_ws", "moe_plan_dispatch_planned", "moe_plan_run",
     "moe_combine_backward", "moe_combine_backward_mx", "moe_dispatch_backward", "moe_combine_checkpoint",
     "moe_mx_row_bytes", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_product",
-    "moe_row_quantize", "moe_row_dequantize", "moe_int8_product", "moe_rms_norm", "moe_rms_norm_backward",
+    "moe_row_quantize", "moe_row_dequantize", "moe_scaled_product", "moe_rms_norm", "moe_rms_norm_backward",
     "moe_rms_norm_backward_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
     "moe_balance_loss_workspace_bytes",
 )
@@ -126,7 +126,7 @@ def _load():
         "moe_mx_product": (ctypes.c_int, [P, P, I64, P, I32, P, P, I32, I32, I32, P, I64, P]),
         "moe_row_quantize": (ctypes.c_int, [P, I64, P, I64, I32, I32, P, P, P]),
         "moe_row_dequantize": (ctypes.c_int, [P, P, P, I64, I32, I32, P, I64, P]),
-        "moe_int8_product": (ctypes.c_int, [P, P, I64, P, I32, P, P, I32, I32, I32, P, I64, P]),
+        "moe_scaled_product": (ctypes.c_int, [P, P, I64, P, I32, P, P, I32, I32, I32, P, I64, P]),
         "moe_rms_norm": (ctypes.c_int, [P, I64, P, I64, P, I32, F32, I64, I32, I32, P, I64, P, P, P, P]),
         "moe_rms_norm_backward_workspace_bytes": (I64, [I64, I32]),
         "moe_rms_norm_backward": (ctypes.c_int, [P, I64, P, I64, P, I32, F32, P, I64, I64, I32, P, P, P, I64, P]),
@@ -1262,7 +1262,7 @@ def moe_row_dequantize(rows8, quant, num_rows=None, out=None, stream=None):
     return out
 
 
-def moe_int8_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=None):
+def moe_scaled_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=None):
     """The experts' product of INT8 rows a (ScaledRows [R, H], e.g. of moe_unpack's expand_x and expand_scales) with
     INT8 weights w (ScaledRows [G, O, H], a scale for each output): row r of group g (group_base int32 [G + 1] on the
     device, e.g. layout.expert_slot_base; [0, R] with G = 1 for a shared expert) gives bf16 [O], or [O / 2] of
@@ -1286,7 +1286,7 @@ def moe_int8_product(a, w, group_base, epilogue=MOE_MX_PLAIN, out=None, stream=N
         if n and (width > 1 and out.stride(1) != 1 or n > 1 and out.stride(0) < width):
             raise ValueError("out must have contiguous rows that do not overlap")
         out_stride = 2 * out.stride(0) if n > 1 else 2 * width
-    _launch(dev, stream, _lib.moe_int8_product, a_ptr, as_ptr, n, base_ptr, G, w_ptr, ws_ptr, O, H, epilogue,
+    _launch(dev, stream, _lib.moe_scaled_product, a_ptr, as_ptr, n, base_ptr, G, w_ptr, ws_ptr, O, H, epilogue,
             out.data_ptr(), out_stride)
     return out
 
@@ -1474,6 +1474,6 @@ __all__ = [
     "moe_combine_checkpoint", "moe_combine_backward_mx", "moe_dispatch_backward", "moe_mx_row_bytes",
     "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_product",
     "MOE_BF16", "MOE_FP32", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "ScaledRows", "moe_row_quantize", "moe_row_dequantize",
-    "moe_int8_product", "RmsNorm", "moe_rms_norm", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace_bytes",
+    "moe_scaled_product", "RmsNorm", "moe_rms_norm", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace_bytes",
     "BalanceLoss", "moe_balance_loss", "moe_balance_loss_backward", "moe_balance_loss_workspace_bytes",
 ]

@@ -1,4 +1,4 @@
-// The experts' product of INT8 rows and weights for gfx950 (see moe_int8_product in moe.h).
+// The experts' product of INT8 rows and weights for gfx950 (see moe_scaled_product in moe.h).
 //
 // v_mfma_i32_16x16x64_i8 multiplies a 16 x 64 by a 64 x 16 tile, lane l giving 16 consecutive values (16 bytes) of row
 // l % 16, k-block l / 16, of either operand. The weights are the first operand, so that a lane's four results are

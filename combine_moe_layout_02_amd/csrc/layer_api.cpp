@@ -78,10 +78,10 @@ int moe_row_dequantize(const void *codes, const float *scales, const int32_t *nu
                                                row_stride_bytes, stream));
 }
 
-int moe_int8_product(const void *a_codes, const float *a_scales, int64_t a_rows,
-                     const int32_t *group_base, int32_t G, const void *w_codes,
-                     const float *w_scales, int32_t O, int32_t H, int32_t epilogue, void *out,
-                     int64_t out_stride_bytes, hipStream_t stream) {
+int moe_scaled_product(const void *a_codes, const float *a_scales, int64_t a_rows,
+                       const int32_t *group_base, int32_t G, const void *w_codes,
+                       const float *w_scales, int32_t O, int32_t H, int32_t epilogue, void *out,
+                       int64_t out_stride_bytes, hipStream_t stream) {
     int st = check_hidden(H);
     if (st != MOE_OK) return st;
     st = check_count(a_rows);

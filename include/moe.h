@@ -690,10 +690,10 @@ int moe_row_dequantize(const void *codes, const float *scales, const int32_t *nu
  * Out: out       bf16, row r at r * out_stride_bytes (2-byte aligned, stride even and at least a row of results).
  *                Rows outside every group, and the bytes between rows, keep their contents.
  * Enqueues one kernel. */
-int moe_int8_product(const void *a_codes, const float *a_scales, int64_t a_rows,
-                     const int32_t *group_base, int32_t G, const void *w_codes,
-                     const float *w_scales, int32_t O, int32_t H, int32_t epilogue, void *out,
-                     int64_t out_stride_bytes, hipStream_t stream);
+int moe_scaled_product(const void *a_codes, const float *a_scales, int64_t a_rows,
+                       const int32_t *group_base, int32_t G, const void *w_codes,
+                       const float *w_scales, int32_t O, int32_t H, int32_t epilogue, void *out,
+                       int64_t out_stride_bytes, hipStream_t stream);
 
 /* Element types of a norm's weight and of the router's logits. */
 typedef enum {
@@ -735,10 +735,10 @@ int moe_rms_norm(const void *x, int64_t x_stride_bytes, const void *residual,
  *      sum        what the forward normed: its sum, or x without a residual; weight, weight_type, eps as there.
  *      d_sum      the gradient that reaches the sum on its other ways, bf16 rows, or NULL.
  *      workspace  16-byte aligned, moe_rms_norm_backward_workspace_bytes(rows, H) at least (MOE_ERR_WINDOW); its
- *                 contents do not matter. Calls that may run at once need one each.
+ *                 contents do not matter. Calls that may run at once need one each. May be NULL where that is 0.
  * Out: dx         bf16 [rows, H], dense, 16-byte aligned.
  *      d_weight   fp32 [H], 16-byte aligned, fully overwritten (zeros for no rows).
- * Enqueues two kernels. */
+ * Enqueues at most two kernels. */
 int64_t moe_rms_norm_backward_workspace_bytes(int64_t rows, int32_t H);
 
 int moe_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *sum,
@@ -765,7 +765,7 @@ int moe_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *s
  *      topk_idx   int32 [S, K]; ids outside [0, E) are not valid; an id that stands twice in a row counts twice.
  *      S in [1, MOE_MAX_TOKENS], K in [1, MOE_MAX_K], E in [1, MOE_MAX_EXPERTS]; coef finite.
  *      workspace  16-byte aligned, moe_balance_loss_workspace_bytes(S, E) at least (MOE_ERR_WINDOW); its contents
- *                 do not matter. Calls that may run at once need one each.
+ *                 do not matter. Calls that may run at once need one each. May be NULL where that is 0.
  * Out: loss fp32 [1], num_tokens_per_expert int32 [E], num_tokens int32 [1] (T). Enqueues at most two kernels.
  * moe_balance_loss_backward
  * In:  d_loss fp32 [1] and the forward's arguments and counts, all DEVICE pointers. (Counts that are summed over

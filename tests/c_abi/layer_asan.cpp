@@ -92,7 +92,7 @@ int main() {
     expect(moe_row_dequantize(at(0), floats(1), nullptr, R, H, I8, at(0, R * H - 16), pitch, nullptr), MOE_ERR_ARG, 0, "rows over the codes");
 
     const auto product = [&](int64_t rows, int32_t G, int32_t O, char *out, int64_t stride, int32_t epilogue) {
-        return moe_int8_product(at(0), floats(1), rows, ints(2), G, at(3), floats(4), O, H, epilogue, out, stride, nullptr);
+        return moe_scaled_product(at(0), floats(1), rows, ints(2), G, at(3), floats(4), O, H, epilogue, out, stride, nullptr);
     };
     const int G = MOE_MAX_EXPERTS, O = MOE_MAX_OUTPUTS;
     expect(product(R, G, O, at(6), 2 * O, MOE_MX_PLAIN), MOE_OK, 1, "product at the largest sizes");

@@ -191,7 +191,7 @@ def product_case(moe, rng, base, R, G, H, O, epilogue, gap=0, what="", a=None, a
     v, group = oracle.int8_product(a, a_scales, base, w, w_scales)
     width = O // 2 if epilogue == GATED else O
     buf = poison((R, width + gap), torch.bfloat16)
-    got = moe.moe_int8_product(moe.ScaledRows(to_dev(a).view(torch.uint8), to_dev(a_scales)), moe.ScaledRows(to_dev(w), to_dev(w_scales)),
+    got = moe.moe_scaled_product(moe.ScaledRows(to_dev(a).view(torch.uint8), to_dev(a_scales)), moe.ScaledRows(to_dev(w), to_dev(w_scales)),
                                to_dev(base), epilogue, out=buf[:, :width])
     inside = group >= 0
     if epilogue == PLAIN:
@@ -267,7 +267,7 @@ def test_product_extremes(moe, epilogue):
     with np.errstate(over="ignore", invalid="ignore"):
         product_case(moe, rng, [0, 25, 40], R, 2, H, 64, epilogue, what="extremes", a=a, a_scales=scales)
     w = np.full((1, 32, H), -128, dtype=np.int8)
-    got = moe.moe_int8_product(moe.ScaledRows(to_dev(a), to_dev(np.full(R, 2.0**-28, dtype=np.float32))),
+    got = moe.moe_scaled_product(moe.ScaledRows(to_dev(a), to_dev(np.full(R, 2.0**-28, dtype=np.float32))),
                                moe.ScaledRows(to_dev(w), torch.ones(1, 32, device=DEV)), to_dev(np.array([0, R], dtype=np.int32)))
     assert np.all(values(got)[::2] == 1.0) and np.all(values(got)[1::2] == values(torch.tensor([-127 / 128], dtype=torch.bfloat16, device=DEV)))
 
@@ -275,7 +275,7 @@ def test_product_extremes(moe, epilogue):
 def test_product_of_no_rows(moe):
     w = moe.ScaledRows(torch.zeros((2, 8, 32), dtype=torch.int8, device=DEV), torch.zeros((2, 8), device=DEV))
     a = moe.ScaledRows(torch.zeros((0, 32), dtype=torch.int8, device=DEV), torch.zeros(0, device=DEV))
-    assert moe.moe_int8_product(a, w, torch.zeros(3, dtype=torch.int32, device=DEV)).shape == (0, 8)
+    assert moe.moe_scaled_product(a, w, torch.zeros(3, dtype=torch.int32, device=DEV)).shape == (0, 8)
 
 
 # ---------------------------------------------------------------- the norm
@@ -548,12 +548,12 @@ class Step:
         moe.moe_dispatch(normed.out, lay.slot_idx, self.window, INT8)
         rows = lay.expert_slot_base[E:]
         un = moe.moe_unpack(self.window, rows, S, K, H, INT8)
-        mid = moe.moe_int8_product(moe.ScaledRows(un.expand_x, un.expand_scales), self.up, lay.expert_slot_base, GATED)
+        mid = moe.moe_scaled_product(moe.ScaledRows(un.expand_x, un.expand_scales), self.up, lay.expert_slot_base, GATED)
         mid8 = moe.moe_row_quantize(mid, INT8, num_rows=rows)
-        expert_out = moe.moe_int8_product(mid8, self.down, lay.expert_slot_base)
+        expert_out = moe.moe_scaled_product(mid8, self.down, lay.expert_slot_base)
         y = moe.moe_combine(expert_out, lay.slot_idx, self.topk_weights)
-        shared = moe.moe_int8_product(normed.rows8, self.shared_up, self.all_rows, GATED)
-        shared = moe.moe_int8_product(moe.moe_row_quantize(shared, INT8), self.shared_down, self.all_rows)
+        shared = moe.moe_scaled_product(normed.rows8, self.shared_up, self.all_rows, GATED)
+        shared = moe.moe_scaled_product(moe.moe_row_quantize(shared, INT8), self.shared_down, self.all_rows)
         d_rows, d_weights = moe.moe_combine_backward(self.dy, expert_out, lay.slot_idx, self.topk_weights)
         d_out = moe.moe_dispatch_backward(d_rows, lay.slot_idx)
         d_logits = moe.moe_balance_loss_backward(torch.ones(1, device=DEV), logits, self.topk_idx, loss.num_tokens_per_expert, loss.num_tokens, 0.01)
@@ -717,7 +717,7 @@ def test_buffers_past_4_gib(moe):
     base = torch.full((301,), R - 40, dtype=torch.int32, device=DEV)
     base[300] = R
     note("product past 4 GiB")
-    got = moe.moe_int8_product(moe.ScaledRows(a, sa), moe.ScaledRows(w, ws), base)
+    got = moe.moe_scaled_product(moe.ScaledRows(a, sa), moe.ScaledRows(w, ws), base)
     v, _ = oracle.int8_product(tail, tail_scales, [0, 40], last[None], np.full((1, 1024), 2.0**-10, dtype=np.float32))
     same_bits(bf16_bits(got[-40:]), bits(v))
     del w, got

@@ -22,7 +22,7 @@ def at(i):
 CALLS = {
     "moe_row_quantize": dict(rows=at(1), stride=2048, num=NULL, n=64, H=1024, quant=INT8, codes=at(5), scales=at(6), stream=None),
     "moe_row_dequantize": dict(codes=at(5), scales=at(6), num=NULL, n=64, H=1024, quant=E4M3, rows=at(1), stride=2048, stream=None),
-    "moe_int8_product": dict(ac=at(0), asc=at(1), n=64, base=at(2), G=8, wc=at(3), ws=at(4), O=100, H=1024, epilogue=0, out=at(5),
+    "moe_scaled_product": dict(ac=at(0), asc=at(1), n=64, base=at(2), G=8, wc=at(3), ws=at(4), O=100, H=1024, epilogue=0, out=at(5),
                              stride=200, stream=None),
     "moe_rms_norm": dict(x=at(0), stride=2048, res=at(1), res_stride=2048, w=at(2), kind=2, eps=1e-6, n=64, H=1024, quant=INT8, sum=at(3),
                          sum_stride=2048, out=at(4), codes=at(5), scales=at(6), stream=None),
@@ -97,26 +97,26 @@ def test_router_arguments(name, kw, err):
     ("moe_row_dequantize", dict(rows=at(6)), ARG),
     ("moe_row_dequantize", dict(rows=at(1) + 8), ALIGN),
     ("moe_row_dequantize", dict(stride=2032), ARG),
-    ("moe_int8_product", dict(G=0), ARG),
-    ("moe_int8_product", dict(G=513), ARG),
-    ("moe_int8_product", dict(O=0), ARG),
-    ("moe_int8_product", dict(O=65537, stride=200000), ARG),
-    ("moe_int8_product", dict(epilogue=2), ARG),
-    ("moe_int8_product", dict(epilogue=1, O=101), UNSUPPORTED),
-    ("moe_int8_product", dict(stride=198), ARG),
-    ("moe_int8_product", dict(stride=201), ALIGN),
-    ("moe_int8_product", dict(stride=1 << 62), ARG),
-    ("moe_int8_product", dict(out=at(5) + 1), ALIGN),
-    ("moe_int8_product", dict(ac=at(0) + 8), ALIGN),
-    ("moe_int8_product", dict(asc=at(1) + 2), ALIGN),
-    ("moe_int8_product", dict(wc=at(3) + 8), ALIGN),
-    ("moe_int8_product", dict(ws=at(4) + 1), ALIGN),
-    ("moe_int8_product", dict(base=at(2) + 2), ALIGN),
-    ("moe_int8_product", dict(out=at(0)), ARG),
-    ("moe_int8_product", dict(out=at(1) + 252), ARG),
-    ("moe_int8_product", dict(out=at(2) + 32), ARG),
-    ("moe_int8_product", dict(out=at(3) + 8 * 100 * 1024 - 2), ARG),
-    ("moe_int8_product", dict(out=at(4) + 8 * 100 * 4 - 2), ARG),
+    ("moe_scaled_product", dict(G=0), ARG),
+    ("moe_scaled_product", dict(G=513), ARG),
+    ("moe_scaled_product", dict(O=0), ARG),
+    ("moe_scaled_product", dict(O=65537, stride=200000), ARG),
+    ("moe_scaled_product", dict(epilogue=2), ARG),
+    ("moe_scaled_product", dict(epilogue=1, O=101), UNSUPPORTED),
+    ("moe_scaled_product", dict(stride=198), ARG),
+    ("moe_scaled_product", dict(stride=201), ALIGN),
+    ("moe_scaled_product", dict(stride=1 << 62), ARG),
+    ("moe_scaled_product", dict(out=at(5) + 1), ALIGN),
+    ("moe_scaled_product", dict(ac=at(0) + 8), ALIGN),
+    ("moe_scaled_product", dict(asc=at(1) + 2), ALIGN),
+    ("moe_scaled_product", dict(wc=at(3) + 8), ALIGN),
+    ("moe_scaled_product", dict(ws=at(4) + 1), ALIGN),
+    ("moe_scaled_product", dict(base=at(2) + 2), ALIGN),
+    ("moe_scaled_product", dict(out=at(0)), ARG),
+    ("moe_scaled_product", dict(out=at(1) + 252), ARG),
+    ("moe_scaled_product", dict(out=at(2) + 32), ARG),
+    ("moe_scaled_product", dict(out=at(3) + 8 * 100 * 1024 - 2), ARG),
+    ("moe_scaled_product", dict(out=at(4) + 8 * 100 * 4 - 2), ARG),
     ("moe_rms_norm", dict(kind=0), ARG),
     ("moe_rms_norm", dict(kind=3), ARG),
     ("moe_rms_norm", dict(quant=3), ARG),
@@ -199,7 +199,7 @@ def test_binding_refuses_host_tensors():
     w, idx, one = torch.zeros(64), torch.zeros((4, 2), dtype=torch.int32), torch.zeros(1)
     rows8 = moe.ScaledRows(torch.zeros((4, 64), dtype=torch.int8), torch.zeros(4))
     for fn in (lambda: moe.moe_row_quantize(x, INT8), lambda: moe.moe_row_dequantize(rows8, INT8),
-               lambda: moe.moe_int8_product(rows8, rows8, idx), lambda: moe.moe_rms_norm(x, w),
+               lambda: moe.moe_scaled_product(rows8, rows8, idx), lambda: moe.moe_rms_norm(x, w),
                lambda: moe.moe_rms_norm_backward(x, x, w), lambda: moe.moe_balance_loss(torch.zeros((4, 8)), idx, 0.1),
                lambda: moe.moe_balance_loss_backward(one, torch.zeros((4, 8)), idx, idx, idx, 0.1)):
         with pytest.raises(ValueError, match="device tensor"):
@@ -208,6 +208,6 @@ def test_binding_refuses_host_tensors():
 
 def test_binding_refuses_other_types():
     for fn in (lambda: moe.moe_row_quantize([1.0], INT8), lambda: moe.moe_rms_norm(None, None),
-               lambda: moe.moe_int8_product(moe.ScaledRows([1], [2]), None, None)):
+               lambda: moe.moe_scaled_product(moe.ScaledRows([1], [2]), None, None)):
         with pytest.raises(TypeError, match="torch.Tensor"):
             fn()
