@@ -229,8 +229,8 @@ def _framework(s):
 
     case = s["case"]
     if case["op"] == "product":
-        return moe.moe_int8_product(moe.ScaledRows(s["a"], s["a_scales"]), moe.ScaledRows(s["w"], s["w_scales"]), s["base"],
-                                    moe.MOE_MX_GATED if case["gated"] else moe.MOE_MX_PLAIN)
+        return moe.moe_scaled_product(moe.ScaledRows(s["a"], s["a_scales"]), moe.ScaledRows(s["w"], s["w_scales"]), s["base"],
+                                      moe.MOE_MX_GATED if case["gated"] else moe.MOE_MX_PLAIN)
     if case["op"] == "rows8":
         rows8 = moe.moe_row_quantize(s["x"], case["quant"], num_rows=s["count"])
         return moe.moe_row_dequantize(rows8, case["quant"], num_rows=s["count"], out=s["out"])
