@@ -33,7 +33,7 @@ __device__ inline float exp_of(float x) {
 
 // The scores of one token from its logits (-inf past E): exp(l - max) over their sum, or sigmoids over theirs. A token whose
 // logits are all far below zero, where sigmoid(l) is exp(l) to fp32, keeps its scores: they are taken against the
-// largest. With no logit above -inf there are none. turn: 1 - sigmoid(l), for MOE_SCORE_SIGMOID.
+// largest. A logit of -inf has score 0, also where there is no other. turn: 1 - sigmoid(l), for MOE_SCORE_SIGMOID.
 template <int N, int SCORE>
 __device__ inline void scores_of(const float (&l)[N], float (&s)[N], float (&turn)[N]) {
     float top = l[0];
@@ -52,10 +52,9 @@ __device__ inline void scores_of(const float (&l)[N], float (&s)[N], float (&tur
         }
         sum += s[i];
     }
-    const bool none = top == -__builtin_inff();
     const float each = 1.0f / wave::sum(sum);
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = none ? 0.0f : s[i] * each;
+    for (int i = 0; i < N; ++i) s[i] = l[i] == -__builtin_inff() ? 0.0f : s[i] * each;
 }
 
 // A token's logits (-inf past E) and entries (-1 past K) in a wave's lanes; nothing of tokens past the end.
@@ -231,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             g[i] = (float)(n[i] - mean);
-            dot += lane + 64 * i < E ? g[i] * s[i] : 0.0f;
+            dot += g[i] * s[i];
         }
         dot = wave::sum(dot);
 #pragma unroll

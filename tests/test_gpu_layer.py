@@ -474,6 +474,30 @@ def test_balance_masks(moe, score):
     assert torch.isfinite(got.loss).all()
 
 
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_balance_of_logits_that_are_no_numbers(moe, score, value):
+    """One NaN, alone among -inf or not, makes the loss NaN and its token's gradient at the NaN; +inf does with a softmax. Other
+    tokens keep their gradients."""
+    rng = np.random.default_rng(4)
+    S, E = 40, 70
+    l = rng.standard_normal((S, E)).astype(np.float32)
+    idx = routing(rng, S, E, 3, "")
+    want = oracle.balance(l, idx, 1.0, score)[3]
+    l[7] = -np.inf
+    l[7, 66] = l[30, 2] = value
+    dev, table = to_dev(l), to_dev(idx)
+    b = moe.moe_balance_loss(dev, table, 1.0, score)
+    d = values(moe.moe_balance_loss_backward(torch.ones(1, device=DEV), dev, table, b.num_tokens_per_expert, b.num_tokens, 1.0, score))
+    lost = bool(np.isnan(value)) or score == 0
+    assert bool(torch.isnan(b.loss)) == lost and np.isnan(d[7, 66]) == np.isnan(d[30, 2]) == lost
+    others = np.delete(np.arange(S), [7, 30])
+    # (64 + far) U s (g + the mean of g) as in balance_case, with far below 20 for normal values and s below 1
+    near(d[others], want[others], 168 * U * E / (3 * S * S) * np.bincount(idx.ravel(), minlength=E).max(), "d_logits")
+    if lost:
+        assert np.isnan(d[30]).all()
+
+
 def test_balance_counts_are_the_layouts(moe):
     rng = np.random.default_rng(3)
     idx = to_dev(routing(rng, 600, 32, 4, "odd"))
