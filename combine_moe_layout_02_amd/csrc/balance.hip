@@ -2,11 +2,12 @@
 //
 // A wave takes a token: lane l holds experts l, l + 64, ... of it, so that its scores are two reductions over the wave's
 // lanes, and their sums over tokens stay in its registers. The exponentials and the reductions' chains bound it, and launches:
-// 8192 tokens of 256 experts (8.4 MB) take 12.9 us forward, 6.0 in the parts and 7 in the one workgroup that joins 256 of
-// them, and 6.5 back, 128 tokens of 16 experts (one part) 7.4 and 4.6. Parts of 128 tokens (64 of them) took 20 + 4.6, of 64
-// 8.0 + 6.4; with the library's expf, divisions and shuffles 13.6 + 20. The gradient with 1024 workgroups the same, 512
-// 7.4, 256 10.8.
+// 8192 tokens of 256 experts (8.4 MB) take 9.9 us forward, 6 in the parts and 4 in the joining kernel, and 6.4 back, 65536 of
+// them 23.2 and 27.6, 128 tokens of 16 experts (one part) 6.9 and 4.6. Parts of 128 tokens (64 of them) took 20, of 64
+// 8; with loads and stores that a test keeps in the row, not the buffer's end, 65536 tokens took 2.8 more; with the library's expf,
+// divisions and shuffles 13.6 + 20. The gradient with 1024 workgroups the same, 512 7.4, 256 10.8.
 
+#include "pack_rows.h"
 #include "wave_ops.h"
 
 namespace moe {
@@ -17,7 +18,6 @@ typedef __bf16 bf16_t;
 constexpr int kPartThreads = 1024, kPartWaves = kPartThreads / 64;
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kFinishThreads = 1024;
-constexpr int kFinishSlices = 32;
 constexpr int kBackwardGrid = 2048;
 
 // exp(x) for x <= 0 to 2 ulp, from the hardware's exp2 of x * log2(e) and the rest of that product; 0 from -200 down, NaN of a
@@ -57,17 +57,26 @@ __device__ inline void scores_of(const float (&l)[N], float (&s)[N], float (&tur
     for (int i = 0; i < N; ++i) s[i] = l[i] == -__builtin_inff() ? 0.0f : s[i] * each;
 }
 
-// A token's logits (-inf past E) and entries (-1 past K) in a wave's lanes; nothing of tokens past the end.
+// A token's logits (-inf past E) and entries (-1 past K) in a wave's lanes; nothing of tokens past the end. Lanes past a row's
+// end read nothing: the buffer ends there.
 template <int N, class T>
 struct Token {
     float l[N];
     int id;
     __device__ void load(const uint8_t *__restrict__ logits, int64_t stride, const int32_t *__restrict__ topk, int t, int end, int K, int E) {
-        const int lane = threadIdx.x & 63;
-        const T *row = reinterpret_cast<const T *>(logits + t * stride);
+        const int lane = threadIdx.x & 63, bytes = t < end ? E * (int)sizeof(T) : 0;
+        const __amdgpu_buffer_rsrc_t row = rows::rsrc(logits + t * stride, bytes);
 #pragma unroll
-        for (int i = 0; i < N; ++i) l[i] = t < end && lane + 64 * i < E ? (float)row[lane + 64 * i] : -__builtin_inff();
-        id = t < end && lane < K ? topk[(int64_t)t * K + lane] : -1;
+        for (int i = 0; i < N; ++i) {
+            const int at = (lane + 64 * i) * (int)sizeof(T);
+            float v;
+            if constexpr (sizeof(T) == 4) v = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row, at, 0, 0));
+            else v = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(row, at, 0, 0) << 16);
+            l[i] = at < bytes ? v : -__builtin_inff();
+        }
+        const int entries = t < end ? K : 0;
+        const int e = __builtin_amdgcn_raw_buffer_load_b32(rows::rsrc(topk + (int64_t)t * K, entries * 4), lane * 4, 0, 0);
+        id = lane < entries ? e : -1;
     }
 };
 
@@ -82,11 +91,12 @@ template <int N, int SCORE, class T>
 __global__ __launch_bounds__(kPartThreads) void balance_parts_kernel(
     const uint8_t *__restrict__ logits, int64_t stride, const int32_t *__restrict__ topk, int S, int K, int E,
     int per, float coef, float *__restrict__ loss, int32_t *__restrict__ counts, int32_t *__restrict__ tokens,
-    float *__restrict__ part_sums, uint16_t *__restrict__ part_counts, int32_t *__restrict__ part_tokens) {
+    float *__restrict__ part_sums, uint16_t *__restrict__ part_counts, int32_t *__restrict__ part_tokens,
+    BalanceShares *__restrict__ shares) {
     __shared__ int32_t count[64 * N];
     __shared__ float sums[kPartWaves][64 * N];
     __shared__ int32_t live[kPartWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     for (int e = tid; e < 64 * N; e += kPartThreads) count[e] = 0;
     __syncthreads();
     float acc[N];
@@ -128,6 +138,7 @@ __global__ __launch_bounds__(kPartThreads) void balance_parts_kernel(
             part_counts[blockIdx.x * wide + e] = (uint16_t)count[e];  // 256 tokens of 16 entries at most
         }
         if (tid == 0) part_tokens[blockIdx.x] = all;
+        if (tid == 0 && blockIdx.x == 0) shares->done = 0;  // for the joining kernel
         return;
     }
     if (wave > 0) return;
@@ -142,61 +153,70 @@ __global__ __launch_bounds__(kPartThreads) void balance_parts_kernel(
     if (lane == 0) *loss = value, *tokens = all;
 }
 
-// One workgroup: four experts a thread, `groups` threads (E / 4 rounded up to a power of two) to a part's row, as many parts
-// at once as there are threads for them, 32 at most; then the threads' sums in order.
+// Workgroup w joins the parts' sums and counts of experts [64 w, 64 w + 64): 16 lanes four experts each of every 64th part, four
+// such rows a wave, then the waves' in order. Each leaves its share of the loss, and the last to come adds the shares in
+// their order, whichever it is. (One workgroup for all experts read 393 KB, of 256 parts of 256 experts, at 33 bytes a cycle: 7 us.)
 __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(
     const float *__restrict__ part_sums, const uint16_t *__restrict__ part_counts,
-    const int32_t *__restrict__ part_tokens, int parts, int E, int groups, float coef, float *__restrict__ loss,
-    int32_t *__restrict__ counts, int32_t *__restrict__ tokens) {
-    __shared__ float sums[4 * kFinishThreads];
-    __shared__ int32_t count[4 * kFinishThreads];
-    __shared__ double share[kFinishThreads / 64];
-    __shared__ int32_t entries[kFinishThreads / 64], lives[kFinishThreads / 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wide = (E + 3) / 4 * 4, e = (tid & (groups - 1)) * 4, slice = tid / groups, slices = min(kFinishThreads / groups, kFinishSlices);
+    const int32_t *__restrict__ part_tokens, int parts, int E, float coef, BalanceShares *__restrict__ shares,
+    float *__restrict__ loss, int32_t *__restrict__ counts, int32_t *__restrict__ tokens) {
+    constexpr int kFinishWaves = kFinishThreads / 64;
+    __shared__ __align__(16) float sums[kFinishWaves][64];
+    __shared__ __align__(16) int32_t count[kFinishWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wide = (E + 3) / 4 * 4, e0 = blockIdx.x * 64, mine = (lane & 15) * 4, e = e0 + mine;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int c[4] = {0, 0, 0, 0}, live = 0;
-    if (e < wide && slice < slices) {
-#pragma unroll 16
-        for (int p = slice; p < parts; p += slices) {
-            const float4 f = *reinterpret_cast<const float4 *>(part_sums + p * wide + e);
-            const ushort4 n = *reinterpret_cast<const ushort4 *>(part_counts + p * wide + e);
-            s[0] += f.x, s[1] += f.y, s[2] += f.z, s[3] += f.w;
-            c[0] += n.x, c[1] += n.y, c[2] += n.z, c[3] += n.w;
-        }
-    }
-    if (tid < parts) live = part_tokens[tid];
-    if (slice < slices) {
+    // parts past the last read as zero, where the buffers end
+    const __amdgpu_buffer_rsrc_t sum_src = rows::rsrc(part_sums, parts * wide * 4), count_src = rows::rsrc(part_counts, parts * wide * 2);
+#pragma unroll
+    for (int k = 0; k < kBalanceParts / (4 * kFinishWaves); ++k) {
+        const int p = wave * 4 + (lane >> 4) + k * 4 * kFinishWaves, at = e < wide ? p * wide + e : 1 << 28;
+        const rows::u32x4 f = rows::load16(sum_src, at * 4);
+        const auto n = __builtin_amdgcn_raw_buffer_load_b64(count_src, at * 2, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            sums[slice * 4 * groups + e + i] = s[i];
-            count[slice * 4 * groups + e + i] = c[i];
+            s[i] += __uint_as_float(f[i]);
+            c[i] += (int)(n[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
         }
+    }
+    if (wave == 0)
+        for (int p = lane; p < parts; p += 64) live += part_tokens[p];
+    const auto add = [](auto a, auto b) { return a + b; };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s[i] = wave::join<false>(wave::join<true>(s[i], add), add);
+        c[i] = wave::join<false>(wave::join<true>(c[i], add), add);
+    }
+    if (lane < 16) {
+        *reinterpret_cast<float4 *>(&sums[wave][mine]) = float4{s[0], s[1], s[2], s[3]};
+        *reinterpret_cast<int4 *>(&count[wave][mine]) = int4{c[0], c[1], c[2], c[3]};
     }
     __syncthreads();
-    double part = 0.0;
+    if (wave > 0) return;
+    float sum = 0.0f;
     int all = 0;
-    if (tid < E) {
-        float sum = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < slices; ++k) {
-            sum += sums[k * 4 * groups + tid];
-            all += count[k * 4 * groups + tid];
-        }
-        part = (double)all * (double)sum;
-        counts[tid] = all;
-    }
-    part = wave::sum(part);
+#pragma unroll
+    for (int w = 0; w < kFinishWaves; ++w) sum += sums[w][lane], all += count[w][lane];
+    if (e0 + lane < E) counts[e0 + lane] = all;
+    double part = wave::sum((double)all * (double)sum);
     all = wave::sum(all);
     live = wave::sum(live);
-    if (lane == 0) share[wave] = part, entries[wave] = all, lives[wave] = live;
-    __syncthreads();
-    if (tid > 0) return;
-    int n = 0, live_all = 0;
-    part = 0.0;
-    for (int w = 0; w < kFinishThreads / 64; ++w) part += share[w], n += entries[w], live_all += lives[w];
-    *loss = loss_of(part, n, live_all, E, coef);
-    *tokens = live_all;
+    if (lane > 0) return;
+    if (gridDim.x > 1) {
+        __hip_atomic_store(&shares->share[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&shares->entries[blockIdx.x], all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const int before = __hip_atomic_fetch_add(&shares->done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        if (before != (int)gridDim.x - 1) return;
+        part = 0.0;
+        all = 0;
+        for (int w = 0; w < (int)gridDim.x; ++w) {
+            part += __hip_atomic_load(&shares->share[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            all += __hip_atomic_load(&shares->entries[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    *loss = loss_of(part, all, live, E, coef);
+    *tokens = live;
 }
 
 // A wave a token, as above. n[e] counts from the mean, which takes nothing from the gradient (the scores' sum is 1), and
@@ -217,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(
     const int mean = sum / E;
     const double all = (double)sum * (double)*tokens;
     const float each = all > 0.0 ? (float)((double)coef * E / all) * *d_loss : 0.0f;
-    int t = blockIdx.x * kWaves + (threadIdx.x >> 6);
+    int t = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Token<N, T> next;
     next.load(logits, stride, topk, t, S, K, E);
     for (; t < S; t += step) {
@@ -233,13 +253,15 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(
             dot += g[i] * s[i];
         }
         dot = wave::sum(dot);
+        const __amdgpu_buffer_rsrc_t dst = rows::rsrc(d_logits + (int64_t)t * E, E * (int)sizeof(T));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int e = lane + 64 * i;
-            if (e >= E) continue;
             float d = each * (s[i] * (g[i] - dot));
             if (SCORE == MOE_SCORE_SIGMOID) d *= turn[i];
-            d_logits[(int64_t)t * E + e] = (T)(lives ? d : 0.0f);
+            d = lives ? d : 0.0f;
+            const int at = (lane + 64 * i) * (int)sizeof(T);
+            if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(d), dst, at, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)d), dst, at, 0, 0);
         }
     }
 }
@@ -270,20 +292,19 @@ hipError_t launch_balance_loss(const void *logits, int64_t logits_stride_bytes, 
                                hipStream_t stream) {
     const int most = balance_parts(S), per = (S + most - 1) / most, parts = (S + per - 1) / per;
     const int64_t each = (int64_t)most * ((E + 3) / 4 * 4);
-    float *sums = static_cast<float *>(workspace);
-    uint16_t *counts = parts > 1 ? reinterpret_cast<uint16_t *>(sums + each) : nullptr;
-    int32_t *tokens = parts > 1 ? reinterpret_cast<int32_t *>(counts + each) : nullptr;
+    BalanceShares *const shares = static_cast<BalanceShares *>(workspace);
+    float *const sums = parts > 1 ? reinterpret_cast<float *>(shares + 1) : nullptr;
+    uint16_t *const counts = parts > 1 ? reinterpret_cast<uint16_t *>(sums + each) : nullptr;
+    int32_t *const tokens = parts > 1 ? reinterpret_cast<int32_t *>(counts + each) : nullptr;
     dispatch(E, logits_type, score, [&](auto n, auto s, auto element) {
         hipLaunchKernelGGL((balance_parts_kernel<decltype(n)::value, decltype(s)::value, decltype(element)>), dim3(parts),
                            dim3(kPartThreads), 0, stream, static_cast<const uint8_t *>(logits), logits_stride_bytes, topk_idx,
-                           S, K, E, per, coef, loss, num_tokens_per_expert, num_tokens, sums, counts, tokens);
+                           S, K, E, per, coef, loss, num_tokens_per_expert, num_tokens, sums, counts, tokens, shares);
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || parts == 1) return e;
-    int groups = 1;
-    while (4 * groups < E) groups *= 2;
-    hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(kFinishThreads), 0, stream, sums, counts, tokens, parts, E,
-                       groups, coef, loss, num_tokens_per_expert, num_tokens);
+    hipLaunchKernelGGL(balance_finish_kernel, dim3((E + 63) / 64), dim3(kFinishThreads), 0, stream, sums, counts, tokens,
+                       parts, E, coef, shares, loss, num_tokens_per_expert, num_tokens);
     return hipGetLastError();
 }
 

@@ -293,11 +293,17 @@ hipError_t launch_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, con
                                     float *d_weight, void *workspace, hipStream_t stream);
 
 // Parts that the balance loss splits its tokens into, one compute unit each. Each has the experts' sums of scores (fp32) and
-// counts (16 bits) in the workspace, E rounded up to 4 of them, behind them every part's number of tokens; a single part
-// needs none, nor a second kernel.
+// counts (16 bits) in the workspace, E rounded up to 4 of them, behind them every part's number of tokens and before them
+// the joining workgroups' shares; a single part needs none, nor a second kernel.
 constexpr int kBalanceAlone = 128;  // tokens that a single part takes
 constexpr int kBalanceTokens = 32;  // tokens of several parts at least
 constexpr int kBalanceParts = 256;  // a part's counts stay below 2^16: MOE_MAX_TOKENS / 256 * MOE_MAX_K = 2^12
+struct alignas(16) BalanceShares {
+    double share[MOE_MAX_EXPERTS / 64];
+    int32_t entries[MOE_MAX_EXPERTS / 64];
+    int32_t done;  // workgroups that have left theirs
+};
+
 inline int balance_parts(int32_t S) {
     if (S <= kBalanceAlone) return 1;
     const int parts = (S + kBalanceTokens - 1) / kBalanceTokens;
@@ -306,7 +312,7 @@ inline int balance_parts(int32_t S) {
 
 inline int64_t balance_workspace(int32_t S, int32_t E) {
     const int64_t parts = balance_parts(S);
-    return parts > 1 ? parts * ((E + 3) / 4 * 4 * 6 + 4) : 0;
+    return parts > 1 ? (int64_t)sizeof(BalanceShares) + parts * ((E + 3) / 4 * 4 * 6 + 4) : 0;
 }
 
 hipError_t launch_balance_loss(const void *logits, int64_t logits_stride_bytes, int32_t logits_type,
