@@ -4,6 +4,8 @@
 // l % 16, k-block l / 16, of either operand. The weights are the first operand, so that a lane's four results are
 // neighbouring outputs of one row. Sums are whole numbers below 2^31 (H * 128 * 128 <= 2^28), the same in any order.
 
+#include <algorithm>
+
 #include "product_rows.h"
 
 namespace moe {
@@ -475,8 +477,17 @@ hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64
     // Where the tiles are no more than the compute units, all of a tile's time is its way through one, and small
     // tiles with more pairs under way shorten it; few_rows, whose waves share H, is ahead while its workgroups read
     // no more than 15360 rows. With more tiles the two pairs' kernels, which start a tile while they end another,
-    // are ahead, the larger the more rows there are to share the weights: 128 x 128 from 64 rows a group and 300 tiles,
-    // 256 x 256 from 160 rows and 192 tiles (its last round goes out in pieces).
+    // are ahead, the larger the more rows there are to share the weights: 128 x 128 from 48 rows a group and 300 tiles,
+    // 256 x 256 from 160 rows and 192 tiles (its last round goes out in pieces). But up to 24 rows a group 64 x 64 with four pairs
+    // gets the bytes sooner, as its rounds are shorter: 85 rows on 32 groups, 6032 -> 2192 gated, 85.9 and 121 with 64 x 128 and
+    // two, 1019 on 61, 5488 -> 1074 gated, 86.8 and 113, 512 on 32, 7168 -> 4096 gated, 161 and 158.
+    //
+    // Four pairs want rows of 12 pairs: 3001 rows on 16 groups, 1040 -> 1000, take 15.9 with 128 x 128 and four, 16.1 with 64 x 128 and
+    // two from memory, 15.4 and 12.0 from the caches; 43 rows on 64 groups, 1520 -> 3494 gated, 38.5 with 64 x 64 and four, 38.4.
+    //
+    // How many tiles uneven groups have is expected, from their mean: a half more than their rows would fill, one at least. Over 226
+    // products with random sizes (1 to 32768 rows, 1 to 64 groups) the rule's choice took 1.9% longer than the best of these
+    // kernels (geometric mean), and 7.1% with each group's tiles counted at five quarters of the mean.
     const int64_t hit = a_rows < G ? a_rows : G, mean = (a_rows + hit - 1) / hit;
     const int64_t most = hit > 1 ? mean + mean / 4 : mean;
     const auto tiles_of = [&](int tm, int tn) {
@@ -486,11 +497,16 @@ hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64
     if (tiles_of(16, 32) * ((most < 16 ? most : 16) + 32) <= 320 * 48) return few_rows(p);  // rows that its workgroups read
     if (tiles_of(32, 64) <= (most <= 32 ? 448 : kUnits)) return tiles<32, 64, 2, 1, 4>(p);  // two at once on a unit, and room for a fuller group
     if (tiles_of(64, 64) <= kUnits) return tiles<64, 64, 4, 1, 4>(p);
-    if (tiles_of(64, 128) <= kUnits) return tiles<64, 128, 2, 2, 4>(p);
-    if (mean >= 160 && tiles_of(256, 256) >= 192) return tiles<256, 256, 2, 4, 2>(p);
-    // short rows do not fill four pairs: 16x188 above takes 15.9 and 16.1 from memory, 15.4 and 12.0 from the caches
-    if (H >= 2048 && tiles_of(128, 128) <= kUnits) return tiles<128, 128, 2, 2, 4>(p);
-    if (mean >= 64 && tiles_of(128, 128) >= 300) return tiles<128, 128, 2, 2, 2>(p);
+    const auto expected = [&](int tm, int tn) {
+        const int outs = gated ? tn / 2 : tn;
+        const int64_t halves = hit > 1 ? std::max<int64_t>(2 * tm, 2 * mean + tm) : (mean + tm - 1) / tm * 2 * tm;  // of tm rows a group, times tm
+        return hit * ((width + outs - 1) / outs) * halves / (2 * tm);
+    };
+    if (expected(64, 128) <= kUnits) return tiles<64, 128, 2, 2, 4>(p);
+    if (mean <= 24 && H >= 1536) return tiles<64, 64, 4, 1, 4>(p);
+    if (mean >= 160 && expected(256, 256) >= 192) return tiles<256, 256, 2, 4, 2>(p);
+    if (H >= 1536 && expected(128, 128) <= kUnits) return tiles<128, 128, 2, 2, 4>(p);
+    if (mean >= 48 && expected(128, 128) >= 300) return tiles<128, 128, 2, 2, 2>(p);
     return tiles<64, 128, 2, 2, 2>(p);
 }
 

@@ -230,9 +230,10 @@ def test_product_strides_and_odd_widths(moe, R, G, H, O, gap, epilogue):
 
 
 @pytest.mark.parametrize("R,G,H,O,epilogue,gap", [
-    (12288, 1, 80, 1024, PLAIN, 0), (9000, 3, 144, 1030, PLAIN, 0), (5000, 4, 208, 4096, GATED, 8),           # tiles of 256 x 256
-    (2500, 7, 3088, 600, PLAIN, 0), (512, 4, 2064, 4096, GATED, 0), (700, 1, 2096, 5000, PLAIN, 3),          # 128 x 128, one a unit
-    (2000, 16, 144, 2050, PLAIN, 0), (1500, 20, 1040, 2048, GATED, 4),                                       # 128 x 128 in turns
+    (12288, 1, 80, 1024, PLAIN, 0), (9000, 3, 144, 1606, PLAIN, 0), (5000, 4, 208, 4096, GATED, 8),           # tiles of 256 x 256
+    (900, 3, 2064, 2100, PLAIN, 0), (512, 4, 2064, 4096, GATED, 0), (700, 1, 2096, 5000, PLAIN, 3),          # 128 x 128, one a unit
+    (9000, 3, 144, 1030, PLAIN, 0), (2000, 16, 144, 2050, PLAIN, 0), (1500, 20, 1040, 2048, GATED, 4),       # 128 x 128 in turns
+    (64, 20, 1552, 1800, PLAIN, 0), (300, 60, 1552, 1100, GATED, 6), (2500, 7, 3088, 600, PLAIN, 0),         # 64 x 64, 64 x 128, one each
     (1024, 32, 272, 4096, PLAIN, 0), (3001, 16, 1040, 1000, PLAIN, 0), (900, 40, 528, 4100, GATED, 0),       # 64 x 128 in turns
     (600, 2, 96, 2000, PLAIN, 0), (250, 3, 1088, 1100, GATED, 2), (40, 5, 2000, 2222, PLAIN, 0),            # smaller ones
     (600, 512, 64, 64, GATED, 0), (9000, 512, 96, 320, PLAIN, 0)])                                           # the most groups
