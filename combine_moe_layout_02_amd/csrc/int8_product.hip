@@ -474,39 +474,42 @@ hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64
     //   64 x 128, two        32.5     52.1    28.2     65.4    70.3    16.1    30.7    42.5   30.6    21.0    7.6
     //   128 x 128, two       30.2     42.4    25.7     58.3    62.1    16.3    32.9    48.3   27.6    19.6    8.1
     //   256 x 256, two       24.1     35.2    23.1     61.1    59.9                           24.8    18.4    11.3
-    // Where the tiles are no more than the compute units, all of a tile's time is its way through one, and small
-    // tiles with more pairs under way shorten it; few_rows, whose waves share H, is ahead while its workgroups read
-    // no more than 15360 rows. With more tiles the two pairs' kernels, which start a tile while they end another,
-    // are ahead, the larger the more rows there are to share the weights: 128 x 128 from 48 rows a group and 300 tiles,
-    // 256 x 256 from 160 rows and 192 tiles (its last round goes out in pieces). But up to 24 rows a group 64 x 64 with four pairs
-    // gets the bytes sooner, as its rounds are shorter: 85 rows on 32 groups, 6032 -> 2192 gated, 85.9 and 121 with 64 x 128 and
-    // two, 1019 on 61, 5488 -> 1074 gated, 86.8 and 113, 512 on 32, 7168 -> 4096 gated, 161 and 158.
+    // Where the tiles are no more than the compute units, all of a tile's time is its way through one, and small tiles
+    // with more pairs under way shorten it; few_rows, whose waves share H, is ahead while its workgroups read no more
+    // than 12288 rows. Its steps of 64 bytes of a row are half lines, or parts of two, which costs it where they come
+    // from memory: 291 rows on 19 groups, 6400 -> 222, 11.9 and 16.3 with 32 x 64; 134 on 30, 6256 -> 300, 26.5 and
+    // 19.0, 86 on one, 6560 -> 1134 (7 MB of weights), 12.1 and 16.6. With more tiles the two pairs' kernels, which
+    // start a tile while they end another, are ahead, the larger the more rows there are to share the weights: 128 x 128
+    // from 48 rows a group and, for short rows, 300 tiles (15766 rows on 32 groups, 7104 -> 148 gated, 278 of them: 71
+    // and 90 with 64 x 128), 256 x 256 from 160 rows and 192 tiles (its last round goes out in pieces). But up to 24
+    // rows a group 64 x 64 with four pairs gets the bytes sooner, as its rounds are shorter: 85 rows on 32 groups, 6032
+    // -> 2192 gated, 85.9 and 121 with 64 x 128 and two, 1019 on 61, 5488 -> 1074 gated, 86.8 and 113, 512 on 32, 7168
+    // -> 4096 gated, 161 and 158.
     //
-    // Four pairs want rows of 12 pairs: 3001 rows on 16 groups, 1040 -> 1000, take 15.9 with 128 x 128 and four, 16.1 with 64 x 128 and
-    // two from memory, 15.4 and 12.0 from the caches; 43 rows on 64 groups, 1520 -> 3494 gated, 38.5 with 64 x 64 and four, 38.4.
+    // Four pairs want rows of 12 pairs: 3001 rows on 16 groups, 1040 -> 1000, take 15.9 with 128 x 128 and four, 16.1
+    // with 64 x 128 and two from memory, 15.4 and 12.0 from the caches; 43 rows on 64 groups, 1520 -> 3494 gated, 38.5
+    // with 64 x 64 and four, 38.4.
     //
-    // How many tiles uneven groups have is expected, from their mean: a half more than their rows would fill, one at least. Over 226
-    // products with random sizes (1 to 32768 rows, 1 to 64 groups) the rule's choice took 1.9% longer than the best of these
-    // kernels (geometric mean), and 7.1% with each group's tiles counted at five quarters of the mean.
+    // How many tiles uneven groups have is expected, from their mean: a half more than their rows would fill, one at
+    // least. Over 514 products of random sizes (1 to 32768 rows on 1 to 64 groups, 4 MB of weights at least) the rule's
+    // choice takes 1.7% longer than the best of these kernels (geometric mean); with each group's tiles counted at five
+    // quarters of the mean it took 5.7.
     const int64_t hit = a_rows < G ? a_rows : G, mean = (a_rows + hit - 1) / hit;
-    const int64_t most = hit > 1 ? mean + mean / 4 : mean;
-    const auto tiles_of = [&](int tm, int tn) {
-        const int outs = gated ? tn / 2 : tn;
-        return hit * ((most + tm - 1) / tm) * ((width + outs - 1) / outs);
-    };
-    if (tiles_of(16, 32) * ((most < 16 ? most : 16) + 32) <= 320 * 48) return few_rows(p);  // rows that its workgroups read
-    if (tiles_of(32, 64) <= (most <= 32 ? 448 : kUnits)) return tiles<32, 64, 2, 1, 4>(p);  // two at once on a unit, and room for a fuller group
-    if (tiles_of(64, 64) <= kUnits) return tiles<64, 64, 4, 1, 4>(p);
     const auto expected = [&](int tm, int tn) {
         const int outs = gated ? tn / 2 : tn;
         const int64_t halves = hit > 1 ? std::max<int64_t>(2 * tm, 2 * mean + tm) : (mean + tm - 1) / tm * 2 * tm;  // of tm rows a group, times tm
         return hit * ((width + outs - 1) / outs) * halves / (2 * tm);
     };
+    const int64_t reads = expected(16, 32) * (std::min<int64_t>(mean, 16) + 32);  // rows that few_rows' workgroups read
+    const bool cached = hit * O * H <= 12 << 20 || reads * H <= 56 << 20;
+    if (reads <= 12288 && (H % 64 == 0 || cached)) return few_rows(p);
+    if (expected(32, 64) <= (mean <= 32 ? 2 * kUnits : kUnits)) return tiles<32, 64, 2, 1, 4>(p);  // two at once on a unit
+    if (expected(64, 64) <= kUnits) return tiles<64, 64, 4, 1, 4>(p);
     if (expected(64, 128) <= kUnits) return tiles<64, 128, 2, 2, 4>(p);
     if (mean <= 24 && H >= 1536) return tiles<64, 64, 4, 1, 4>(p);
     if (mean >= 160 && expected(256, 256) >= 192) return tiles<256, 256, 2, 4, 2>(p);
     if (H >= 1536 && expected(128, 128) <= kUnits) return tiles<128, 128, 2, 2, 4>(p);
-    if (mean >= 48 && expected(128, 128) >= 300) return tiles<128, 128, 2, 2, 2>(p);
+    if (mean >= 48 && (H >= 1536 || expected(128, 128) >= 300)) return tiles<128, 128, 2, 2, 2>(p);
     return tiles<64, 128, 2, 2, 2>(p);
 }
 
