@@ -533,6 +533,113 @@ def test_balance_gradient_is_the_losss_difference(moe, score):
     assert abs(quotient - inner) <= off + 2 * 412 * U * max(losses) / (2 * h) + 100 * U * float(np.abs(d * v).sum())
 
 
+# ---------------------------------------------------------------- workspaces and ends of buffers
+
+
+def inside(shape, dtype, front=64, back=64):
+    """A poisoned device buffer and the part of it, 64 bytes aligned, that a call gets."""
+    n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+    whole = poison(front + n + back, torch.uint8)
+    return whole, whole[front : front + n].view(dtype).view(shape)
+
+
+def untouched(whole, front=64, back=64):
+    return poisoned(whole[:front]) and poisoned(whole[len(whole) - back :])
+
+
+@pytest.mark.parametrize("S,H", [(1, 16), (2, 528), (300, 2064), (1531, 1040), (700, 16384)])
+def test_norm_gradient_workspace(moe, S, H):
+    """Exactly the bytes that are asked for, whatever they hold, and none around them or around the outputs."""
+    rng = np.random.default_rng(S)
+    dy, h, w = bf16_dev(spread_rows(rng, S, H)), bf16_dev(spread_rows(rng, S, H)), torch.ones(H, device=DEV)
+    note("workspace", S, H)
+    want = moe.moe_rms_norm_backward(dy, h, w)
+    need = moe.moe_rms_norm_backward_workspace_bytes(S, H)
+    ws, dx, dw = inside((need,), torch.uint8), inside((S, H), torch.bfloat16), inside((H,), torch.float32)
+    for _ in range(2):  # the second time over the first one's parts
+        moe.moe_rms_norm_backward(dy, h, w, dx=dx[1], d_weight=dw[1], workspace=ws[1])
+        assert torch.equal(dx[1], want[0]) and torch.equal(dw[1], want[1])
+    assert all(untouched(b[0]) for b in (ws, dx, dw))
+    if need:
+        with pytest.raises(ValueError):
+            moe.moe_rms_norm_backward(dy, h, w, workspace=ws[1][:-16])
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("S,E,K", [(1, 1, 1), (128, 63, 3), (129, 5, 2), (700, 65, 4), (4001, 130, 8), (9000, 511, 6)])
+def test_balance_workspace(moe, S, E, K, kind):
+    rng = np.random.default_rng(S)
+    idx, l = to_dev(routing(rng, S, E, K, "padded")), torch.randn((S, E), device=DEV).to(kind)
+    note("balance workspace", S, E, K)
+    want = moe.moe_balance_loss(l, idx, 0.1)
+    one = torch.ones(1, device=DEV)
+    want_d = moe.moe_balance_loss_backward(one, l, idx, want.num_tokens_per_expert, want.num_tokens, 0.1)
+    need = moe.moe_balance_loss_workspace_bytes(S, E)
+    bufs = [inside(s, d) for s, d in (((1,), torch.float32), ((E,), torch.int32), ((1,), torch.int32), ((S, E), kind), ((need,), torch.uint8))]
+    loss, counts, tokens, d, ws = (b[1] for b in bufs)
+    for _ in range(3):
+        moe.moe_balance_loss(l, idx, 0.1, out=(loss, counts, tokens), workspace=ws)
+        moe.moe_balance_loss_backward(one, l, idx, counts, tokens, 0.1, d_logits=d)
+        assert torch.equal(loss, want.loss) and torch.equal(counts, want.num_tokens_per_expert) and torch.equal(tokens, want.num_tokens)
+        assert torch.equal(d, want_d)
+    assert all(untouched(b[0]) for b in bufs)
+    if need:
+        with pytest.raises(ValueError):
+            moe.moe_balance_loss(l, idx, 0.1, workspace=ws[:-16])
+
+
+@pytest.mark.parametrize("quant", [E4M3, INT8])
+@pytest.mark.parametrize("S,H", [(1, 16), (3, 1040), (258, 7184)])
+def test_dense_outputs_end_where_they_end(moe, S, H, quant):
+    rng = np.random.default_rng(H)
+    x, w = bf16_dev(spread_rows(rng, S, H)), torch.ones(H, device=DEV)
+    want = moe.moe_rms_norm(x, w, residual=x, quant=quant, out=poison((S, H), torch.bfloat16))
+    bufs = [inside(s, d) for s, d in (((S, H), torch.bfloat16), ((S, H), torch.bfloat16), ((S, H), torch.uint8), ((S,), torch.float32))]
+    total, out, codes, scales = (b[1] for b in bufs)
+    moe.moe_rms_norm(x, w, residual=x, quant=quant, sum=total, out=out, rows8=(codes, scales))
+    assert torch.equal(total, want.sum) and torch.equal(out, want.out)
+    assert torch.equal(codes, want.rows8.codes) and torch.equal(scales, want.rows8.scales)
+    rows = moe.moe_row_quantize(x, quant)
+    moe.moe_row_quantize(x, quant, out=(codes, scales))
+    assert torch.equal(codes, rows.codes) and torch.equal(scales, rows.scales)
+    back = moe.moe_row_dequantize(rows, quant)
+    moe.moe_row_dequantize(rows, quant, out=total)
+    assert torch.equal(total, back) and all(untouched(b[0]) for b in bufs)
+
+
+def test_shared_workspace_in_order(moe):
+    """Calls one behind the other may share a workspace, in a graph as well, and two graphs of one stream too."""
+    rng = np.random.default_rng(5)
+    S, E, K, H = 900, 200, 4, 528
+    idx = [to_dev(routing(rng, S, E, K, f)) for f in ("", "padded")]
+    l = [torch.randn((S, E), device=DEV) for _ in idx]
+    dy, h, w = bf16_dev(spread_rows(rng, S, H)), bf16_dev(spread_rows(rng, S, H)), torch.ones(H, device=DEV)
+    ws = poison(max(moe.moe_balance_loss_workspace_bytes(S, E), moe.moe_rms_norm_backward_workspace_bytes(S, H)), torch.uint8)
+
+    def both():
+        a = [moe.moe_balance_loss(x, t, 1.0, workspace=ws) for x, t in zip(l, idx)]
+        return [v for b in a for v in b] + list(moe.moe_rms_norm_backward(dy, h, w, workspace=ws))
+
+    want = both()
+    alone = [v for x, t in zip(l, idx) for v in moe.moe_balance_loss(x, t, 1.0)] + list(moe.moe_rms_norm_backward(dy, h, w))
+    assert all(torch.equal(a, b) for a, b in zip(want, alone))
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = both()
+        graphs.append((g, out))
+    for _ in range(3):
+        for g, out in graphs:
+            ws.fill_(POISON)
+            for t in l:
+                t.normal_()
+            eager = both()
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, eager))
+
+
 # ---------------------------------------------------------------- together, streams, graphs
 
 
