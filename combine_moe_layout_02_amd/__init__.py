@@ -1233,18 +1233,28 @@ def _some_rows(t, name, n, H, dev):
     return _rows_arg(t, name, H, dev)[:2]
 
 
+def _row_matrix(t, name):
+    """Device, shape, pointer and row stride in bytes of bf16 rows [R, H], of which there may be none."""
+    if isinstance(t, _Tensor) and t.dtype is _bf16 and t.is_contiguous():
+        dev, shape = t.get_device(), t.shape
+        if dev >= 0 and len(shape) == 2:
+            n, H = shape
+            return dev, n, H, t.data_ptr(), 2 * H
+    dev, n, H = _matrix(t, name, _bf16)
+    return dev, n, H, *_some_rows(t, name, n, H, dev)
+
+
 def moe_row_quantize(rows, quant, num_rows=None, out=None, stream=None):
     """ScaledRows of bf16 rows [R, H] (any row stride) in MOE_QUANT_INT8_DYN or MOE_QUANT_FP8_E4M3_DYN, as moe_dispatch
     computes them. num_rows: None, or the device count of rows to take (e.g. layout.expert_slot_base[E:]); the
     outputs' other rows keep their contents (undefined where they are allocated here)."""
-    dev, n, H = _matrix(rows, "rows", _bf16)
+    dev, n, H, ptr, stride = _row_matrix(rows, "rows")
     if out is None:
         out = _row8_empty(n, H, dev, stream)
         codes, scales = out[0].data_ptr(), out[1].data_ptr()
     else:
         codes, scales = _row8_args(out, "out", (n, H), dev)
     count = _count_arg(num_rows, dev)
-    ptr, stride = _some_rows(rows, "rows", n, H, dev)
     _launch(dev, stream, _lib.moe_row_quantize, ptr, stride, count, n, H, quant, codes, scales)
     return ScaledRows(*out)
 
@@ -1309,8 +1319,7 @@ def moe_rms_norm(x, weight, eps=1e-6, residual=None, quant=MOE_QUANT_NONE, out=N
     """The root-mean-square norm of bf16 rows x [S, H], or of x + residual, times weight (bf16 or fp32 [H]): bf16 rows,
     with a quant (MOE_QUANT_INT8_DYN, MOE_QUANT_FP8_E4M3_DYN) rows in 8 bits instead, and both where out is passed too.
     x, residual and sum may have any row stride; sum may be x or residual itself (an addition in place)."""
-    dev, n, H = _matrix(x, "x", _bf16)
-    ptr, stride = _some_rows(x, "x", n, H, dev)
+    dev, n, H, ptr, stride = _row_matrix(x, "x")
     res_ptr, res_stride, sum_ptr, sum_stride, out_ptr, codes, scales = None, 0, None, 0, None, None, None
     if residual is not None:
         res_ptr, res_stride = _some_rows(residual, "residual", n, H, dev)
@@ -1367,8 +1376,7 @@ def moe_rms_norm_backward(dy, sum, weight, eps=1e-6, d_sum=None, dx=None, d_weig
     of dy, the rows that the forward normed (its sum), weight and eps. d_sum: the gradient that reaches the sum on its
     other ways, added to dx. dy, sum and d_sum may have any row stride. workspace: a device buffer of at least
     moe_rms_norm_backward_workspace_bytes(S, H) bytes, or None to have one allocated."""
-    dev, n, H = _matrix(sum, "sum", _bf16)
-    ptr, stride = _some_rows(sum, "sum", n, H, dev)
+    dev, n, H, ptr, stride = _row_matrix(sum, "sum")
     dy_ptr, dy_stride = _some_rows(dy, "dy", n, H, dev)
     ds_ptr, ds_stride = (None, 0) if d_sum is None else _some_rows(d_sum, "d_sum", n, H, dev)
     w_ptr, kind = _weight_arg(weight, H, dev)
