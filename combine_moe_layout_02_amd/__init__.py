@@ -1451,7 +1451,8 @@ def moe_balance_loss(logits, topk_idx, coef, score=MOE_SCORE_SOFTMAX, out=None, 
 def moe_balance_loss_backward(d_loss, logits, topk_idx, num_tokens_per_expert, num_tokens, coef, score=MOE_SCORE_SOFTMAX,
                               d_logits=None, stream=None):
     """The balance loss's gradient d_logits ([S, E] of the logits' type) of d_loss (fp32 [1]), with the forward's
-    arguments and counts."""
+    arguments and counts; or with the sums of both num_tokens_per_expert and num_tokens over several GPUs, for the loss over
+    all their tokens."""
     dev, S, K, E, ptr, stride, kind, table = _router_args(logits, topk_idx)
     dl_ptr = _dense(d_loss, "d_loss", _fp32, (1,), dev)
     counts = _dense(num_tokens_per_expert, "num_tokens_per_expert", _int32, (E,), dev)

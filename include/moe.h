@@ -768,8 +768,9 @@ int moe_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *s
  *                 do not matter. Calls that may run at once need one each. May be NULL where that is 0.
  * Out: loss fp32 [1], num_tokens_per_expert int32 [E], num_tokens int32 [1] (T). Enqueues at most two kernels.
  * moe_balance_loss_backward
- * In:  d_loss fp32 [1] and the forward's arguments and counts, all DEVICE pointers. (Counts that are summed over
- *      several GPUs give the gradient of the loss over them, with num_tokens the local T.)
+ * In:  d_loss fp32 [1] and the forward's arguments and counts, all DEVICE pointers. Counts and num_tokens that are both
+ *      summed over several GPUs give each of them its tokens' part of the gradient of the loss over all the tokens: N and T
+ *      in the formula are those sums.
  * Out: d_logits   [S, E] of logits_type, dense. Enqueues one kernel. */
 typedef enum {
     MOE_SCORE_SOFTMAX = 0,

@@ -1,0 +1,42 @@
+"""GPU tests of the 8-bit layer's calls at their edges: the balance loss over several GPUs' tokens and at the ends of its
+factors' ranges.
+
+Tolerances, derived before the first run, are written at each test; u = 2^-24 is fp32's rounding. The oracle is numpy in
+64 bits.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from test_gpu_layer import DEV, U, moe, near, note, routing, to_dev, values  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- the balance loss
+
+
+@pytest.mark.parametrize("score", [0, 1])
+def test_gradient_of_the_loss_over_several_gpus(moe, score):  # noqa: F811
+    """A batch in three uneven parts, of which one is half padding, as three GPUs have them: with the sums of their counts and of
+    their numbers of tokens each part gets its rows of the whole batch's gradient. Tolerance: d_logits = c s (g - dot), (64 + far)
+    u c s (|g| + sum s |g|), with far below 20 for normal values and the bracket at most twice the largest |g|."""
+    rng = np.random.default_rng(20 + score)
+    S, E, K, coef = 700, 48, 4, 0.3
+    l = rng.standard_normal((S, E)).astype(np.float32)
+    idx = routing(rng, S, E, K, "")
+    idx[rng.random((S, K)) < 0.1] = -1
+    idx[100:160] = -1
+    counts, tokens, want = oracle.balance(l, idx, coef, score)[1:]
+    parts = [slice(0, 20), slice(20, 160), slice(160, S)]
+    logits, tables = [to_dev(l[p]) for p in parts], [to_dev(idx[p]) for p in parts]
+    own = [moe.moe_balance_loss(a, t, coef, score) for a, t in zip(logits, tables)]
+    all_counts = sum(b.num_tokens_per_expert for b in own)
+    all_tokens = sum(b.num_tokens for b in own)
+    assert np.array_equal(all_counts.cpu().numpy(), counts) and int(all_tokens) == tokens
+    one = torch.ones(1, device=DEV)
+    got = [values(moe.moe_balance_loss_backward(one, a, t, all_counts, all_tokens, coef, score)) for a, t in zip(logits, tables)]
+    largest = np.abs(counts - counts.sum() // E).max()
+    near(np.concatenate(got), want, 84 * U * coef * E / (counts.sum() * tokens) * 2 * largest, "d_logits")
