@@ -227,15 +227,16 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(
     const int32_t *__restrict__ topk, const int32_t *__restrict__ counts, const int32_t *__restrict__ tokens, int S,
     int K, int E, float coef, T *__restrict__ d_logits) {
     const int lane = threadIdx.x & 63, step = gridDim.x * kWaves;
-    int n[N], sum = 0;
+    int n[N];
+    double sum = 0.0;  // counts of many GPUs may pass 32 bits together
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         n[i] = lane + 64 * i < E ? counts[lane + 64 * i] : 0;
         sum += n[i];
     }
     sum = wave::sum(sum);
-    const int mean = sum / E;
-    const double all = (double)sum * (double)*tokens;
+    const int mean = (int)(sum / E);
+    const double all = sum * (double)*tokens;
     const float each = all > 0.0 ? (float)((double)coef * E / all) * *d_loss : 0.0f;
     int t = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Token<N, T> next;

@@ -40,3 +40,25 @@ def test_gradient_of_the_loss_over_several_gpus(moe, score):  # noqa: F811
     got = [values(moe.moe_balance_loss_backward(one, a, t, all_counts, all_tokens, coef, score)) for a, t in zip(logits, tables)]
     largest = np.abs(counts - counts.sum() // E).max()
     near(np.concatenate(got), want, 84 * U * coef * E / (counts.sum() * tokens) * 2 * largest, "d_logits")
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+def test_gradient_of_counts_that_pass_32_bits_together(moe, kind):  # noqa: F811
+    """Counts of many GPUs, each in int32, 2^33 in all. Tolerance: (64 + far) u c s (|g| + sum s |g|), with far below 20 for normal
+    values and |g| at most the largest count, and half a step of bf16."""
+    rng = np.random.default_rng(22)
+    S, E = 9, 6
+    l = rng.standard_normal((S, E)).astype(np.float32)
+    dev = to_dev(l).to(kind)
+    l = dev.float().cpu().numpy().astype(np.float64)
+    counts = np.array([2**31 - 1, 2**31 - 1, 2**31 - 5, 2**31 - 1, 17, 0], dtype=np.int32)
+    tokens = 2**31 - 1
+    idx = to_dev(rng.integers(0, E, (S, 2)).astype(np.int32))
+    got = moe.moe_balance_loss_backward(torch.ones(1, device=DEV), dev, idx, to_dev(counts), to_dev(np.array([tokens], dtype=np.int32)), 1.0)
+    n = counts.astype(np.float64)
+    s = np.exp(l - l.max(axis=1, keepdims=True))
+    s /= s.sum(axis=1, keepdims=True)
+    each = E / (n.sum() * tokens)
+    want = each * s * (n - (s * n).sum(axis=1, keepdims=True))
+    tol = 84 * U * each * s * 2 * n.max() + (2.0**-8 * np.abs(want) if kind is torch.bfloat16 else 0)
+    near(got.float().cpu().numpy(), want, tol, "d_logits")
