@@ -237,7 +237,11 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(
     sum = wave::sum(sum);
     const int mean = (int)(sum / E);
     const double all = sum * (double)*tokens;
-    const float each = all > 0.0 ? (float)((double)coef * E / all) * *d_loss : 0.0f;
+    // in 64 bits until it meets the counts: coef, d_loss and 1 / (N T) may each be near an end of fp32's range
+    const double each = all > 0.0 ? (double)coef * E / all * *d_loss : 0.0;
+    float g[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) g[i] = (float)(each * (n[i] - mean));
     int t = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Token<N, T> next;
     next.load(logits, stride, topk, t, S, K, E);
@@ -245,19 +249,16 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(
         const Token<N, T> token = next;
         next.load(logits, stride, topk, t + step, S, K, E);
         const bool lives = __any(token.id >= 0 && token.id < E);
-        float s[N], turn[N], g[N];
+        float s[N], turn[N];
         scores_of<N, SCORE>(token.l, s, turn);
         float dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            g[i] = (float)(n[i] - mean);
-            dot += g[i] * s[i];
-        }
+        for (int i = 0; i < N; ++i) dot += g[i] * s[i];
         dot = wave::sum(dot);
         const __amdgpu_buffer_rsrc_t dst = rows::rsrc(d_logits + (int64_t)t * E, E * (int)sizeof(T));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float d = each * (s[i] * (g[i] - dot));
+            float d = s[i] * (g[i] - dot);
             if (SCORE == MOE_SCORE_SIGMOID) d *= turn[i];
             d = lives ? d : 0.0f;
             const int at = (lane + 64 * i) * (int)sizeof(T);

@@ -62,3 +62,25 @@ def test_gradient_of_counts_that_pass_32_bits_together(moe, kind):  # noqa: F811
     want = each * s * (n - (s * n).sum(axis=1, keepdims=True))
     tol = 84 * U * each * s * 2 * n.max() + (2.0**-8 * np.abs(want) if kind is torch.bfloat16 else 0)
     near(got.float().cpu().numpy(), want, tol, "d_logits")
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("coef,d_loss", [(3e38, 1e-36), (1e-36, 1e30), (1e-44, 3e38), (1.0, 1e-37)])
+def test_gradient_of_factors_at_both_ends_of_the_range(moe, score, coef, d_loss):  # noqa: F811
+    """coef * E / (N T) may leave fp32's range where the gradient does not. Tolerance: (64 + far) u c s (|g| + sum s |g|) with
+    c = d_loss coef E / (N T), far below 20 for normal values, and half of the smallest subnormal for each rounding: the factor of
+    a count, the 12 products of the row's sum, and two more products."""
+    rng = np.random.default_rng(23)
+    S, E, K = 5, 12, 2
+    l = rng.standard_normal((S, E)).astype(np.float32)
+    idx = np.full((S, K), -1, dtype=np.int32)
+    idx[2] = 3, 7
+    counts, tokens, unit = oracle.balance(l, idx, 1.0, score)[1:]
+    factor = float(np.float32(coef)) * float(np.float32(d_loss))
+    want = unit * factor
+    dev, table = to_dev(l), to_dev(idx)
+    b = moe.moe_balance_loss(dev, table, coef, score)
+    got = moe.moe_balance_loss_backward(torch.tensor([d_loss], device=DEV), dev, table, b.num_tokens_per_expert, b.num_tokens, coef, score)
+    largest = np.abs(counts - counts.sum() // E).max()
+    note("factors", coef, d_loss, np.abs(want).max())
+    near(values(got), want, 84 * U * factor * E / (counts.sum() * tokens) * 2 * largest + 15 * 2.0**-150, "d_logits")
