@@ -1353,11 +1353,16 @@ def moe_rms_norm(x, weight, eps=1e-6, residual=None, quant=MOE_QUANT_NONE, out=N
 
 
 @functools.lru_cache(maxsize=256)
-def moe_rms_norm_backward_workspace_bytes(rows, H):
-    v = _lib.moe_rms_norm_backward_workspace_bytes(int(rows), int(H))
+def _workspace_bytes(name, a, b):
+    """The library's answer to a size query of two numbers (never of objects, whose values may change)."""
+    v = getattr(_lib, name)(a, b)
     if v < 0:
         _check(int(v))
     return int(v)
+
+
+def moe_rms_norm_backward_workspace_bytes(rows, H):
+    return _workspace_bytes("moe_rms_norm_backward_workspace_bytes", int(rows), int(H))
 
 
 def _workspace(workspace, need, dev, stream):
@@ -1420,12 +1425,8 @@ def _router_args(logits, topk_idx):
     return dev, S, K, E, logits.data_ptr(), size * (step if S > 1 else E), kind, table
 
 
-@functools.lru_cache(maxsize=256)
 def moe_balance_loss_workspace_bytes(S, E):
-    v = _lib.moe_balance_loss_workspace_bytes(int(S), int(E))
-    if v < 0:
-        _check(int(v))
-    return int(v)
+    return _workspace_bytes("moe_balance_loss_workspace_bytes", int(S), int(E))
 
 
 def moe_balance_loss(logits, topk_idx, coef, score=MOE_SCORE_SOFTMAX, out=None, workspace=None, stream=None):

@@ -1,0 +1,19 @@
+"""The binding of the 8-bit layer where it needs no device: its size queries. Needs no GPU."""
+
+import numpy as np
+import pytest
+import torch
+
+import combine_moe_layout_02_amd as moe
+
+
+@pytest.mark.parametrize("query,lib", [(moe.moe_balance_loss_workspace_bytes, moe._lib.moe_balance_loss_workspace_bytes),
+                                       (moe.moe_rms_norm_backward_workspace_bytes, moe._lib.moe_rms_norm_backward_workspace_bytes)])
+def test_size_queries_go_by_values(query, lib):
+    """A number in a tensor or an array whose value changes between two queries."""
+    for number in (torch.tensor(200), np.array(200)):
+        assert query(number, 64) == lib(200, 64)
+        number[...] = 5000
+        assert query(number, 64) == lib(5000, 64) != lib(200, 64)
+    with pytest.raises(ValueError):
+        query(torch.tensor(-1), 64)
