@@ -1395,7 +1395,7 @@ def moe_rms_norm_backward(dy, sum, weight, eps=1e-6, d_sum=None, dx=None, d_weig
         dw_ptr = d_weight.data_ptr()
     else:
         dw_ptr = _dense(d_weight, "d_weight", _fp32, (H,), dev)
-    workspace, ws_ptr, ws_bytes = _workspace(workspace, moe_rms_norm_backward_workspace_bytes(n, H), dev, stream)
+    workspace, ws_ptr, ws_bytes = _workspace(workspace, _workspace_bytes("moe_rms_norm_backward_workspace_bytes", n, H), dev, stream)
     _launch(dev, stream, _lib.moe_rms_norm_backward, dy_ptr, dy_stride, ptr, stride, w_ptr, kind, eps, ds_ptr, ds_stride,
             n, H, dx_ptr, dw_ptr, ws_ptr, ws_bytes)
     return dx, d_weight
@@ -1443,7 +1443,7 @@ def moe_balance_loss(logits, topk_idx, coef, score=MOE_SCORE_SOFTMAX, out=None, 
         loss = _dense(out.loss, "loss", _fp32, (1,), dev)
         counts = _dense(out.num_tokens_per_expert, "num_tokens_per_expert", _int32, (E,), dev)
         tokens = _dense(out.num_tokens, "num_tokens", _int32, (1,), dev)
-    workspace, ws_ptr, ws_bytes = _workspace(workspace, moe_balance_loss_workspace_bytes(S, E), dev, stream)
+    workspace, ws_ptr, ws_bytes = _workspace(workspace, _workspace_bytes("moe_balance_loss_workspace_bytes", S, E), dev, stream)
     _launch(dev, stream, _lib.moe_balance_loss, ptr, stride, kind, table, S, K, E, score, coef, loss, counts, tokens, ws_ptr,
             ws_bytes)
     return out
