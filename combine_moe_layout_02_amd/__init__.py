@@ -1083,11 +1083,12 @@ def _count_arg(num_rows, dev):
 _CALL_ROWS = 1 << 20  # MOE_MAX_OUT_ROWS: the rows that one call of the library converts at most
 
 
-def _mx_parts(name, ptr, stride, codes, scales, count, num_rows, n, H, format, dev, stream):
-    """Rows to MX or back, more of them than one call converts: call after call, all on the one stream."""
-    quantize, fn, width, blocks = name == "moe_mx_quantize", getattr(_lib, name), _mx_width(H, format), H // 32
+def _row_parts(name, ptr, stride, codes, width, scales, scale_bytes, count, num_rows, n, H, kind, dev, stream):
+    """bf16 rows to codes (width bytes a row) and scales, or back, more rows than one call converts: call after call, all on
+    the one stream. kind: the codes' format or quant."""
+    quantize, fn = name.endswith("_quantize"), getattr(_lib, name)
     # a call checks its own part alone for outputs over inputs or over one another
-    spans = ((ptr, (n - 1) * stride + 2 * H), (codes, n * width), (scales, n * blocks), (count or 0, 4 if count else 0))
+    spans = ((ptr, (n - 1) * stride + 2 * H), (codes, n * width), (scales, n * scale_bytes), (count or 0, 4 if count else 0))
     for i, j in (((0, 1), (0, 2), (1, 2), (1, 3), (2, 3)) if quantize else ((0, 1), (0, 2), (0, 3))):
         (x, x_bytes), (y, y_bytes) = spans[i], spans[j]
         if y_bytes and x < y + y_bytes and y < x + x_bytes:
@@ -1097,11 +1098,12 @@ def _mx_parts(name, ptr, stride, codes, scales, count, num_rows, n, H, format, d
             rows, left = min(_CALL_ROWS, n - at), None
             if count is not None:
                 left = num_rows.reshape(-1)[:1].long().sub(at).clamp(0, rows).int()
-            r, c, s, left_ptr = ptr + at * stride, codes + at * width, scales + at * blocks, left if left is None else left.data_ptr()
+            r, c, s = ptr + at * stride, codes + at * width, scales + at * scale_bytes
+            left_ptr = None if left is None else left.data_ptr()
             if quantize:
-                _launch(dev, stream, fn, r, stride, left_ptr, rows, H, format, c, s)
+                _launch(dev, stream, fn, r, stride, left_ptr, rows, H, kind, c, s)
             else:
-                _launch(dev, stream, fn, c, s, left_ptr, rows, H, format, r, stride)
+                _launch(dev, stream, fn, c, s, left_ptr, rows, H, kind, r, stride)
 
 
 def moe_mx_quantize(rows, format, num_rows=None, out=None, stream=None):
@@ -1117,7 +1119,7 @@ def moe_mx_quantize(rows, format, num_rows=None, out=None, stream=None):
     if n:
         ptr, stride, _ = _rows_arg(rows, "rows", H, dev)
         if n > _CALL_ROWS:
-            _mx_parts("moe_mx_quantize", ptr, stride, codes, scales, count, num_rows, n, H, format, dev, stream)
+            _row_parts("moe_mx_quantize", ptr, stride, codes, _mx_width(H, format), scales, H // 32, count, num_rows, n, H, format, dev, stream)
         else:
             _launch(dev, stream, _lib.moe_mx_quantize, ptr, stride, count, n, H, format, codes, scales)
     return MxRows(*out)
@@ -1136,7 +1138,7 @@ def moe_mx_dequantize(mx, format, num_rows=None, out=None, stream=None):
         if rows != n:
             raise ValueError(f"out must have {n} rows")
         if n > _CALL_ROWS:
-            _mx_parts("moe_mx_dequantize", ptr, stride, codes, scales, count, num_rows, n, H, format, dev, stream)
+            _row_parts("moe_mx_dequantize", ptr, stride, codes, _mx_width(H, format), scales, H // 32, count, num_rows, n, H, format, dev, stream)
         else:
             _launch(dev, stream, _lib.moe_mx_dequantize, codes, scales, count, n, H, format, ptr, stride)
     return out
@@ -1245,8 +1247,8 @@ def _row_matrix(t, name):
 
 
 def moe_row_quantize(rows, quant, num_rows=None, out=None, stream=None):
-    """ScaledRows of bf16 rows [R, H] (any row stride) in MOE_QUANT_INT8_DYN or MOE_QUANT_FP8_E4M3_DYN, as moe_dispatch
-    computes them. num_rows: None, or the device count of rows to take (e.g. layout.expert_slot_base[E:]); the
+    """ScaledRows of bf16 rows [R, H] (any row stride), R without a limit, in MOE_QUANT_INT8_DYN or MOE_QUANT_FP8_E4M3_DYN, as
+    moe_dispatch computes them. num_rows: None, or the device count of rows to take (e.g. layout.expert_slot_base[E:]); the
     outputs' other rows keep their contents (undefined where they are allocated here)."""
     dev, n, H, ptr, stride = _row_matrix(rows, "rows")
     if out is None:
@@ -1255,12 +1257,15 @@ def moe_row_quantize(rows, quant, num_rows=None, out=None, stream=None):
     else:
         codes, scales = _row8_args(out, "out", (n, H), dev)
     count = _count_arg(num_rows, dev)
-    _launch(dev, stream, _lib.moe_row_quantize, ptr, stride, count, n, H, quant, codes, scales)
+    if n > _CALL_ROWS:
+        _row_parts("moe_row_quantize", ptr, stride, codes, H, scales, 4, count, num_rows, n, H, quant, dev, stream)
+    else:
+        _launch(dev, stream, _lib.moe_row_quantize, ptr, stride, count, n, H, quant, codes, scales)
     return ScaledRows(*out)
 
 
 def moe_row_dequantize(rows8, quant, num_rows=None, out=None, stream=None):
-    """The values of ScaledRows [R, H] as bf16 rows (out: any row stride)."""
+    """The values of ScaledRows [R, H] as bf16 rows (out: any row stride), R without a limit."""
     dev, n, H, codes, scales = _row8_matrix(rows8, "rows8")
     if out is None:
         out = _out(n, H, _bf16, dev, stream)
@@ -1268,7 +1273,10 @@ def moe_row_dequantize(rows8, quant, num_rows=None, out=None, stream=None):
     else:
         ptr, stride = _some_rows(out, "out", n, H, dev)
     count = _count_arg(num_rows, dev)
-    _launch(dev, stream, _lib.moe_row_dequantize, codes, scales, count, n, H, quant, ptr, stride)
+    if n > _CALL_ROWS:
+        _row_parts("moe_row_dequantize", ptr, stride, codes, H, scales, 4, count, num_rows, n, H, quant, dev, stream)
+    else:
+        _launch(dev, stream, _lib.moe_row_dequantize, codes, scales, count, n, H, quant, ptr, stride)
     return out
 
 

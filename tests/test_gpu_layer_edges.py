@@ -1,5 +1,5 @@
 """GPU tests of the 8-bit layer's calls at their edges: the balance loss over several GPUs' tokens and at the ends of its
-factors' ranges.
+factors' ranges, and more rows than one call of the library converts.
 
 Tolerances, derived before the first run, are written at each test; u = 2^-24 is fp32's rounding. The oracle is numpy in
 64 bits.
@@ -10,7 +10,8 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_layer import DEV, U, moe, near, note, routing, to_dev, values  # noqa: F401
+from test_gpu_layer import (DEV, E4M3, INT8, U, bf16_bits, bf16_dev, bits, moe, near, note, poison, poisoned, routing, same_bits,
+                            same_rows8, to_dev, values)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,59 @@ def test_gradient_of_factors_at_both_ends_of_the_range(moe, score, coef, d_loss)
     largest = np.abs(counts - counts.sum() // E).max()
     note("factors", coef, d_loss, np.abs(want).max())
     near(values(got), want, 84 * U * factor * E / (counts.sum() * tokens) * 2 * largest + 15 * 2.0**-150, "d_logits")
+
+
+# ---------------------------------------------------------------- rows in 8 bits
+
+
+MOST = 1 << 20  # rows that one call of the library converts
+
+
+@pytest.mark.parametrize("quant", [E4M3, INT8])
+@pytest.mark.parametrize("given", [False, True])
+def test_more_rows_than_one_call_converts(moe, quant, given):  # noqa: F811
+    """2^20 + 300 rows at a stride, as all experts' weights may be, with counts on both sides of the parts' border; on the
+    current stream and on one that the call is given. Bit for bit."""
+    rng = np.random.default_rng(24 + quant)
+    R, H = MOST + 300, 32
+    x = bits(rng.standard_normal((R, H)))
+    wide = poison((R, H + 8), torch.bfloat16)
+    wide[:, :H] = bf16_dev(x)
+    at = np.concatenate((np.arange(40), np.arange(MOST - 40, R)))
+    codes, scales = oracle.row_quantize(x[at], quant)
+    back = bits(oracle.row_values(codes, scales, quant))
+    index = to_dev(at)
+    stream = torch.cuda.Stream() if given else None
+    for n in (None, -3, 5, MOST, MOST + 1, R - 1, R + 9):
+        used = R if n is None else min(max(n, 0), R)
+        count = None if n is None else torch.tensor([n], dtype=torch.int32, device=DEV)
+        out = moe.ScaledRows(poison((R, H), torch.uint8), poison(R, torch.float32))
+        values_out = poison((R, H + 8), torch.bfloat16)
+        torch.cuda.synchronize()  # the buffers are whole before another stream uses them
+        note("rows in parts", quant, given, n)
+        moe.moe_row_quantize(wide[:, :H], quant, num_rows=count, out=out, stream=stream)
+        moe.moe_row_dequantize(out, quant, num_rows=count, out=values_out[:, :H], stream=stream)
+        torch.cuda.synchronize()
+        some = at < used
+        same_rows8(moe.ScaledRows(out.codes[index][: some.sum()], out.scales[index][: some.sum()]), codes[some], scales[some])
+        same_bits(bf16_bits(values_out[:, :H][index])[some], back[some])
+        assert poisoned(out.codes[used:]) and poisoned(out.scales[used:]) and poisoned(values_out[used:]) and poisoned(values_out[:, H:])
+
+
+def test_parts_of_rows_refuse_what_one_call_refuses(moe):  # noqa: F811
+    """Outputs over inputs and over one another, where only parts that do not run together touch."""
+    R, H = MOST + 300, 32
+    buf = torch.zeros(2 * R * H + 64, dtype=torch.uint8, device=DEV)
+    rows = buf[: 2 * R * H].view(torch.bfloat16).view(R, H)
+    scales = torch.zeros(R, device=DEV)
+    last = buf[2 * R * H - R * H : 2 * R * H].view(R, H)  # over the later rows
+    with pytest.raises(ValueError, match="overlap"):
+        moe.moe_row_quantize(rows, INT8, out=(last, scales))
+    with pytest.raises(ValueError, match="overlap"):
+        moe.moe_row_dequantize((last, scales), INT8, out=rows)
+    codes = torch.zeros((R, H), dtype=torch.uint8, device=DEV)
+    over = codes.view(-1)[-4 * R :].view(torch.float32)  # scales over the later codes
+    with pytest.raises(ValueError, match="overlap"):
+        moe.moe_row_quantize(rows, INT8, out=(codes, over))
+    with pytest.raises(ValueError):
+        moe.moe_row_quantize(rows, 0, out=(codes, scales))
