@@ -486,6 +486,13 @@ hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64
     // -> 2192 gated, 85.9 and 121 with 64 x 128 and two, 1019 on 61, 5488 -> 1074 gated, 86.8 and 113, 512 on 32, 7168
     // -> 4096 gated, 161 and 158.
     //
+    // 256 x 256 also wants its columns filled. One column of 128 weight rows leaves half of every tile without results: 65536
+    // rows on 8 groups, 256 -> 128 gated, 21.2 and 11.7 with 128 x 128, 2^20 rows on one, 4096 -> 128, 1034 and 915. Three
+    // columns leave a quarter, which long rows make up for and short ones do not: 65536 rows on 8 groups, 256 -> 384, 27.1
+    // and 20.5, 262144 on one, 4096 -> 384, 508 and 645. Over 310 products of 49152 to 2^20 rows on 1 or 8 groups, 256 to
+    // 4096 -> 64 to 1000, the choice takes 1.6% longer than the best of the two pairs' kernels, 37% at most; without
+    // this condition 9.3% and 81%.
+    //
     // Four pairs want rows of 12 pairs: 3001 rows on 16 groups, 1040 -> 1000, take 15.9 with 128 x 128 and four, 16.1
     // with 64 x 128 and two from memory, 15.4 and 12.0 from the caches; 43 rows on 64 groups, 1520 -> 3494 gated, 38.5
     // with 64 x 64 and four, 38.4.
@@ -501,13 +508,15 @@ hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64
         return hit * ((width + outs - 1) / outs) * halves / (2 * tm);
     };
     const int64_t reads = expected(16, 32) * (std::min<int64_t>(mean, 16) + 32);  // rows that few_rows' workgroups read
+    const int cols = gated ? 64 : 128, columns = (width + cols - 1) / cols, spare = columns % 2;  // of 128 weight rows, one alone in a tile of 256
+    const bool filled = spare * 5 <= columns || (H >= 1536 && spare * 3 <= columns);
     const bool cached = hit * O * H <= 12 << 20 || reads * H <= 56 << 20;
     if (reads <= 12288 && (H % 64 == 0 || cached)) return few_rows(p);
     if (expected(32, 64) <= (mean <= 32 ? 2 * kUnits : kUnits)) return tiles<32, 64, 2, 1, 4>(p);  // two at once on a unit
     if (expected(64, 64) <= kUnits) return tiles<64, 64, 4, 1, 4>(p);
     if (expected(64, 128) <= kUnits) return tiles<64, 128, 2, 2, 4>(p);
     if (mean <= 24 && H >= 1536) return tiles<64, 64, 4, 1, 4>(p);
-    if (mean >= 160 && expected(256, 256) >= 192) return tiles<256, 256, 2, 4, 2>(p);
+    if (mean >= 160 && filled && expected(256, 256) >= 192) return tiles<256, 256, 2, 4, 2>(p);
     if (H >= 1536 && expected(128, 128) <= kUnits) return tiles<128, 128, 2, 2, 4>(p);
     if (mean >= 48 && (H >= 1536 || expected(128, 128) >= 300)) return tiles<128, 128, 2, 2, 2>(p);
     return tiles<64, 128, 2, 2, 2>(p);

@@ -1,5 +1,5 @@
 """GPU tests of the 8-bit layer's calls at their edges: the balance loss over several GPUs' tokens and at the ends of its
-factors' ranges, and more rows than one call of the library converts.
+factors' ranges, more rows than one call of the library converts, and products of many rows.
 
 Tolerances, derived before the first run, are written at each test; u = 2^-24 is fp32's rounding. The oracle is numpy in
 64 bits.
@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_layer import (DEV, E4M3, INT8, U, bf16_bits, bf16_dev, bits, moe, near, note, poison, poisoned, routing, same_bits,
+from test_gpu_layer import (DEV, E4M3, GATED, INT8, PLAIN, U, bf16_bits, bf16_dev, bits, int8_rows, moe, near, note, poison, poisoned, routing, same_bits,
                             same_rows8, to_dev, values)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +141,29 @@ def test_parts_of_rows_refuse_what_one_call_refuses(moe):  # noqa: F811
         moe.moe_row_quantize(rows, INT8, out=(codes, over))
     with pytest.raises(ValueError):
         moe.moe_row_quantize(rows, 0, out=(codes, scales))
+
+
+# ---------------------------------------------------------------- the product
+
+
+@pytest.mark.parametrize("R,G,H,O,epilogue", [(65536, 8, 256, 128, GATED), (50000, 1, 272, 100, PLAIN), (65536, 8, 256, 384, PLAIN), (50000, 3, 1552, 260, PLAIN),
+                                              (70000, 2, 144, 640, GATED), (1 << 20, 1, 64, 64, PLAIN)])
+def test_products_of_many_rows_and_few_outputs(moe, R, G, H, O, epilogue):  # noqa: F811
+    """Rows around the groups' borders and at the ends, bit for bit; gated ones to silu's 2^-14 and half a step of bf16."""
+    rng = np.random.default_rng(R + O)
+    base = np.concatenate(([0], np.sort(rng.integers(0, R + 1, G - 1)), [R])).astype(np.int32)
+    a, scales = int8_rows(rng, R, H)
+    w = rng.integers(-128, 128, (G, O, H)).astype(np.int8)
+    w_scales = (np.exp2(rng.uniform(-5, 0, (G, O))) / (np.sqrt(H) * 4)).astype(np.float32)
+    note("many rows", R, G, H, O, epilogue)
+    got = moe.moe_scaled_product(moe.ScaledRows(to_dev(a), to_dev(scales)), moe.ScaledRows(to_dev(w), to_dev(w_scales)), to_dev(base), epilogue)
+    at = np.unique(np.clip(np.concatenate([np.arange(b - 300, b + 300) for b in base]), 0, R - 1))
+    v, group = oracle.int8_product(a[at], scales[at], np.searchsorted(at, base), w, w_scales)
+    assert (group == np.searchsorted(base, at, side="right") - 1).all()
+    some = got[to_dev(at)]
+    if epilogue == PLAIN:
+        same_bits(bf16_bits(some), bits(v))
+    else:
+        gate, up = v[:, : O // 2].astype(np.float64), v[:, O // 2 :].astype(np.float64)
+        want = gate / (1 + np.exp(-gate)) * up
+        near(values(some), want, (2.0**-8 + 2.0**-13) * np.abs(want) + 2.0**-133, "gated")
