@@ -20,8 +20,10 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kFinishThreads = 1024;
 constexpr int kBackwardGrid = 2048;
 
-// exp(x) for x <= 0 to 2 ulp, from the hardware's exp2 of x * log2(e) and the rest of that product; 0 from -200 down, NaN of a
-// NaN. A third of the library function's instructions, which bound these kernels.
+// exp(x) to 2 ulp for x in [-87.3, 0], from the hardware's exp2 of x * log2(e) and the rest of that product; 0 below, where exp(x)
+// is less than 2^-126 and the hardware gives no subnormals; NaN of a NaN. -200 keeps the rest of -inf a number. A third of
+// the library function's instructions, which bound these kernels. What is taken as 0 is a score that far below the largest, or 1 -
+// sigmoid(l) of l > 87.3.
 __device__ inline float exp_of(float x) {
     constexpr float kLog2e = 1.44269502e+00f, kLog2eRest = 1.92596299e-08f, kLn2 = 6.93147182e-01f;
     x = x < -200.0f ? -200.0f : x;
@@ -31,9 +33,10 @@ __device__ inline float exp_of(float x) {
     return __builtin_fmaf(y, rest * kLn2, y);
 }
 
-// The scores of one token from its logits (-inf past E): exp(l - max) over their sum, or sigmoids over theirs. A token whose
-// logits are all far below zero, where sigmoid(l) is exp(l) to fp32, keeps its scores: they are taken against the
-// largest. A logit of -inf has score 0, also where there is no other. turn: 1 - sigmoid(l), for MOE_SCORE_SIGMOID.
+// The scores of one token from its logits (-inf past E): exp(l - max) over their sum, or sigmoids over theirs. Where all
+// logits are below zero the sigmoids, exp(l) / (1 + exp(l)), are taken against exp(max): a token far below zero keeps its scores,
+// also those far below its largest. A logit of -inf has score 0, also where there is no other. turn: 1 - sigmoid(l), for
+// MOE_SCORE_SIGMOID.
 template <int N, int SCORE>
 __device__ inline void scores_of(const float (&l)[N], float (&s)[N], float (&turn)[N]) {
     float top = l[0];
@@ -46,7 +49,7 @@ __device__ inline void scores_of(const float (&l)[N], float (&s)[N], float (&tur
         if constexpr (SCORE == MOE_SCORE_SIGMOID) {
             const float far = exp_of(-fabsf(l[i])), share = __builtin_amdgcn_rcpf(1.0f + far);
             turn[i] = (l[i] > 0.0f ? far : 1.0f) * share;
-            s[i] = top < -60.0f ? exp_of(l[i] - top) : (l[i] > 0.0f ? 1.0f : far) * share;
+            s[i] = (top < 0.0f ? exp_of(l[i] - top) : l[i] > 0.0f ? 1.0f : far) * share;
         } else {
             s[i] = exp_of(l[i] - top);
         }

@@ -758,7 +758,8 @@ int moe_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, const void *s
  *                    (times 1 - sigmoid(logits[t, e]) for MOE_SCORE_SIGMOID); 0 for padding
  *
  * The counts have no gradient. Logits of -inf (experts a token may not go to) have score 0 and gradient 0; a token
- * whose logits are all -inf has no scores. Everything in fp32, the sums over tokens in an order fixed by S and E.
+ * whose logits are all -inf has no scores; scores below 2^-125 of the token's largest may be 0. Everything in fp32, the
+ * sums over tokens in an order fixed by S and E.
  * moe_balance_loss
  * In:  logits     [S, E] of logits_type (moe_float), row t at t * logits_stride_bytes (a multiple of the element and at
  *                 least E of them), aligned to the element.

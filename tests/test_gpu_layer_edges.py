@@ -10,8 +10,8 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_layer import (DEV, E4M3, GATED, INT8, PLAIN, U, bf16_bits, bf16_dev, bits, int8_rows, moe, near, note, poison, poisoned, routing, same_bits,
-                            same_rows8, to_dev, values)  # noqa: F401
+from test_gpu_layer import (DEV, E4M3, GATED, INT8, PLAIN, U, balance_case, bf16_bits, bf16_dev, bits, int8_rows, moe, near, note, poison,
+                            poisoned, routing, same_bits, same_rows8, to_dev, values)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -87,6 +87,17 @@ def test_gradient_of_factors_at_both_ends_of_the_range(moe, score, coef, d_loss)
     near(values(got), want, 84 * U * factor * E / (counts.sum() * tokens) * 2 * largest + 15 * 2.0**-150, "d_logits")
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("score", [0, 1])
+def test_scores_far_below_the_largest(moe, score, kind):  # noqa: F811
+    """Tokens whose largest logit lies anywhere from -200 to 40 and whose others lie up to 85 below it: each keeps its score and its
+    gradient, to balance_case's bounds."""
+    rng = np.random.default_rng(25)
+    S, E = 150, 40
+    l = (np.linspace(-200, 40, S)[:, None] - rng.uniform(0, 85, (S, E))).astype(np.float32)
+    balance_case(moe, l, routing(rng, S, E, 4, ""), score, kind, coef=1.0)
+
+
 # ---------------------------------------------------------------- rows in 8 bits
 
 
@@ -146,8 +157,8 @@ def test_parts_of_rows_refuse_what_one_call_refuses(moe):  # noqa: F811
 # ---------------------------------------------------------------- the product
 
 
-@pytest.mark.parametrize("R,G,H,O,epilogue", [(65536, 8, 256, 128, GATED), (50000, 1, 272, 100, PLAIN), (65536, 8, 256, 384, PLAIN), (50000, 3, 1552, 260, PLAIN),
-                                              (70000, 2, 144, 640, GATED), (1 << 20, 1, 64, 64, PLAIN)])
+@pytest.mark.parametrize("R,G,H,O,epilogue", [(65536, 8, 256, 128, GATED), (50000, 1, 272, 100, PLAIN), (65536, 8, 256, 384, PLAIN),
+                                              (50000, 3, 1552, 260, PLAIN), (70000, 2, 144, 640, GATED), (1 << 20, 1, 64, 64, PLAIN)])
 def test_products_of_many_rows_and_few_outputs(moe, R, G, H, O, epilogue):  # noqa: F811
     """Rows around the groups' borders and at the ends, bit for bit; gated ones to silu's 2^-14 and half a step of bf16."""
     rng = np.random.default_rng(R + O)
