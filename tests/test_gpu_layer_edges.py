@@ -1,5 +1,5 @@
 """GPU tests of the 8-bit layer's calls at their edges: the balance loss over several GPUs' tokens and at the ends of its
-factors' ranges, more rows than one call of the library converts, and products of many rows.
+factors' ranges, more rows than one call of the library converts, products of many rows, and the links of a whole step.
 
 Tolerances, derived before the first run, are written at each test; u = 2^-24 is fp32's rounding. The oracle is numpy in
 64 bits.
@@ -10,8 +10,8 @@ import pytest
 import torch
 
 import oracle
-from test_gpu_layer import (DEV, E4M3, GATED, INT8, PLAIN, U, balance_case, bf16_bits, bf16_dev, bits, int8_rows, moe, near, note, poison,
-                            poisoned, routing, same_bits, same_rows8, to_dev, values)  # noqa: F401
+from test_gpu_layer import (DEV, E4M3, GATED, INT8, PLAIN, Step, U, balance_case, bf16_bits, bf16_dev, bits, equal, int8_rows, moe, near, note,
+                            poison, poisoned, routing, same_bits, same_rows8, to_dev, values)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -178,3 +178,137 @@ def test_products_of_many_rows_and_few_outputs(moe, R, G, H, O, epilogue):  # no
         gate, up = v[:, : O // 2].astype(np.float64), v[:, O // 2 :].astype(np.float64)
         want = gate / (1 + np.exp(-gate)) * up
         near(values(some), want, (2.0**-8 + 2.0**-13) * np.abs(want) + 2.0**-133, "gated")
+
+
+# ---------------------------------------------------------------- together
+
+
+def silu_bound(v):
+    """Gate times up of the product's values v [R, 2 I], and its bound: silu to 2^-14, then half a step of bf16."""
+    half = v.shape[1] // 2
+    gate, up = v[:, :half].astype(np.float64), v[:, half:].astype(np.float64)
+    want = gate / (1 + np.exp(-gate)) * up
+    return want, (2.0**-8 + 2.0**-13) * np.abs(want) + 2.0**-133
+
+
+def host8(rows8):
+    return rows8[0].cpu().numpy().view(np.int8), rows8[1].cpu().numpy()
+
+
+def test_every_link_of_a_step(moe):  # noqa: F811
+    """A layer's forward and backward pass, each call's result against the oracle's of what that call was given on the GPU: bit for
+    bit but for the activation (silu_bound), the balance loss (as in balance_case), the weights' gradient of the combine (128
+    additions' roundings) and the norm's gradients (2^-21 of their terms and half a step; (S / 256 + 85) u for d_weight)."""
+    step = Step(moe, 7)
+    S, H, E, K = step.S, step.H, step.E, step.K
+    coef = 0.01
+    normed = moe.moe_rms_norm(step.x, step.norm_weight, residual=step.residual, quant=INT8, out=torch.empty_like(step.x))
+    logits = normed.out.float() @ step.router
+    lay = moe.moe_layout(step.topk_idx, E, 1, 1)
+    loss = moe.moe_balance_loss(logits, step.topk_idx, coef)
+    moe.moe_dispatch(normed.out, lay.slot_idx, step.window, INT8)
+    rows = lay.expert_slot_base[E:]
+    un = moe.moe_unpack(step.window, rows, S, K, H, INT8)
+    mid = moe.moe_scaled_product(moe.ScaledRows(un.expand_x, un.expand_scales), step.up, lay.expert_slot_base, GATED)
+    mid8 = moe.moe_row_quantize(mid, INT8, num_rows=rows)
+    expert_out = moe.moe_scaled_product(mid8, step.down, lay.expert_slot_base)
+    y = moe.moe_combine(expert_out, lay.slot_idx, step.topk_weights)
+    shared_mid = moe.moe_scaled_product(normed.rows8, step.shared_up, step.all_rows, GATED)
+    shared_mid8 = moe.moe_row_quantize(shared_mid, INT8)
+    shared = moe.moe_scaled_product(shared_mid8, step.shared_down, step.all_rows)
+    d_rows, d_weights = moe.moe_combine_backward(step.dy, expert_out, lay.slot_idx, step.topk_weights)
+    d_out = moe.moe_dispatch_backward(d_rows, lay.slot_idx)
+    d_logits = moe.moe_balance_loss_backward(torch.ones(1, device=DEV), logits, step.topk_idx, loss.num_tokens_per_expert, loss.num_tokens, coef)
+    dx, d_norm = moe.moe_rms_norm_backward(d_out, normed.sum, step.norm_weight, d_sum=step.dy)
+
+    idx, weights, slots = step.topk_idx.cpu().numpy(), step.topk_weights.cpu().numpy(), lay.slot_idx.cpu().numpy()
+    w = step.norm_weight.cpu().numpy()
+    total, yn = oracle.rms_norm(bf16_bits(step.x), bf16_bits(step.residual), w, 1e-6)
+    same_bits(bf16_bits(normed.sum), total, "sum")
+    same_bits(bf16_bits(normed.out), bits(yn), "normed")
+    same_rows8(normed.rows8, *oracle.row_quantize_f32(yn, INT8), "normed in 8 bits")
+    want = oracle.layout(idx, E, 1, 1)
+    assert np.array_equal(slots, want["slot_idx"])
+    base, used = want["expert_slot_base"], int(want["expert_slot_base"][E])
+    token = np.empty(used, dtype=np.int64)
+    token[slots.ravel()] = np.arange(slots.size) // K
+    codes, scales = oracle.row_quantize(bf16_bits(normed.out), INT8)
+    same_rows8(moe.ScaledRows(un.expand_x[:used], un.expand_scales[:used]), codes[token], scales[token], "unpacked")
+    for first, at, up, second, down, out, edges in ((moe.ScaledRows(un.expand_x, un.expand_scales), mid, step.up, mid8, step.down, expert_out, base),
+                                                    (normed.rows8, shared_mid, step.shared_up, shared_mid8, step.shared_down, shared, [0, S])):
+        near(values(at), *silu_bound(oracle.int8_product(*host8(first), edges, *host8(up))[0]), "activation")
+        same_rows8(second, *oracle.row_quantize(bf16_bits(at), INT8), "activation in 8 bits")
+        same_bits(bf16_bits(out), bits(oracle.int8_product(*host8(second), edges, *host8(down))[0]), "second product")
+    same_bits(bf16_bits(y), oracle.combine(bf16_bits(expert_out), slots, weights), "y")
+
+    want_rows, want_w, magnitude = oracle.combine_backward(bf16_bits(step.dy), values(expert_out), slots, weights, bf16_bits(d_rows))
+    same_bits(bf16_bits(d_rows), want_rows, "d_rows")
+    near(values(d_weights), want_w, 128 * U * magnitude + 1e-37, "d_weights")
+    same_bits(bf16_bits(d_out), oracle.dispatch_backward(want_rows, slots), "d_out")
+    l = values(logits)
+    want, counts, tokens, want_d = oracle.balance(l, idx, coef, 0)
+    near(values(loss.loss), [want], 412 * U * want, "loss")
+    assert np.array_equal(loss.num_tokens_per_expert.cpu().numpy(), counts) and int(loss.num_tokens) == tokens == S
+    far = l.max(axis=1, keepdims=True).astype(np.float64) - l
+    s = np.exp(-far) / np.exp(-far).sum(axis=1, keepdims=True)
+    g = np.abs(counts - counts.sum() // E)
+    near(values(d_logits), want_d, coef * E / (counts.sum() * tokens) * U * (64 + far) * s * (g + (s * g).sum(axis=1, keepdims=True)), "d_logits")
+    want_dx, want_dw = oracle.rms_norm_backward(bf16_bits(d_out), total, w, 1e-6, bf16_bits(step.dy))
+    h, do = oracle.bf16_bits_to_f32(total).astype(np.float64), values(d_out).astype(np.float64)
+    r = 1 / np.sqrt((h * h).mean(axis=1, keepdims=True) + 1e-6)
+    terms = np.abs(r * do * w) + np.abs(h * r * r * (do * w * h * r).mean(axis=1, keepdims=True)) + np.abs(values(step.dy))
+    near(values(dx), want_dx, 2.0**-21 * terms + 2.0**-8 * np.abs(want_dx) + 2.0**-133, "dx")
+    near(values(d_norm), want_dw, (S / 256 + 85) * U * np.abs(do * h * r).sum(axis=0), "d_norm")
+
+
+def test_steps_on_streams_that_wait_for_their_inputs(moe):  # noqa: F811
+    """Steps on streams of their own, each behind the one that made its inputs: eagerly, then both at once as graphs."""
+    steps = [Step(moe, 8), Step(moe, 9)]
+    want = [s() for s in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    graphs = []
+    for s, stream, w in zip(steps, streams, want):
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            got = s()
+        torch.cuda.synchronize()
+        assert equal(got, w)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            outs = s()
+        graphs.append((g, outs))
+    for _ in range(3):
+        for s in steps:
+            s.x.copy_(torch.randn(s.S, s.H, device=DEV).to(torch.bfloat16))
+        want = [s() for s in steps]
+        torch.cuda.synchronize()
+        for (g, _), stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(equal(outs, w) for (_, outs), w in zip(graphs, want))
+
+
+def test_calls_that_are_given_their_stream(moe):  # noqa: F811
+    """Each call on a stream that waits for its inputs, which outlive it; results as on the current stream."""
+    step = Step(moe, 10)
+    logits = torch.randn((step.S, step.E), device=DEV)
+    one = torch.ones(1, device=DEV)
+
+    def calls(stream):
+        n = moe.moe_rms_norm(step.x, step.norm_weight, residual=step.residual, quant=INT8, stream=stream)
+        v = moe.moe_row_dequantize(n.rows8, INT8, stream=stream)
+        q = moe.moe_row_quantize(v, E4M3, stream=stream)
+        mid = moe.moe_scaled_product(n.rows8, step.shared_up, step.all_rows, GATED, stream=stream)
+        dx, dw = moe.moe_rms_norm_backward(step.dy, n.sum, step.norm_weight, d_sum=v, stream=stream)
+        b = moe.moe_balance_loss(logits, step.topk_idx, 1.0, stream=stream)
+        d = moe.moe_balance_loss_backward(one, logits, step.topk_idx, b.num_tokens_per_expert, b.num_tokens, 1.0, stream=stream)
+        return [n.sum, n.rows8.codes, n.rows8.scales, v, q.codes, q.scales, mid, dx, dw, *b, d]
+
+    want = calls(None)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    for given in (stream, stream.cuda_stream):
+        got = calls(given)
+        torch.cuda.synchronize()
+        assert equal(got, want)
