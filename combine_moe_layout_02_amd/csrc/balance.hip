@@ -295,7 +295,7 @@ hipError_t launch_balance_loss(const void *logits, int64_t logits_stride_bytes, 
                                int32_t score, float coef, float *loss,
                                int32_t *num_tokens_per_expert, int32_t *num_tokens, void *workspace,
                                hipStream_t stream) {
-    const int most = balance_parts(S), per = (S + most - 1) / most, parts = (S + per - 1) / per;
+    const int most = balance_parts(S, E), per = (S + most - 1) / most, parts = (S + per - 1) / per;
     const int64_t each = (int64_t)most * ((E + 3) / 4 * 4);
     BalanceShares *const shares = static_cast<BalanceShares *>(workspace);
     float *const sums = parts > 1 ? reinterpret_cast<float *>(shares + 1) : nullptr;

@@ -295,7 +295,11 @@ hipError_t launch_rms_norm_backward(const void *dy, int64_t dy_stride_bytes, con
 // Parts that the balance loss splits its tokens into, one compute unit each. Each has the experts' sums of scores (fp32) and
 // counts (16 bits) in the workspace, E rounded up to 4 of them, behind them every part's number of tokens and before them
 // the joining workgroups' shares; a single part needs none, nor a second kernel.
-constexpr int kBalanceAlone = 128;  // tokens that a single part takes
+// A single part is one launch and no join, but its waves take the tokens in turn. 128 tokens of 64 experts take it 5.8 us (6.6 with
+// sigmoids) in a graph, several parts 5.7 (5.8), called one by one 7.4 and 10.7; of 256 experts 8.5 (9.7) and 8.0 (8.3), 8.7
+// (9.9) and 10.8; of 512 experts 12.1 (14.7) and 9.4 (10.0), 12.2 (14.8) and 10.8, but 64 of those 7.4 (8.7) and 9.3 (10.0).
+// 192 tokens of 64 experts 7.8 (8.9) and 5.7 (5.8).
+inline int balance_alone(int32_t E) { return E <= 256 ? 128 : 64; }  // tokens that a single part takes
 constexpr int kBalanceTokens = 32;  // tokens of several parts at least
 constexpr int kBalanceParts = 256;  // a part's counts stay below 2^16: MOE_MAX_TOKENS / 256 * MOE_MAX_K = 2^12
 struct alignas(16) BalanceShares {
@@ -304,14 +308,14 @@ struct alignas(16) BalanceShares {
     int32_t done;  // workgroups that have left theirs
 };
 
-inline int balance_parts(int32_t S) {
-    if (S <= kBalanceAlone) return 1;
+inline int balance_parts(int32_t S, int32_t E = MOE_MAX_EXPERTS) {  // without E, the most that S tokens have
+    if (S <= balance_alone(E)) return 1;
     const int parts = (S + kBalanceTokens - 1) / kBalanceTokens;
     return parts < kBalanceParts ? parts : kBalanceParts;
 }
 
 inline int64_t balance_workspace(int32_t S, int32_t E) {
-    const int64_t parts = balance_parts(S);
+    const int64_t parts = balance_parts(S, E);
     return parts > 1 ? (int64_t)sizeof(BalanceShares) + parts * ((E + 3) / 4 * 4 * 6 + 4) : 0;
 }
 

@@ -98,6 +98,13 @@ def test_scores_far_below_the_largest(moe, score, kind):  # noqa: F811
     balance_case(moe, l, routing(rng, S, E, 4, ""), score, kind, coef=1.0)
 
 
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("S,E", [(64, 512), (65, 512), (128, 257), (128, 256), (129, 256)])
+def test_around_the_most_tokens_of_one_workgroup(moe, S, E, score):  # noqa: F811
+    rng = np.random.default_rng(S + E)
+    balance_case(moe, rng.standard_normal((S, E)).astype(np.float32), routing(rng, S, E, 6, "padded"), score, "fp32")
+
+
 # ---------------------------------------------------------------- rows in 8 bits
 
 

@@ -1,4 +1,4 @@
-"""The binding of the 8-bit layer where it needs no device: its size queries. Needs no GPU."""
+"""The size queries of the 8-bit layer. Needs no GPU."""
 
 import numpy as np
 import pytest
@@ -17,3 +17,10 @@ def test_size_queries_go_by_values(query, lib):
         assert query(number, 64) == lib(5000, 64) != lib(200, 64)
     with pytest.raises(ValueError):
         query(torch.tensor(-1), 64)
+
+
+@pytest.mark.parametrize("E,alone", [(1, 128), (16, 128), (256, 128), (257, 64), (512, 64)])
+def test_small_batches_need_no_workspace(E, alone):
+    """One workgroup takes them by itself, the fewer the more experts a token has."""
+    assert [moe.moe_balance_loss_workspace_bytes(S, E) for S in (1, alone)] == [0, 0]
+    assert moe.moe_balance_loss_workspace_bytes(alone + 1, E) > 0
