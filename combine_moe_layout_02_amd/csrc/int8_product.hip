@@ -500,7 +500,9 @@ hipError_t launch_int8_product(const void *a_codes, const float *a_scales, int64
     // How many tiles uneven groups have is expected, from their mean: a half more than their rows would fill, one at
     // least. Over 514 products of random sizes (1 to 32768 rows on 1 to 64 groups, 4 MB of weights at least) the rule's
     // choice takes 1.7% longer than the best of these kernels (geometric mean); with each group's tiles counted at five
-    // quarters of the mean it took 5.7.
+    // quarters of the mean it took 5.7. Over 450 others, of up to 2^20 rows on up to 512 groups, it is 1.8% behind, 42% at most
+    // (290 rows on 6 groups, 7104 -> 2229), and a bound of 1024, 1280, 2048 or 2560 on H in place of 1536 makes it 1.9, 1.8, 1.8
+    // and 1.9.
     const int64_t hit = a_rows < G ? a_rows : G, mean = (a_rows + hit - 1) / hit;
     const auto expected = [&](int tm, int tn) {
         const int outs = gated ? tn / 2 : tn;
