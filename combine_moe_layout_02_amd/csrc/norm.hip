@@ -5,13 +5,14 @@
 // i * lanes of 8 values, so that every byte is moved once. The sum of squares is taken in 64 bits: the squares of bf16 values are
 // exact there, nothing overflows, and the codes, which lie next to borders, do not depend on the order of the additions.
 //
-// HBM bounds all of it (4096 rows of 7168, us and TB/s of what is read and written): to bf16 41.9 and 5.6, to INT8 38.6 and 5.3,
-// the gradients 50.5 and 4.7 with d_weight's second kernel (4.7 of them). Two vectors a lane: to INT8 such rows take
-// 42.0 with two, 42.2 with four, 55 with eight and 77 with one, 1531 rows of 2064 7.8, 8.5, 12.0 and 10.4, 4096 rows
-// of 1024 7.2, 9.6, 21.4 and 9.3, 128 rows of 7168 5.2, 5.4, 6.3 and 6.3. A workgroup that takes row after row with the weights in
-// its registers and the next row's loads under way is no faster (44.9, two rows a compute unit in flight) and its
-// registers cost short rows (1531 rows 9.9 to 14). Stores with nt 42.0, sc0 sc1 nt 42.2, written back 43.8. Reductions through
-// shuffles, an LDS access a step, and four times the waves a row took 72.
+// HBM bounds the forward, and a row's chain the gradient. Call after call, 4096 rows of 7168, us and TB/s of what is read and
+// written: to bf16 41.8 and 5.6, to INT8 38.5 and 5.3, the gradients 50.7 and 4.6 with d_weight's second kernel (4.7 of them). Two
+// vectors a lane: to INT8 such rows take 38.5, with four 37.4, with eight 39.0, with one 55.6; 1531 rows of 2064 7.6, 8.5, 8.9 and
+// 9.9; 4096 rows of 1024 7.5, 8.8, 12.1 and 9.2; 128 rows of 7168 5.1, 5.2, 5.8 and 6.2. Stores with nt (bf16, INT8) 41.8 and 38.5,
+// with sc0 sc1 nt 42.0 and 38.8, written back 43.6 and 39.9. A workgroup that takes row after row with the weights in its
+// registers and the next row's loads under way was no faster (44.9 where this form then took 42.0, two rows a compute unit in
+// flight) and its registers cost short rows (1531 rows 9.9 to 14). Reductions through shuffles, an LDS access a step, and four
+// times the waves a row took 72.
 
 #include "row_codes.h"
 #include "wave_ops.h"
@@ -167,10 +168,14 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_kernel(
 }
 
 // Rows first, first + step, ..., a workgroup or a wave each, the next one's loads under way while one is turned; a lane's share of
-// d_weight stays in registers until the end, where each workgroup's, or its waves', go to partial[part]. 256 parts of rows
-// of 7168 47.0 us for 4096 of them, 512 parts 50.7, 1024 58 (their sums are written and read again); shorter rows leave room for
-// more on a compute unit: 1531 rows of 2064 14.2, 13.8 and 16.3, 4096 of 1024 21.8, 14.7 and 14.0. Several rows a workgroup,
-// their shares of d_weight joined through LDS, took 52.7, 18.4 and 21.2.
+// d_weight stays in registers until the end, where each workgroup's, or its waves', go to partial[part]. What bounds it is a
+// row's chain with little beside it: two reductions in 64 bits, a barrier, then the divisions and the root, before the first
+// store. Two vectors a lane need 162 registers, three waves a SIMD, so that of rows of 7168, seven waves each, one is on a compute
+// unit at a time, and more parts than units are rounds and not rows at once: 256 parts 50.7 us for 4096 rows with the second kernel,
+// 512 parts 53.2, 1024 56.6 (their sums are written and read again); 2048 rows of 16384 55.6, 62.7 and 79.4. Shorter rows leave room
+// for more: 4096 of 2048 23.7, 21.0 and 21.0, 4096 of 1024 21.7, 15.0 and 14.4, 1531 of 2064 13.7, 13.7 and 16.3. More rows' loads
+// under way gain nothing: two, three and four ahead 51.3, 50.0 and 50.0 where one took 50.5. Several rows a workgroup, their
+// shares of d_weight joined through LDS, took 52.7, and 1531 rows 18.4.
 template <int VPL, int WTYPE>
 __global__ __launch_bounds__(kMaxThreads) void rms_norm_backward_kernel(
     const uint8_t *__restrict__ dy, int64_t dy_stride, const uint8_t *__restrict__ sum, int64_t sum_stride,

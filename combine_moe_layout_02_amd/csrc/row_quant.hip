@@ -1,11 +1,11 @@
 // Rows to 8 bits with one fp32 scale a row, and back, for gfx950 (see moe_row_quantize in moe.h; row_codes.h has the
 // arithmetic, the quantised dispatch's).
 //
-// Both directions are streams that HBM bounds: 32768 rows of 7168 to INT8 and back, 705 MB each, take 121 and 115 us (5.8 and
-// 6.1 TB/s; a large copy reaches 6.7). The quotients' corrections count on the way there: with a clamp, the zeros' signs and a
-// conversion for each the same rows took 131, with an uncorrected product and a division where it comes near a border
-// 157 (bf16 rows often hold half of their largest value, halfway between two codes), and a row over 448 lanes of two
-// neighbouring vectors, reduced by shuffles, 143. On the way back one vector a lane takes 122.
+// Both directions are streams that HBM bounds: 32768 rows of 7168 to INT8 and back, 705 MB each, take 118 and 115 us (6.0 and
+// 6.1 TB/s; a large copy reaches 6.7). The quotients' corrections count on the way there. In loops of calls, 121 as it is, the
+// same rows took 131 with a clamp, the zeros' signs and a conversion for each, 157 with an uncorrected product and a division
+// where it comes near a border (bf16 rows often hold half of their largest value, halfway between two codes), and 143 as a
+// row over 448 lanes of two neighbouring vectors, reduced by shuffles. On the way back one vector a lane takes 122.
 
 #include "row_codes.h"
 #include "wave_ops.h"
