@@ -6,7 +6,7 @@
 // exact there, nothing overflows, and the codes, which lie next to borders, do not depend on the order of the additions.
 //
 // HBM bounds the forward, and a row's chain the gradient. Call after call, 4096 rows of 7168, us and TB/s of what is read and
-// written: to bf16 41.8 and 5.6, to INT8 38.5 and 5.3, the gradients 50.7 and 4.6 with d_weight's second kernel (4.7 of them). Two
+// written: to bf16 41.8 and 5.6, to INT8 38.5 and 5.3, the gradients 50.6 and 4.6 with d_weight's second kernel (4.7 of them). Two
 // vectors a lane: to INT8 such rows take 38.5, with four 37.4, with eight 39.0, with one 55.6; 1531 rows of 2064 7.6, 8.5, 8.9 and
 // 9.9; 4096 rows of 1024 7.5, 8.8, 12.1 and 9.2; 128 rows of 7168 5.1, 5.2, 5.8 and 6.2. Stores with nt (bf16, INT8) 41.8 and 38.5,
 // with sc0 sc1 nt 42.0 and 38.8, written back 43.6 and 39.9. A workgroup that takes row after row with the weights in its
@@ -170,12 +170,14 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_kernel(
 // Rows first, first + step, ..., a workgroup or a wave each, the next one's loads under way while one is turned; a lane's share of
 // d_weight stays in registers until the end, where each workgroup's, or its waves', go to partial[part]. What bounds it is a
 // row's chain with little beside it: two reductions in 64 bits, a barrier, then the divisions and the root, before the first
-// store. Two vectors a lane need 162 registers, three waves a SIMD, so that of rows of 7168, seven waves each, one is on a compute
-// unit at a time, and more parts than units are rounds and not rows at once: 256 parts 50.7 us for 4096 rows with the second kernel,
-// 512 parts 53.2, 1024 56.6 (their sums are written and read again); 2048 rows of 16384 55.6, 62.7 and 79.4. Shorter rows leave room
-// for more: 4096 of 2048 23.7, 21.0 and 21.0, 4096 of 1024 21.7, 15.0 and 14.4, 1531 of 2064 13.7, 13.7 and 16.3. More rows' loads
-// under way gain nothing: two, three and four ahead 51.3, 50.0 and 50.0 where one took 50.5. Several rows a workgroup, their
-// shares of d_weight joined through LDS, took 52.7, and 1531 rows 18.4.
+// store. Two vectors a lane need 162 registers (130 with fp32 weights), three waves a SIMD, so that of rows of 7168, seven waves
+// each, one is on a compute unit at a time, and more parts than units are rounds and not rows at once: with bf16 weights 256
+// parts 50.6 us for 4096 rows with the second kernel, 512 parts 53.8, 1024 57.0 (their sums are written and read again); 2048
+// rows of 16384 55.4, 63.0 and 78.5. Shorter rows leave room for more: 4096 of 2048 23.9, 21.0 and 20.9, 4096 of 1024 21.8, 15.1
+// and 14.4, 1531 of 2064 13.9, 13.7 and 16.3. fp32 weights take 49.8, 56.4, 21.5, 14.8 and 14.4 in the kept forms, 50.8, 55.7,
+// 21.0, 14.5 and 13.7 where their products with dy were rounded before the mean. More rows' loads under way gain nothing: two,
+// three and four ahead 51.3, 50.0 and 50.0 where one took 50.5. Several rows a workgroup, their shares of d_weight joined through
+// LDS, took 52.7, and 1531 rows 18.4.
 template <int VPL, int WTYPE>
 __global__ __launch_bounds__(kMaxThreads) void rms_norm_backward_kernel(
     const uint8_t *__restrict__ dy, int64_t dy_stride, const uint8_t *__restrict__ sum, int64_t sum_stride,
@@ -223,7 +225,9 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_backward_kernel(
             for (int e = 0; e < 8; ++e) {
                 const double hv = value(h[i], e);
                 square = fma(hv, hv, square);
-                dot = fma(hv, (double)(value(g[i], e) * wt[i].value(e)), dot);
+                // exact, as the sum may cancel: bf16 by bf16 in 32 bits, by fp32 in 64
+                const double gw = WTYPE == MOE_BF16 ? (double)(value(g[i], e) * wt[i].value(e)) : (double)value(g[i], e) * (double)wt[i].value(e);
+                dot = fma(hv, gw, dot);
             }
         square = wave::sum(square);
         dot = wave::sum(dot);

@@ -1,5 +1,6 @@
 """GPU tests of the 8-bit layer's calls at their edges: the balance loss over several GPUs' tokens and at the ends of its
-factors' ranges, more rows than one call of the library converts, products of many rows, and the links of a whole step.
+factors' ranges, more rows than one call of the library converts, products of many rows, gradients of the norm
+whose mean cancels, and the links of a whole step.
 
 Tolerances, derived before the first run, are written at each test; u = 2^-24 is fp32's rounding. The oracle is numpy in
 64 bits.
@@ -159,6 +160,41 @@ def test_parts_of_rows_refuse_what_one_call_refuses(moe):  # noqa: F811
         moe.moe_row_quantize(rows, INT8, out=(codes, over))
     with pytest.raises(ValueError):
         moe.moe_row_quantize(rows, 0, out=(codes, scales))
+
+
+# ---------------------------------------------------------------- the norm's gradient
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("S,H", [(40, 64), (40, 528), (20, 1040)])
+def test_norm_gradient_where_the_mean_cancels(moe, S, H, kind):  # noqa: F811
+    """Rows whose mean of g * n all but cancels, by the last weight, so that it is what the products' roundings would make of it; where
+    dy is 0 the gradient is that mean alone. The reference is in 80 bits. Tolerance: as for other rows, 2^-21 of the terms and
+    half a step; the mean's own sum, of H products in 64 bits, is off by (H + 8) 2^-53 of their magnitudes."""
+    rng = np.random.default_rng(H)
+    h, dy = (oracle.bf16_bits_to_f32(bits(rng.standard_normal((S, H)))).astype(np.longdouble) for _ in range(2))
+    w = (1 + 0.3 * rng.standard_normal(H)).astype(np.float32)
+    if kind == "bf16":
+        w = oracle.bf16_bits_to_f32(bits(w))
+    dy[:, ::5] = 0
+    h[:, -1] = dy[:, -1] = 1
+    h[1:], dy[1:] = h[0], dy[0]  # one weight for all rows: they differ in sign and in powers of two
+    h *= np.exp2(rng.integers(-9, 9, (S, 1)))
+    dy *= np.exp2(rng.integers(-9, 9, (S, 1))) * rng.choice([-1, 1], (S, 1))
+    near_zero = -(h[0, :-1] * dy[0, :-1] * w[:-1].astype(np.longdouble)).sum() / (h[0, -1] * dy[0, -1])
+    w[-1] = oracle.bf16_bits_to_f32(bits([near_zero]))[0] if kind == "bf16" else np.float32(near_zero)
+    g = dy * w.astype(np.longdouble)
+    r = 1 / np.sqrt((h * h).mean(axis=1, keepdims=True) + float(np.float32(1e-5)))
+    n = h * r
+    m = (g * n).mean(axis=1, keepdims=True)
+    want = r * (g - n * m)
+    off = (H + 8) * 2.0**-53 * np.abs(g * n).mean(axis=1, keepdims=True)
+    tol = 2.0**-21 * (np.abs(r * g) + np.abs(r * n * m)) + np.abs(r * n) * off + 2.0**-8 * np.abs(want) + 2.0**-133
+    weight = bf16_dev(bits(w)) if kind == "bf16" else to_dev(w)
+    as_rows = lambda v: bf16_dev(bits(v.astype(np.float64)))  # noqa: E731
+    assert np.array_equal(values(as_rows(h)), h.astype(np.float32)) and np.array_equal(values(as_rows(dy)), dy.astype(np.float32))
+    dx, _ = moe.moe_rms_norm_backward(as_rows(dy), as_rows(h), weight, 1e-5)
+    near(values(dx), want.astype(np.float64), tol.astype(np.float64), "dx")
 
 
 # ---------------------------------------------------------------- the product
