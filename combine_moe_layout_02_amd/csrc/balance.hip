@@ -3,7 +3,7 @@
 // A wave takes a token: lane l holds experts l, l + 64, ... of it, so that its scores are two reductions over the wave's
 // lanes, and their sums over tokens stay in its registers. The exponentials and the reductions' chains bound it, and launches.
 // Calls one after another in a graph, us with a softmax and with sigmoids: 8192 tokens of 256 experts (8.4 MB) 9.9 and 10.2 forward
-// (5.8 in the parts, 4.9 in the joining kernel) and 5.8 and 6.2 back, 65536 of them 21.0 and 23.5, 24.6 and 25.9, 128 tokens of 16
+// (5.8 in the parts, 5.0 in the joining kernel) and 5.8 and 6.2 back, 65536 of them 21.0 and 23.5, 24.6 and 25.9, 128 tokens of 16
 // experts (one part) 5.8 and 6.6, 2.3 and 2.3. 8192 tokens in parts of 64 take 10.6 and 11.2, of 128 13.5 and 14.7. With the library's
 // expf 65536 tokens take 22.7 and 30.7, 25.3 and 30.6; with loads and stores that a test keeps in the row, not the buffer's
 // end, 2.8 more. The gradient with 1024 workgroups takes 5.7 and 6.2 (65536 tokens 25.4 and 28.4), with 512 5.9 and 6.7 (29.5 and 34.5),
