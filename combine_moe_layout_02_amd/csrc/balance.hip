@@ -3,7 +3,7 @@
 // A wave takes a token: lane l holds experts l, l + 64, ... of it, so that its scores are two reductions over the wave's
 // lanes, and their sums over tokens stay in its registers. The exponentials and the reductions' chains bound it, and launches.
 // Calls one after another in a graph, us with a softmax and with sigmoids: 8192 tokens of 256 experts (8.4 MB) 9.9 and 10.2 forward
-// (5.8 in the parts, 5.0 in the joining kernel) and 5.8 and 6.2 back, 65536 of them 21.0 and 23.5, 24.6 and 25.9, 128 tokens of 16
+// (5.8 in the parts, 5.0 in the joining kernel) and 5.9 and 6.2 back, 65536 of them 20.6 and 23.1, 24.9 and 26.0, 128 tokens of 16
 // experts (one part) 5.8 and 6.6, 2.3 and 2.3. 8192 tokens in parts of 64 take 10.6 and 11.2, of 128 13.5 and 14.7. With the library's
 // expf 65536 tokens take 22.7 and 30.7, 25.3 and 30.6; with loads and stores that a test keeps in the row, not the buffer's
 // end, 2.8 more. The gradient with 1024 workgroups takes 5.7 and 6.2 (65536 tokens 25.4 and 28.4), with 512 5.9 and 6.7 (29.5 and 34.5),
@@ -242,8 +242,10 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(
     sum = wave::sum(sum);
     const int mean = (int)(sum / E);
     const double all = sum * (double)*tokens;
-    // in 64 bits until it meets the counts: coef, d_loss and 1 / (N T) may each be near an end of fp32's range
-    const double each = all > 0.0 ? (double)coef * E / all * *d_loss : 0.0;
+    // coef, d_loss and 1 / (N T) may each be near an end of fp32's range: the factor is taken in 64 bits, its mantissa meets the
+    // counts and its exponent the result
+    int power;
+    const double each = __builtin_frexp(all > 0.0 ? (double)coef * E / all * *d_loss : 0.0, &power);
     float g[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) g[i] = (float)(each * (n[i] - mean));
@@ -265,7 +267,7 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(
         for (int i = 0; i < N; ++i) {
             float d = s[i] * (g[i] - dot);
             if (SCORE == MOE_SCORE_SIGMOID) d *= turn[i];
-            d = lives ? d : 0.0f;
+            d = lives ? __builtin_ldexpf(d, power) : 0.0f;
             const int at = (lane + 64 * i) * (int)sizeof(T);
             if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(d), dst, at, 0, 0);
             else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)d), dst, at, 0, 0);

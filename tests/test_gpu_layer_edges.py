@@ -88,6 +88,31 @@ def test_gradient_of_factors_at_both_ends_of_the_range(moe, score, coef, d_loss)
     near(values(got), want, 84 * U * factor * E / (counts.sum() * tokens) * 2 * largest + 15 * 2.0**-150, "d_logits")
 
 
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("coef,d_loss", [(3e38, 3.0), (1e-33, -1e-3), (1e20, 1e20)])
+def test_gradient_of_small_scores_and_large_factors(moe, score, coef, d_loss):  # noqa: F811
+    """The factor alone, times a count, is outside fp32's range, and the gradients of an expert that all but has the token and of
+    the others, with scores of 1e-9, are not. Tolerance: (64 + far) u c s (|g| + sum s |g|), far 20, and 15 halves of the smallest
+    subnormal, as above."""
+    S, E, K = 5, 12, 2
+    rng = np.random.default_rng(26)
+    l = (rng.standard_normal((S, E)) - 20).astype(np.float32)
+    l[:, 3] = 1
+    idx = np.full((S, K), -1, dtype=np.int32)
+    idx[2] = 3, 7
+    unit = oracle.balance(l, idx, 1.0, score)[3]
+    factor = float(np.float32(coef)) * float(np.float32(d_loss))
+    u = l[2].astype(np.float64) if score == 0 else -np.logaddexp(0, -l[2].astype(np.float64))
+    s = np.exp(u - u.max()) / np.exp(u - u.max()).sum()
+    g = np.isin(np.arange(E), (3, 7))
+    tol = np.zeros((S, E))
+    tol[2] = 88 * U * abs(factor) * E / 2 * s * (g + (s * g).sum()) + 15 * 2.0**-150
+    dev, table = to_dev(l), to_dev(idx)
+    b = moe.moe_balance_loss(dev, table, coef, score)
+    got = values(moe.moe_balance_loss_backward(torch.tensor([d_loss], device=DEV), dev, table, b.num_tokens_per_expert, b.num_tokens, coef, score))
+    near(got, unit * factor, tol, "d_logits")
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 @pytest.mark.parametrize("score", [0, 1])
 def test_scores_far_below_the_largest(moe, score, kind):  # noqa: F811
